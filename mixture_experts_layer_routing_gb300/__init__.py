@@ -354,3 +354,6 @@ class MoeLayer:
 
     def status(self, stream=None) -> int:
         return moe_get_status(self.h, stream)
+
+
+from .ops import MoeOps, default_ops  # noqa: E402,F401  (the operators of include/moe_ops.h)

@@ -33,7 +33,7 @@ def _nvcc() -> str:
 def _stamp(sources) -> str:
     h = hashlib.sha256(" ".join(FLAGS).encode())
     for p in sorted(sources + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) +
-                    [os.path.join(ROOT, "include", "moe.h")]):
+                    glob.glob(os.path.join(ROOT, "include", "*.h"))):
         h.update(p.encode())
         with open(p, "rb") as fh:
             h.update(fh.read())

@@ -1,0 +1,725 @@
+// Products of e4m3 operands with a scale for each 128 values (include/moe_ops.h) on tcgen05.mma kind::f8f6f4.
+//
+// The scales change every 128 values of the reduction, so a product of 128 is finished in TMEM by itself (four
+// MMAs of K = 32 into one of several partial accumulators), read back, and added with its scales to sums that live
+// in registers: c += (sa sb) * partial, in fp32. Two kernels:
+//
+// wide: many rows. CTA tile 128 rows x 256 columns, one CTA a SM, persistent. TMEM holds two partials of 256
+//   columns (all 512), so that the tensor core works on one while eight epilogue warps (128 sums a thread) take
+//   in the other. Per K block the MMAs take 512 cycles and the 32,768 FMAs of the sums 256.
+// narrow: few rows a segment (decoding). The operands change places: 128 weight rows are the MMA's M and 16 to 64
+//   token rows its N, so that the MMA's M is filled by weights and a weight byte is read once. The reduction is
+//   split over the CTAs of a cluster where tiles alone would not fill the GPU; the parts are added through
+//   distributed shared memory in rank order. Bound by the weights' bytes.
+//
+// Operands come by TMA (128-byte swizzle); gathered rows (row_index) by TMA gathers of four rows. Every wait is
+// bounded: a role that gives up sets the abort flag and the others leave their loops too.
+#include "common.cuh"
+#include "launch.cuh"
+#include "segs.cuh"
+#include "tc_ptx.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int BK = 128;                      // bytes (values) of the reduction a stage holds: one scale block
+
+// kind::f8f6f4: e4m3 A and B (both K-major), fp32 accumulator, M x N.
+__host__ __device__ constexpr uint32_t idesc_f8(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+// Four rows r0 .. r3 of the map's matrix, 128 bytes from column c each (rows past the matrix: zeros).
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* tm, int c, int r0, int r1, int r2, int r3,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
+      "%5, %6}], [%7];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(c), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void named_sync(int id, int nthreads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
+template <int COLS> __device__ __forceinline__ void tmem_alloc(uint32_t slot) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "n"(COLS) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+template <int COLS> __device__ __forceinline__ void tmem_free(uint32_t base) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "n"(COLS));
+}
+// Bounded wait that does not look at the abort flag: for what a role itself has in flight when it leaves.
+__device__ __forceinline__ void wait_own(uint32_t bar, uint32_t parity, int* status) {
+  const uint64_t t0 = global_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (global_ns() - t0 > kWaitLimitNs) {
+      set_error(status, MOE_ERR_TIMEOUT);
+      break;
+    }
+  }
+}
+
+// As mbar_wait, without a call: a call inside the epilogue's loop would have to save its 128 sums.
+__device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+#pragma unroll 1
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 63) == 0) {
+      if (*abort_flag) return false;
+      if (global_ns() - t0 > kWaitLimitNs) {
+        set_error(status, MOE_ERR_TIMEOUT);
+        *abort_flag = 1;
+        return false;
+      }
+    }
+  }
+}
+
+struct GemmParams {
+  const float* sa;        // scales of the rows: [a_rows][nkb], or (wgrad) [K blocks][M]
+  const float* sb;        // of the columns: [G][ceil(N / 128)][nkb], or (wgrad) [K blocks][N]
+  const int* row_index;
+  const int* off;
+  int G;
+  int rows;               // rows of all segments (off's bound): M, or (wgrad) tokens
+  int a_rows;             // rows of a (gathered from)
+  int M;                  // wgrad: rows of c
+  int N;
+  int nkb;                // K blocks (wgrad: from the segment)
+  void* c;
+  int* status;
+};
+
+// Row of a that row m of c reads; past the segment, or with an index out of range, the first row behind a (zeros).
+__device__ __forceinline__ int gather_row(const GemmParams& p, int m, int row_end) {
+  const int r = m < row_end ? p.row_index[m] : p.a_rows;
+  return (unsigned)r < (unsigned)p.a_rows ? r : p.a_rows;
+}
+
+template <typename O> struct Out;
+template <> struct Out<bf16> {
+  static __device__ __forceinline__ void store(bf16* p, const float* f) { *reinterpret_cast<uint4*>(p) = pack8(f); }
+};
+template <> struct Out<float> {
+  static __device__ __forceinline__ void store(float* p, const float* f) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+  }
+};
+
+// ------------------------------------------------------------------- wide
+constexpr int WM = 128, WN = 256, kWStages = 4, kWBufs = 2;
+constexpr int kWStageBytes = (WM + WN) * BK;
+constexpr int kWEpi = 8;                               // epilogue warps: four lane quadrants x two column halves
+constexpr int kWThreads = (4 + kWEpi) * 32;            // producer, MMA, two idle warps, epilogue
+struct WideSmem {
+  SegSmem seg;
+  alignas(16) float sb[kWBufs][WN];                    // wgrad: column scales of the K block in each partial
+  uint64_t full[kWStages], empty[kWStages], pfull[kWBufs], pempty[kWBufs];
+  uint32_t tmem;
+  int abort;
+};
+constexpr int kWSmem = kWStages * kWStageBytes + 1024 + (int)sizeof(WideSmem);
+// Registers: 384 threads are launched with 168 each; the epilogue's 256 take 216, the other 128 give down to 72.
+constexpr int kWRegs = 168, kWRegsEpi = 216, kWRegsRest = 72;
+static_assert(256 * kWRegsEpi + 128 * kWRegsRest <= kWThreads * kWRegs, "register split");
+
+struct WTile {
+  int g, row0, row_end, n0, kb0, nkb;
+};
+
+// Unit L of the schedule: row tiles in groups of 16, all column tiles of a group before the next (L2 reuse).
+template <bool WGRAD>
+__device__ __forceinline__ WTile wide_tile(const GemmParams& p, const SegSmem& s, int L) {
+  const int nt = (p.N + WN - 1) / WN;
+  WTile t;
+  int m, mt, local;
+  if (WGRAD) {
+    mt = (p.M + WM - 1) / WM;
+    t.g = L / (mt * nt);
+    local = L - t.g * mt * nt;
+  } else {
+    int lo = 0, hi = p.G;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s.tile[mid] * nt <= L) lo = mid; else hi = mid;
+    }
+    t.g = lo;
+    mt = s.tile[lo + 1] - s.tile[lo];
+    local = L - s.tile[lo] * nt;
+  }
+  const int grp = local / (kRasterM * nt), gm = min(kRasterM, mt - grp * kRasterM);
+  const int within = local - grp * kRasterM * nt;
+  m = grp * kRasterM + within % gm;
+  t.n0 = within / gm * WN;
+  if (WGRAD) {
+    t.row0 = m * WM;
+    t.row_end = p.M;
+    t.kb0 = s.tile[t.g];
+    t.nkb = s.tile[t.g + 1] - t.kb0;
+  } else {
+    t.row0 = s.off[t.g] + m * WM;
+    t.row_end = s.off[t.g + 1];
+    t.kb0 = 0;
+    t.nkb = p.nkb;
+  }
+  return t;
+}
+template <bool WGRAD>
+__device__ __forceinline__ int wide_units(const GemmParams& p, const SegSmem& s) {
+  const int nt = (p.N + WN - 1) / WN;
+  return (WGRAD ? p.G * ((p.M + WM - 1) / WM) : s.tile[p.G]) * nt;
+}
+
+template <bool WGRAD, bool GATHER, typename O>
+__global__ void __launch_bounds__(kWThreads, 1)
+    fp8_wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, GemmParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  WideSmem& sm = *reinterpret_cast<WideSmem*>(ring + kWStages * kWStageBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = &sm.abort;
+  const uint32_t full0 = smem_u32(sm.full), empty0 = smem_u32(sm.empty), pfull0 = smem_u32(sm.pfull),
+                 pempty0 = smem_u32(sm.pempty);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kWStages; ++i) {
+      mbar_init(full0 + 8 * i, 1);
+      mbar_init(empty0 + 8 * i, 1);
+    }
+    for (int i = 0; i < kWBufs; ++i) {
+      mbar_init(pfull0 + 8 * i, 1);
+      mbar_init(pempty0 + 8 * i, kWEpi);
+    }
+    sm.abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  griddep_wait();     // before the allocation: no CTA holds TMEM while the predecessor may still want some
+  griddep_launch();
+  if (warp == 1) tmem_alloc<512>(smem_u32(&sm.tmem));
+  load_segments(sm.seg, p.off, p.G, p.rows, WGRAD ? BK : WM, p.status);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+  const int units = wide_units<WGRAD>(p, sm.seg);
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWRegsRest));
+    if (warp == 0) {
+      // ---------------------------------------------------------------- producer
+      int it = 0;
+      bool ok = true;
+      for (int L = blockIdx.x; L < units && ok; L += gridDim.x) {
+        const WTile t = wide_tile<WGRAD>(p, sm.seg, L);
+        int r[4];
+        if (GATHER) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int m = t.row0 + 4 * lane + i;
+            r[i] = gather_row(p, m, t.row_end);
+          }
+        }
+        const int brow = WGRAD ? t.n0 : t.g * p.N + t.n0;
+        for (int kb = 0; kb < t.nkb; ++kb, ++it) {
+          const int s = it % kWStages;
+          ok = __all_sync(0xffffffffu,
+                          mbar_wait(empty0 + 8 * s, ((it / kWStages) & 1) ^ 1, abort_flag, p.status));
+          if (!ok) break;
+          const uint32_t a = smem_u32(ring + s * kWStageBytes), fb = full0 + 8 * s;
+          const int k = (t.kb0 + kb) * BK;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(fb, kWStageBytes);
+            tma_load_2d(a + WM * BK, &tmB, k, brow, fb);
+            if (!GATHER) tma_load_2d(a, &tmA, k, t.row0, fb);
+          }
+          if (GATHER) {
+            __syncwarp();
+            tma_gather4(a + lane * 4 * BK, &tmA, k, r[0], r[1], r[2], r[3], fb);
+          }
+        }
+      }
+      if (!ok && lane == 0) {   // the copies still in flight
+        for (int i = max(0, it - kWStages); i < it; ++i)
+          wait_own(full0 + 8 * (i % kWStages), (i / kWStages) & 1, p.status);
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      // --------------------------------------------------------------------- MMA (lane 0 issues)
+      int it = 0, last = -1;
+      bool ok = true;
+      for (int L = blockIdx.x; L < units && ok && lane == 0; L += gridDim.x) {
+        const WTile t = wide_tile<WGRAD>(p, sm.seg, L);
+        for (int kb = 0; kb < t.nkb; ++kb, ++it) {
+          const int s = it % kWStages, b = it % kWBufs;
+          ok = mbar_wait(pempty0 + 8 * b, ((it / kWBufs) & 1) ^ 1, abort_flag, p.status) &&
+               mbar_wait(full0 + 8 * s, (it / kWStages) & 1, abort_flag, p.status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t a = smem_u32(ring + s * kWStageBytes);
+          const uint64_t da = desc_kmajor(a), db = desc_kmajor(a + WM * BK);
+#pragma unroll
+          for (int k = 0; k < BK / 32; ++k)
+            mma_f8(tmem + b * WN, da + 2 * k, db + 2 * k, idesc_f8(WM, WN), k > 0 ? 1u : 0u);
+          mma_commit(empty0 + 8 * s);
+          mma_commit(pfull0 + 8 * b);
+          last = it;
+        }
+      }
+      // the last MMAs' arrival: nothing of this CTA's is in flight when its TMEM is given back
+      if (last >= 0) wait_own(pfull0 + 8 * (last % kWBufs), (last / kWBufs) & 1, p.status);
+      __syncwarp();
+    }
+  } else {
+    // -------------------------------------------------------------------- epilogue
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWRegsEpi));
+    const int quad = warp & 3, half = (warp - 4) >> 2;
+    const int r = quad * 32 + lane, ht = threadIdx.x & 127;   // row of the tile; thread of this column half
+    const uint32_t tq = tmem + half * 128 + ((uint32_t)(quad * 32) << 16);
+    const int nb = (p.N + 127) / 128;
+    const bool vec = p.N % 8 == 0;
+    int it = 0;
+    bool ok = true;   // after a failed wait: no more waiting or storing, every named barrier still reached
+    for (int L = blockIdx.x; L < units; L += gridDim.x) {
+      const WTile t = wide_tile<WGRAD>(p, sm.seg, L);
+      const int row = t.row0 + r, col0 = t.n0 + half * 128;
+      const bool valid = row < t.row_end;
+      const float *sa = p.sa, *sb = p.sb;
+      int sa_step = 1;
+      bool zero = false;   // a row index out of range reads zeros
+      if (WGRAD) {
+        sa += (size_t)t.kb0 * p.M + (valid ? row : 0);
+        sa_step = p.M;
+        sb += (size_t)t.kb0 * p.N + min(col0 + ht, p.N - 1);
+      } else {
+        int ar = valid ? (GATHER ? p.row_index[row] : row) : 0;
+        if ((unsigned)ar >= (unsigned)p.a_rows) {
+          set_error(p.status, MOE_ERR_DEVICE_INDEX);
+          ar = 0;
+          zero = true;
+        }
+        sa += (size_t)ar * p.nkb;
+        sb += ((size_t)t.g * nb + min(col0 / 128, nb - 1)) * p.nkb;
+      }
+      float acc[128];
+#pragma unroll
+      for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+      float na = t.nkb > 0 ? __ldg(sa) : 0.f, nsb = t.nkb > 0 ? __ldg(sb) : 0.f;
+      for (int kb = 0; kb < t.nkb; ++kb, ++it) {
+        const int b = it % kWBufs;
+        float s = zero ? 0.f : na;
+        if (WGRAD) {
+          sm.sb[b][half * 128 + ht] = nsb;
+          named_sync(1 + half, 128);
+        } else {
+          s *= nsb;
+        }
+        if (kb + 1 < t.nkb) {
+          na = __ldg(sa + (size_t)(kb + 1) * sa_step);
+          nsb = __ldg(sb + (size_t)(kb + 1) * (WGRAD ? p.N : 1));
+        }
+        ok = __all_sync(0xffffffffu, ok && wait_inline(pfull0 + 8 * b, (it / kWBufs) & 1, abort_flag, p.status));
+        if (ok) {
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < 128; c += 16) {
+            uint32_t u[16];
+            tmem_ld16(tq + b * WN + c, u);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+              float4 v = make_float4(s, s, s, s);
+              if (WGRAD) {
+                v = *reinterpret_cast<const float4*>(&sm.sb[b][half * 128 + c + i]);
+                v = make_float4(s * v.x, s * v.y, s * v.z, s * v.w);
+              }
+              acc[c + i] = fmaf(__uint_as_float(u[i]), v.x, acc[c + i]);
+              acc[c + i + 1] = fmaf(__uint_as_float(u[i + 1]), v.y, acc[c + i + 1]);
+              acc[c + i + 2] = fmaf(__uint_as_float(u[i + 2]), v.z, acc[c + i + 2]);
+              acc[c + i + 3] = fmaf(__uint_as_float(u[i + 3]), v.w, acc[c + i + 3]);
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(pempty0 + 8 * b);
+        }
+      }
+      if (!ok || !valid) continue;
+      O* out = (O*)p.c + (WGRAD ? (size_t)t.g * p.M : (size_t)0) * p.N + (size_t)row * p.N + col0;
+#pragma unroll
+      for (int i = 0; i < 128; i += 8) {
+        if (vec) {
+          if (col0 + i < p.N) Out<O>::store(out + i, acc + i);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (col0 + i + j < p.N) out[i + j] = from_f<O>(acc[i + j]);
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_free<512>(tmem);
+}
+
+// ----------------------------------------------------------------- narrow
+constexpr int kNThreads = 256, kNBufs = 4;
+template <int NT> constexpr int n_stages() { return NT == 16 ? 5 : 4; }
+template <int NT> constexpr int n_stage_bytes() { return (128 + NT) * BK; }
+template <int NT>
+struct alignas(16) NarrowSmem {
+  SegSmem seg;
+  uint64_t full[8], empty[8], pfull[kNBufs], pempty[kNBufs];
+  uint32_t tmem;
+  int abort;
+};
+template <int NT> constexpr int n_smem(int nkb) {
+  return n_stages<NT>() * n_stage_bytes<NT>() + 1024 + (int)sizeof(NarrowSmem<NT>) + nkb * NT * 4;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// Cluster of S CTAs per unit (token tile, 128 weight rows); rank r takes K blocks r nkb / S .. (r + 1) nkb / S.
+template <int NT, bool GATHER, typename O>
+__global__ void __launch_bounds__(kNThreads)
+    fp8_narrow_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, GemmParams p,
+                      int S) {
+  constexpr int ST = n_stages<NT>(), SB = n_stage_bytes<NT>(), COLS = kNBufs * NT;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  NarrowSmem<NT>& sm = *reinterpret_cast<NarrowSmem<NT>*>(ring + ST * SB);
+  float* sas = reinterpret_cast<float*>(ring + ST * SB + sizeof(NarrowSmem<NT>));   // [K block][token]
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int* abort_flag = &sm.abort;
+  const uint32_t full0 = smem_u32(sm.full), empty0 = smem_u32(sm.empty), pfull0 = smem_u32(sm.pfull),
+                 pempty0 = smem_u32(sm.pempty);
+  if (tid == 0) {
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(full0 + 8 * i, 1);
+      mbar_init(empty0 + 8 * i, 1);
+    }
+    for (int i = 0; i < kNBufs; ++i) {
+      mbar_init(pfull0 + 8 * i, 1);
+      mbar_init(pempty0 + 8 * i, 4);
+    }
+    sm.abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  griddep_wait();     // before the allocation, as in the wide kernel
+  griddep_launch();
+  if (warp == 1) tmem_alloc<COLS>(smem_u32(&sm.tmem));
+  load_segments(sm.seg, p.off, p.G, p.rows, NT, p.status);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+  const int rank = blockIdx.x % S, unit = blockIdx.x / S;
+  const int nt = (p.N + 127) / 128, tt = unit / nt, n0 = (unit - tt * nt) * 128;
+  const bool live = tt < sm.seg.tile[p.G];   // the same in the whole cluster
+  int g = 0, row0 = 0, row_end = 0, kb0 = 0, nkb = 0;
+  if (live) {
+    g = segment_of(sm.seg, p.G, tt);
+    row0 = sm.seg.off[g] + (tt - sm.seg.tile[g]) * NT;
+    row_end = min(sm.seg.off[g + 1], row0 + NT);
+    kb0 = (int)((long long)rank * p.nkb / S);
+    nkb = (int)((long long)(rank + 1) * p.nkb / S) - kb0;
+  }
+  // the token tile's scales for this CTA's K blocks (zero past the segment)
+  for (int i = tid; i < NT * nkb; i += kNThreads) {
+    const int j = i / nkb, kb = i - j * nkb;
+    float s = 0.f;
+    if (row0 + j < row_end) {
+      const int ar = GATHER ? p.row_index[row0 + j] : row0 + j;
+      if ((unsigned)ar < (unsigned)p.a_rows) {
+        s = p.sa[(size_t)ar * p.nkb + kb0 + kb];
+      } else {
+        set_error(p.status, MOE_ERR_DEVICE_INDEX);
+      }
+    }
+    sas[kb * NT + j] = s;
+  }
+  __syncthreads();
+
+  float acc[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) acc[j] = 0.f;
+  bool ok = true;
+  if (warp == 0) {
+    // ---------------------------------------------------------------- producer
+    int r[4];
+    if (GATHER) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int m = row0 + 4 * lane + i;
+        r[i] = gather_row(p, m, row_end);
+      }
+    }
+    const int brow = g * p.N + n0;
+    int kb = 0;
+    for (; kb < nkb; ++kb) {
+      const int s = kb % ST;
+      ok = __all_sync(0xffffffffu, mbar_wait(empty0 + 8 * s, ((kb / ST) & 1) ^ 1, abort_flag, p.status));
+      if (!ok) break;
+      const uint32_t a = smem_u32(ring + s * SB), fb = full0 + 8 * s;
+      const int k = (kb0 + kb) * BK;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(fb, SB);
+        tma_load_2d(a, &tmB, k, brow, fb);
+        if (!GATHER) tma_load_2d(a + 128 * BK, &tmA, k, row0, fb);
+      }
+      if (GATHER) {
+        __syncwarp();
+        if (lane < NT / 4) tma_gather4(a + (128 + 4 * lane) * BK, &tmA, k, r[0], r[1], r[2], r[3], fb);
+      }
+    }
+    if (!ok && lane == 0) {
+      for (int i = max(0, kb - ST); i < kb; ++i) wait_own(full0 + 8 * (i % ST), (i / ST) & 1, p.status);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // --------------------------------------------------------------------- MMA
+    if (lane == 0) {
+      int last = -1;
+      for (int kb = 0; kb < nkb; ++kb) {
+        const int s = kb % ST, b = kb % kNBufs;
+        ok = mbar_wait(pempty0 + 8 * b, ((kb / kNBufs) & 1) ^ 1, abort_flag, p.status) &&
+             mbar_wait(full0 + 8 * s, (kb / ST) & 1, abort_flag, p.status);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t a = smem_u32(ring + s * SB);
+        const uint64_t da = desc_kmajor(a), db = desc_kmajor(a + 128 * BK);
+#pragma unroll
+        for (int k = 0; k < BK / 32; ++k)
+          mma_f8(tmem + b * NT, da + 2 * k, db + 2 * k, idesc_f8(128, NT), k > 0 ? 1u : 0u);
+        mma_commit(empty0 + 8 * s);
+        mma_commit(pfull0 + 8 * b);
+        last = kb;
+      }
+      if (last >= 0) wait_own(pfull0 + 8 * (last % kNBufs), (last / kNBufs) & 1, p.status);
+    }
+    __syncwarp();
+  } else if (warp < 6) {
+    // -------------------------------------------------------------------- epilogue: thread = weight row
+    const int quad = warp & 3;
+    const uint32_t tq = tmem + ((uint32_t)(quad * 32) << 16);
+    const float* sb = p.sb + ((size_t)g * nt + n0 / 128) * p.nkb + kb0;
+    float nsb = nkb > 0 ? __ldg(sb) : 0.f;
+    for (int kb = 0; kb < nkb; ++kb) {
+      const int b = kb % kNBufs;
+      const float s = nsb;
+      if (kb + 1 < nkb) nsb = __ldg(sb + kb + 1);
+      ok = __all_sync(0xffffffffu, mbar_wait(pfull0 + 8 * b, (kb / kNBufs) & 1, abort_flag, p.status));
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < NT; c += 16) {
+        uint32_t u[16];
+        tmem_ld16(tq + b * NT + c, u);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+          const float4 v = *reinterpret_cast<const float4*>(sas + kb * NT + c + i);
+          acc[c + i] = fmaf(__uint_as_float(u[i]), s * v.x, acc[c + i]);
+          acc[c + i + 1] = fmaf(__uint_as_float(u[i + 1]), s * v.y, acc[c + i + 1]);
+          acc[c + i + 2] = fmaf(__uint_as_float(u[i + 2]), s * v.z, acc[c + i + 2]);
+          acc[c + i + 3] = fmaf(__uint_as_float(u[i + 3]), s * v.w, acc[c + i + 3]);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pempty0 + 8 * b);
+    }
+    const int wr = quad * 32 + lane, col = n0 + wr;
+    if (S == 1) {
+      if (ok && col < p.N) {
+        O* out = (O*)p.c + (size_t)row0 * p.N + col;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          if (row0 + j < row_end) out[(size_t)j * p.N] = from_f<O>(acc[j]);
+      }
+    } else {   // every MMA and copy of this CTA has ended: the ring is free
+      float* red = reinterpret_cast<float*>(ring);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) red[j * 128 + wr] = acc[j];
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_free<COLS>(tmem);
+  if (S > 1) {
+    // add the parts in rank order; the CTAs share out the tokens
+    cluster_sync();
+    if (*abort_flag == 0) {
+      const uint32_t red = smem_u32(ring);
+      const int wr = tid & 127, col = n0 + wr;
+      for (int j = rank * 2 + (tid >> 7); row0 + j < row_end; j += 2 * S) {
+        float v = 0.f;
+        for (int q = 0; q < S; ++q) v += ld_cluster(mapa_shared(red + (j * 128 + wr) * 4, q));
+        if (col < p.N) ((O*)p.c)[(size_t)(row0 + j) * p.N + col] = from_f<O>(v);
+      }
+    }
+    cluster_sync();   // no CTA leaves while another reads its part
+  }
+}
+
+// -------------------------------------------------------------------- host
+constexpr int kMaxSmem = 227 * 1024, kNarrowMaxKb = 128;
+static_assert(kWSmem <= kMaxSmem && n_smem<64>(kNarrowMaxKb) <= kMaxSmem && n_smem<16>(kNarrowMaxKb) <= kMaxSmem &&
+                  n_smem<32>(kNarrowMaxKb) <= kMaxSmem,
+              "shared memory per CTA");
+
+template <typename K>
+cudaError_t set_smem(K kern) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+}
+template <bool WGRAD, bool GATHER, typename O>
+cudaError_t init_wide() {
+  auto kern = fp8_wide_kernel<WGRAD, GATHER, O>;
+  cudaFuncAttributes at;
+  MOE_TRY(cudaFuncGetAttributes(&at, kern));
+  if (at.numRegs != kWRegs) return cudaErrorInvalidKernelImage;   // what the epilogue's registers are taken out of
+  return set_smem(kern);
+}
+template <int NT>
+cudaError_t init_narrow() {
+  MOE_TRY(set_smem(fp8_narrow_kernel<NT, false, bf16>));
+  MOE_TRY(set_smem(fp8_narrow_kernel<NT, false, float>));
+  MOE_TRY(set_smem(fp8_narrow_kernel<NT, true, bf16>));
+  return set_smem(fp8_narrow_kernel<NT, true, float>);
+}
+
+template <bool WGRAD, bool GATHER, typename O>
+cudaError_t launch_wide(const moe_ops_s* o, const CUtensorMap& a, const CUtensorMap& b, const GemmParams& p,
+                        long long units, cudaStream_t s) {
+  auto kern = fp8_wide_kernel<WGRAD, GATHER, O>;
+  const int grid = (int)(units < o->sms ? units : o->sms);
+  return launch_pdl(kern, dim3(grid), dim3(kWThreads), kWSmem, s, a, b, p);
+}
+
+template <int NT, bool GATHER, typename O>
+cudaError_t launch_narrow(const CUtensorMap& a, const CUtensorMap& b, const GemmParams& p, long long units, int S,
+                          cudaStream_t s) {
+  auto kern = fp8_narrow_kernel<NT, GATHER, O>;
+  const int smem = n_smem<NT>(ceil_div(p.nkb, S));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(units * S));
+  cfg.blockDim = dim3(kNThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = S;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, a, b, p, S);
+}
+
+template <int NT>
+cudaError_t pick_narrow(const CUtensorMap& a, const CUtensorMap& b, const GemmParams& p, long long units, int S,
+                        bool fp32, cudaStream_t s) {
+  if (p.row_index)
+    return fp32 ? launch_narrow<NT, true, float>(a, b, p, units, S, s) : launch_narrow<NT, true, bf16>(a, b, p, units, S, s);
+  return fp32 ? launch_narrow<NT, false, float>(a, b, p, units, S, s) : launch_narrow<NT, false, bf16>(a, b, p, units, S, s);
+}
+
+}  // namespace
+
+cudaError_t fp8_init() {
+  MOE_TRY((init_wide<false, false, bf16>()));
+  MOE_TRY((init_wide<false, false, float>()));
+  MOE_TRY((init_wide<false, true, bf16>()));
+  MOE_TRY((init_wide<false, true, float>()));
+  MOE_TRY((init_wide<true, false, bf16>()));
+  MOE_TRY((init_wide<true, false, float>()));
+  MOE_TRY(init_narrow<16>());
+  MOE_TRY(init_narrow<32>());
+  return init_narrow<64>();
+}
+
+cudaError_t fp8_matmul(const moe_ops_s* o, const void* a, const float* sa, int a_rows, const int* row_index, int M,
+                       const void* b, const float* sb, const int* off, int G, int N, int K, void* c, int out_fp32,
+                       cudaStream_t s, long long* n) {
+  GemmParams p = {};
+  p.sa = sa;
+  p.sb = sb;
+  p.row_index = row_index;
+  p.off = off;
+  p.G = G;
+  p.rows = M;
+  p.a_rows = a_rows;
+  p.N = N;
+  p.nkb = ceil_div(K, BK);
+  p.c = c;
+  p.status = o->status;
+  CUtensorMap ta, tb;
+  const int avg = ceil_div(M, G);
+  *n += 1;
+  if (avg <= 64 && p.nkb <= kNarrowMaxKb) {
+    const int NT = avg <= 12 ? 16 : avg <= 24 ? 32 : 64;
+    if (!make_tmap(&ta, a, K, a_rows, BK, row_index ? 1 : NT, 1) ||
+        !make_tmap(&tb, b, K, (uint64_t)G * N, BK, 128, 1))
+      return cudaErrorInvalidValue;
+    const int nt = ceil_div(N, 128);
+    // token tiles: at most one that is not full for each segment that holds a row
+    const long long most = (G < M ? G : M), units = (M / NT + most < M ? M / NT + most : M) * (long long)nt;
+    int S = 1;
+    while (S < 8 && 2 * S <= p.nkb && units * S * 2 <= 2 * o->sms) S *= 2;
+    return NT == 16 ? pick_narrow<16>(ta, tb, p, units, S, out_fp32, s)
+           : NT == 32 ? pick_narrow<32>(ta, tb, p, units, S, out_fp32, s)
+                      : pick_narrow<64>(ta, tb, p, units, S, out_fp32, s);
+  }
+  if (!make_tmap(&ta, a, K, a_rows, BK, row_index ? 1 : WM, 1) || !make_tmap(&tb, b, K, (uint64_t)G * N, BK, WN, 1))
+    return cudaErrorInvalidValue;
+  const long long units = ((long long)ceil_div(M, WM) + (G > 1 ? G : 0)) * ceil_div(N, WN);
+  if (row_index)
+    return out_fp32 ? launch_wide<false, true, float>(o, ta, tb, p, units, s)
+                    : launch_wide<false, true, bf16>(o, ta, tb, p, units, s);
+  return out_fp32 ? launch_wide<false, false, float>(o, ta, tb, p, units, s)
+                  : launch_wide<false, false, bf16>(o, ta, tb, p, units, s);
+}
+
+cudaError_t fp8_wgrad(const moe_ops_s* o, const void* dct, const float* sdct, const void* xt, const float* sxt, int T,
+                      const int* off, int G, int N, int K, void* c, int out_fp32, cudaStream_t s, long long* n) {
+  GemmParams p = {};
+  p.sa = sdct;
+  p.sb = sxt;
+  p.off = off;
+  p.G = G;
+  p.rows = T;
+  p.M = N;
+  p.N = K;
+  p.c = c;
+  p.status = o->status;
+  const int Tp = quant_cols_rows(T, G);
+  CUtensorMap ta, tb;
+  if (!make_tmap(&ta, dct, Tp, N, BK, WM, 1) || !make_tmap(&tb, xt, Tp, K, BK, WN, 1)) return cudaErrorInvalidValue;
+  const long long units = (long long)G * ceil_div(N, WM) * ceil_div(K, WN);
+  *n += 1;
+  return out_fp32 ? launch_wide<true, false, float>(o, ta, tb, p, units, s)
+                  : launch_wide<true, false, bf16>(o, ta, tb, p, units, s);
+}
+
+}  // namespace moe

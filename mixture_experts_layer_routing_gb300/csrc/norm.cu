@@ -1,0 +1,218 @@
+// RMS norm with the residual's addition and an e4m3 output, and its backward pass (include/moe_ops.h).
+//
+// Forward, one row a CTA: the row is read once, h = x + residual stays in registers (8 values a thread and step)
+// through the one reduction (sum of squares), and every output leaves from there. A 128-value scale block is 16
+// neighbouring lanes, so its maximum takes four shuffles. Bound by HBM at many rows, by latency at few.
+//
+// Backward: a CTA walks rows with stride gridDim, keeps its part of dw in registers and makes one
+// reduction a row (mean(u n); rstd comes from the forward pass). The parts are summed in a fixed order by a
+// second kernel, so dw does not depend on timing.
+#include "fp8_quant.cuh"
+#include "launch.cuh"
+#include "ops.h"
+
+namespace moe {
+namespace {
+
+constexpr int kNormCtas = 304;   // two CTAs a SM walk the rows of the backward pass
+
+// Sum over the block; red holds one word a warp and is free for reuse after the next barrier.
+__device__ __forceinline__ float block_sum(float v, float* red) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  v = warp_sum(v);
+  if (lane == 0) red[w] = v;
+  __syncthreads();
+  return warp_sum(lane < nw ? red[lane] : 0.f);
+}
+
+template <typename T, int VPT>
+__global__ void __launch_bounds__(1024) norm_fwd_kernel(const T* x, long long ld_x, const T* res,
+                                                        long long ld_res, const T* __restrict__ w, int d, float eps, T* h, T* y,
+                                                        uint8_t* q, float* scale, float* rstd) {
+  __shared__ float red[32];
+  griddep_wait();
+  griddep_launch();
+  const long long t = blockIdx.x;
+  const int nv = d >> 3;
+  float v[VPT][8];
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = i * blockDim.x + threadIdx.x;
+    if (c < nv) load8(x + t * ld_x + 8 * c, v[i]);
+  }
+  if (res) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = i * blockDim.x + threadIdx.x;
+      if (c < nv) {
+        float r[8];
+        load8(res + t * ld_res + 8 * c, r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] = to_f(from_f<T>(v[i][j] + r[j]));   // the sum as it is stored
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = i * blockDim.x + threadIdx.x;
+    if (c < nv) {
+      if (h) store8(h + t * d + 8 * c, v[i]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss += v[i][j] * v[i][j];
+    }
+  }
+  const float r = __frsqrt_rn(block_sum(ss, red) / (float)d + eps);
+  if (rstd && threadIdx.x == 0) rstd[t] = r;
+  if (!y && !q) return;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = i * blockDim.x + threadIdx.x;
+    if (c < nv) {
+      float g[8];
+      load8(w + 8 * c, g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * r * g[j];
+      if (y) store8(y + t * d + 8 * c, v[i]);
+    }
+    if (q) {   // every lane takes part in the shuffles
+      const float m = half_warp_max(c < nv ? amax8(v[i]) : 0.f);
+      if (c < nv) {
+        *reinterpret_cast<uint2*>(q + t * d + 8 * c) = codes8(v[i], m);
+        if ((c & 15) == 0) scale[t * ((d + kScaleBlock - 1) / kScaleBlock) + (c >> 4)] = block_scale(m);
+      }
+    }
+  }
+}
+
+template <typename T, int VPT>
+__global__ void __launch_bounds__(1024) norm_bwd_kernel(const T* dy, const T* dh, const T* __restrict__ h,
+                                                        const T* __restrict__ w, const float* __restrict__ rstd,
+                                                        int rows, int d, T* dx, float* part) {
+  __shared__ float red[2][32];
+  griddep_wait();
+  griddep_launch();
+  const int nv = d >> 3;
+  float acc[VPT][8];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
+  const float inv_d = 1.0f / (float)d;
+  int flip = 0;
+  for (long long t = blockIdx.x; t < rows; t += gridDim.x, flip ^= 1) {
+    const float r = rstd[t];
+    float a[VPT][8], n[VPT][8], s = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = i * blockDim.x + threadIdx.x;
+      if (c < nv) {
+        load8(dy + t * d + 8 * c, a[i]);
+        load8(h + t * d + 8 * c, n[i]);
+        float g[8];
+        load8(w + 8 * c, g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          n[i][j] *= r;
+          acc[i][j] += a[i][j] * n[i][j];
+          a[i][j] *= g[j];
+          s += a[i][j] * n[i][j];
+        }
+      }
+    }
+    if (!dx) continue;
+    const float mean = block_sum(s, red[flip]) * inv_d;   // two buffers: one barrier a row
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = i * blockDim.x + threadIdx.x;
+      if (c < nv) {
+        float o[8];
+        if (dh) load8(dh + t * d + 8 * c, o);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = (dh ? o[j] : 0.f) + r * (a[i][j] - n[i][j] * mean);
+        store8(dx + t * d + 8 * c, o);
+      }
+    }
+  }
+  if (part) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = i * blockDim.x + threadIdx.x;
+      if (c < nv) store8(part + (long long)blockIdx.x * d + 8 * c, acc[i]);
+    }
+  }
+}
+
+// dw[c] = sum over the parts: a CTA takes 32 columns, its 8 rows of threads every eighth part.
+__global__ void __launch_bounds__(256) norm_dw_kernel(const float* __restrict__ part, int parts, int d, float* dw) {
+  __shared__ float red[8][33];
+  griddep_wait();
+  griddep_launch();
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+  float s = 0.f;
+  if (c < d)
+#pragma unroll 8
+    for (int p = w; p < parts; p += 8) s += part[(long long)p * d + c];
+  red[w][lane] = s;
+  __syncthreads();
+  if (w == 0 && c < d) {
+    float t = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t += red[i][lane];
+    dw[c] = t;
+  }
+}
+
+template <typename T, int VPT>
+cudaError_t fwd(const void* x, long long ld_x, const void* res, long long ld_res, const void* w, int rows, int d,
+                float eps, void* h, void* y, void* q, float* scale, float* rstd, cudaStream_t s) {
+  const int threads = ceil_div(ceil_div(d / 8, VPT), 32) * 32;
+  return launch_pdl(norm_fwd_kernel<T, VPT>, dim3(rows), dim3(threads), 0, s, (const T*)x, ld_x, (const T*)res, ld_res,
+                    (const T*)w, d, eps, (T*)h, (T*)y, (uint8_t*)q, scale, rstd);
+}
+template <typename T, int VPT>
+cudaError_t bwd(const void* dy, const void* dh, const void* h, const void* w, const float* rstd, int rows, int d,
+                void* dx, float* part, int parts, cudaStream_t s) {
+  const int threads = ceil_div(ceil_div(d / 8, VPT), 32) * 32;
+  return launch_pdl(norm_bwd_kernel<T, VPT>, dim3(parts), dim3(threads), 0, s, (const T*)dy, (const T*)dh, (const T*)h,
+                    (const T*)w, rstd, rows, d, (T*)dx, part);
+}
+
+// Steps of 8 values a thread. Few rows: as many threads as there are (one step up to d = 8192).
+inline int steps(int d, bool wide) {
+  const int nv = d / 8;
+  if (wide) return nv <= 1024 ? 1 : 2;
+  return nv <= 256 ? 1 : nv <= 512 ? 2 : 4;
+}
+
+}  // namespace
+
+int norm_partials(int T) { return T < kNormCtas ? T : kNormCtas; }
+
+cudaError_t norm_forward(const moe_ops_s* o, int dtype, const void* x, long long ld_x, const void* res,
+                         long long ld_res, const void* w, int T, int d, float eps, void* h, void* y, void* q,
+                         float* scale, float* rstd, cudaStream_t s, long long* n) {
+  const int vpt = steps(d, T < 2 * o->sms);
+  const bool b = dtype == MOE_BF16;
+  const auto call = vpt == 1 ? (b ? fwd<bf16, 1> : fwd<float, 1>) : vpt == 2 ? (b ? fwd<bf16, 2> : fwd<float, 2>)
+                                                                            : (b ? fwd<bf16, 4> : fwd<float, 4>);
+  *n += 1;
+  return call(x, ld_x, res, ld_res, w, T, d, eps, h, y, q, scale, rstd, s);
+}
+
+cudaError_t norm_backward(const moe_ops_s* o, int dtype, const void* dy, const void* dh, const void* h,
+                          const void* w, const float* rstd, int T, int d, void* dx, float* dw, float* part,
+                          cudaStream_t s, long long* n) {
+  const int vpt = steps(d, true), parts = norm_partials(T);
+  if (T > 0) {
+    *n += 1;
+    const bool b = dtype == MOE_BF16;
+    const auto call = vpt == 1 ? (b ? bwd<bf16, 1> : bwd<float, 1>) : (b ? bwd<bf16, 2> : bwd<float, 2>);
+    MOE_TRY(call(dy, dh, h, w, rstd, T, d, dx, dw ? part : nullptr, parts, s));
+  }
+  if (!dw) return cudaSuccess;
+  *n += 1;
+  return launch_pdl(norm_dw_kernel, dim3(ceil_div(d, 32)), dim3(256), 0, s, (const float*)part, parts, d, dw);
+}
+
+}  // namespace moe

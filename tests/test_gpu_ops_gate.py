@@ -1,0 +1,210 @@
+"""Routing operators against the 64-bit restatement (GPU): selections and dispatch equal, gates and gradients near.
+
+Gates: a score is within 14 units in the last place of the largest score (see the kernel), a renormalised gate
+within three times that: 2^-18 of the sum's share. Gradients likewise, relative to the magnitudes that cancel.
+"""
+import numpy as np
+import pytest
+import torch
+
+import __graft_entry__
+from oracle import ops_oracle as oo
+
+pytestmark = pytest.mark.gpu
+NEAR = 2.0 ** -18
+
+
+@pytest.fixture(scope="module")
+def ops():
+    __graft_entry__.build()
+    import mixture_experts_layer_routing_gb300 as moe
+    return moe.default_ops()
+
+
+def check(ops, logits, bias, k, router="sigmoid", renorm=True, scale=1.0, n_groups=1, topk_groups=1):
+    T, E = logits.shape
+    kw = dict(router=router, renorm=renorm, n_groups=n_groups, topk_groups=topk_groups)
+    out = ops.gate(logits.cuda(), k, bias=None if bias is None else bias.cuda(), route_scale=scale, **kw)
+    idx, gate = oo.gate(logits.double().numpy(), None if bias is None else bias.double().numpy(), k, scale=scale, **kw)
+    assert ops.status() == 0
+    got = {n: t.cpu().numpy() for n, t in out.items()}
+    assert np.array_equal(got["idx"], idx)
+    for n, want in zip(("cnt", "off", "perm", "inv"), oo.dispatch(idx, E)):
+        assert np.array_equal(got[n], want), n
+    fine = np.isfinite(gate)
+    assert np.array_equal(np.isnan(got["gate"]), np.isnan(gate))
+    # softmax scores: relative to the row's largest
+    top = oo.scores(logits.double().numpy(), router).max(1, keepdims=True) * scale if not renorm else gate
+    assert np.all(np.abs(got["gate"] - gate)[fine] <= NEAR * np.maximum(np.abs(gate), np.broadcast_to(top, gate.shape))[fine])
+    return out
+
+
+CASES = [
+    # T, E, k, router, renorm, groups, kept, bias
+    (1, 1, 1, "softmax", True, 1, 1, False), (1, 256, 8, "sigmoid", True, 8, 4, True),
+    (4, 256, 8, "sigmoid", True, 8, 4, True), (64, 64, 6, "softmax", True, 1, 1, False),
+    (65, 64, 6, "softmax", False, 1, 1, True), (129, 60, 4, "softmax", False, 1, 1, True),
+    (200, 96, 3, "sigmoid", False, 4, 1, True), (77, 160, 8, "softmax", True, 8, 3, True),
+    (1000, 128, 2, "sigmoid", True, 32, 7, True), (33, 32, 5, "sigmoid", True, 32, 9, True),
+    (500, 8, 2, "softmax", True, 2, 1, False), (300, 255, 7, "sigmoid", True, 5, 2, True),
+    (40, 17, 8, "sigmoid", True, 1, 1, True), (9, 200, 1, "softmax", True, 8, 8, True),
+]
+
+
+@pytest.mark.parametrize("T,E,k,router,renorm,groups,kept,bias", CASES)
+def test_forward(ops, T, E, k, router, renorm, groups, kept, bias):
+    g = torch.Generator().manual_seed(T * 7 + E)
+    check(ops, 1.5 * torch.randn(T, E, generator=g), 0.1 * torch.randn(E, generator=g) if bias else None, k, router,
+          renorm, 2.5, groups, kept)
+
+
+def test_many_chunks(ops):
+    """More than 64 tokens a chunk, the last one short (the selection is checked on a sample)."""
+    g = torch.Generator().manual_seed(3)
+    T, E, k = 20011, 48, 5
+    logits = torch.randn(T, E, generator=g)
+    out = ops.gate(logits.cuda(), k, router="softmax")
+    idx = out["idx"].cpu().numpy()
+    assert np.array_equal(idx[::97], oo.gate(logits.double().numpy()[::97], None, k, "softmax", True, 1.0)[0])
+    for n, want in zip(("cnt", "off", "perm", "inv"), oo.dispatch(idx, E)):
+        assert np.array_equal(out[n].cpu().numpy(), want), n
+
+
+@pytest.mark.parametrize("router", ["softmax", "sigmoid"])
+def test_equal_and_nearly_equal_keys(ops, router):
+    """Ties go to the lower index; keys closer than 32 bits can tell are decided as in 64."""
+    g = torch.Generator().manual_seed(4)
+    base = torch.randn(300, 4, generator=g).repeat(1, 16)                   # each value 16 times
+    near = base + torch.randint(-2, 3, base.shape, generator=g) * 1e-7      # or a few last places apart
+    bias = torch.randint(-3, 4, (64,), generator=g) * 2.0 ** -24
+    check(ops, base, None, 6, router)
+    check(ops, near, None, 6, router)
+    check(ops, near, bias, 8, router, n_groups=8, topk_groups=3)
+    check(ops, torch.zeros(5, 64), None, 4, router, n_groups=4, topk_groups=2)
+    check(ops, 30 + near, bias, 6, router)                                   # saturated sigmoids
+
+
+@pytest.mark.parametrize("router", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups,kept", [(1, 1), (4, 2)])
+def test_masked_experts(ops, router, groups, kept):
+    """-inf takes an expert out; a row without any selects the lowest indexes with gates of 0; the lowest finite
+    value is a number like others."""
+    g = torch.Generator().manual_seed(5)
+    l = torch.randn(64, 32, generator=g)
+    l[torch.rand(64, 32, generator=g) < 0.5] = -float("inf")
+    l[3], l[4, 1:], l[5, :-1] = -float("inf"), -float("inf"), -float("inf")
+    l[6] = torch.finfo(torch.float32).min
+    l[7, ::2] = torch.finfo(torch.float32).min
+    bias = 0.2 * torch.randn(32, generator=g)
+    for b in (None, bias):
+        out = check(ops, l, b, 4, router, n_groups=groups, topk_groups=kept)
+        assert torch.equal(out["gate"][3].cpu(), torch.zeros(4))
+        assert torch.isfinite(out["gate"]).all()
+
+
+def test_nan_logits_come_last(ops):
+    g = torch.Generator().manual_seed(6)
+    l = torch.randn(16, 40, generator=g)
+    l[2, 7], l[3, :], l[4, 5] = float("nan"), float("nan"), float("inf")
+    out = check(ops, l, None, 3, "sigmoid")
+    assert torch.isnan(out["gate"][3]).all() and 7 not in out["idx"][2].tolist()
+    out = ops.gate(l.cuda(), 3, router="softmax")       # a NaN makes every score of its row NaN
+    assert torch.isnan(out["gate"][2:5]).all() and out["idx"][2].tolist() == [0, 1, 2]
+    assert torch.isfinite(out["gate"][5:]).all()
+
+
+def test_without_dispatch_and_without_tokens(ops):
+    g = torch.Generator().manual_seed(7)
+    l = torch.randn(100, 64, generator=g).cuda()
+    a, b = ops.gate(l, 6), ops.gate(l, 6, dispatch=False)
+    assert set(b) == {"idx", "gate"} and torch.equal(a["idx"], b["idx"]) and torch.equal(a["gate"], b["gate"])
+    out = ops.gate(l[:0], 6)
+    assert out["off"].tolist() == [0] * 65 and out["cnt"].tolist() == [0] * 64
+    assert ops.gate_backward(l[:0], out["idx"], out["gate"])["dlogits"].shape == (0, 64)
+
+
+@pytest.mark.parametrize("T,E,k,router,renorm", [(1, 256, 8, "sigmoid", True), (77, 64, 6, "softmax", True),
+                                                 (130, 60, 4, "softmax", False), (33, 100, 3, "sigmoid", False),
+                                                 (500, 8, 2, "softmax", True), (5, 1, 1, "softmax", False),
+                                                 (9, 17, 8, "sigmoid", True)])
+def test_backward(ops, T, E, k, router, renorm):
+    g = torch.Generator().manual_seed(T + E)
+    l, dg = 2 * torch.randn(T, E, generator=g), torch.randn(T, k, generator=g)
+    idx = torch.stack([torch.randperm(E, generator=g)[:k] for _ in range(T)]).int()
+    got = ops.gate_backward(l.cuda(), idx.cuda(), dg.cuda(), router=router, renorm=renorm, route_scale=2.5)["dlogits"]
+    want, size = oo.gate_backward(l.double().numpy(), idx.numpy().astype(np.int64), dg.double().numpy(), router,
+                                  renorm, 2.5)
+    err = np.abs(got.double().cpu().numpy() - want)
+    assert np.all(err <= NEAR * size), (err / np.maximum(size, 1e-30)).max()
+    if renorm or router == "sigmoid":
+        assert np.all(got.cpu().numpy()[want == 0] == 0)
+    assert ops.status() == 0
+
+
+def test_backward_of_masked_rows_and_bad_indexes(ops):
+    import mixture_experts_layer_routing_gb300 as moe
+    l = torch.randn(8, 16)
+    l[1] = -float("inf")
+    l[2, 3] = -float("inf")
+    idx = torch.tensor([[3, 5]] * 8, dtype=torch.int32)
+    for router in ("softmax", "sigmoid"):
+        for renorm in (True, False):
+            d = ops.gate_backward(l.cuda(), idx.cuda(), torch.ones(8, 2).cuda(), router=router, renorm=renorm)["dlogits"]
+            assert torch.isfinite(d).all() and not d[1].any()
+    assert ops.status() == 0
+    idx[4, 0], idx[5, 1] = 16, -1                      # out of range: recorded, their gradient left out
+    d = ops.gate_backward(l.cuda(), idx.cuda(), torch.ones(8, 2).cuda(), router="sigmoid", renorm=False)["dlogits"]
+    assert ops.status() == moe.MOE_ERR_DEVICE_INDEX and ops.status() == 0
+    assert d[4].nonzero().flatten().tolist() == [5] and d[5].nonzero().flatten().tolist() == [3]
+
+
+def test_gradient_against_differences(ops):
+    g = torch.Generator().manual_seed(8)
+    l, dg = torch.randn(3, 24, generator=g).double(), torch.randn(3, 4, generator=g)
+    out = ops.gate(l.float().cuda(), 4, router="sigmoid", n_groups=4, topk_groups=2, route_scale=2.5)
+    idx = out["idx"].cpu().numpy()
+    d = ops.gate_backward(l.float().cuda(), out["idx"], dg.cuda(), router="sigmoid", route_scale=2.5)["dlogits"].cpu()
+    def loss(z):
+        p = oo.scores(z, "sigmoid")[np.arange(3)[:, None], idx]
+        return (2.5 * p / p.sum(1, keepdims=True) * dg.double().numpy()).sum()
+    l = l.float().double().numpy()
+    for t in range(3):
+        for e in range(24):
+            a, b = l.copy(), l.copy()
+            a[t, e] += 1e-5
+            b[t, e] -= 1e-5
+            assert abs((loss(a) - loss(b)) / 2e-5 - d[t, e].item()) <= 1e-5
+
+
+def test_another_stream_graph_and_repeats(ops):
+    g = torch.Generator().manual_seed(9)
+    l, b = torch.randn(3000, 256, generator=g).cuda(), (0.1 * torch.randn(256, generator=g)).cuda()
+    kw = dict(bias=b, router="sigmoid", n_groups=8, topk_groups=4)
+    want = ops.gate(l, 8, **kw)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = ops.gate(l, 8, stream=s, **kw)
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cap = ops.gate(l, 8, **kw)
+    graph.replay()
+    torch.cuda.synchronize()
+    for n in want:
+        assert torch.equal(want[n], got[n]) and torch.equal(want[n], cap[n]), n
+
+
+def test_python_refusals(ops):
+    l = torch.randn(4, 64).cuda()
+    with pytest.raises(TypeError):
+        ops.gate(l.double(), 4)
+    with pytest.raises(ValueError):
+        ops.gate(l.t(), 4)
+    with pytest.raises(KeyError):
+        ops.gate(l, 4, router="relu")
+    with pytest.raises(RuntimeError):
+        ops.gate(l, 9)
+    with pytest.raises(RuntimeError):
+        ops.gate(l, 4, n_groups=7)
+    with pytest.raises(ValueError):
+        ops.gate_backward(l, torch.zeros(4, 2, dtype=torch.int32).cuda(), torch.zeros(4, 3).cuda())
