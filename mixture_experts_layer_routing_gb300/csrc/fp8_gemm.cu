@@ -110,6 +110,51 @@ __device__ __forceinline__ int gather_row(const GemmParams& p, int m, int row_en
   return (unsigned)r < (unsigned)p.a_rows ? r : p.a_rows;
 }
 
+// Pairs of fp32 values, for the two-wide multiply-add.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ void fma2(uint64_t& c, uint64_t a, uint64_t b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(a), "l"(b));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// Waits for this thread's TMEM loads; u is used after it.
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&u)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(u[0]), "+r"(u[1]), "+r"(u[2]), "+r"(u[3]), "+r"(u[4]), "+r"(u[5]), "+r"(u[6]), "+r"(u[7]),
+                 "+r"(u[8]), "+r"(u[9]), "+r"(u[10]), "+r"(u[11]), "+r"(u[12]), "+r"(u[13]), "+r"(u[14]), "+r"(u[15]),
+                 "+r"(u[16]), "+r"(u[17]), "+r"(u[18]), "+r"(u[19]), "+r"(u[20]), "+r"(u[21]), "+r"(u[22]),
+                 "+r"(u[23]), "+r"(u[24]), "+r"(u[25]), "+r"(u[26]), "+r"(u[27]), "+r"(u[28]), "+r"(u[29]),
+                 "+r"(u[30]), "+r"(u[31])
+               :
+               : "memory");
+}
+// acc += u s (columns' scales v too, where they differ) for 32 columns.
+template <bool COLS>
+__device__ __forceinline__ void add_scaled(uint64_t* acc, const uint32_t (&u)[32], float s, const float* v) {
+  const uint64_t s2 = pair(s, s);
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) {
+    uint64_t a = s2, b = s2;
+    if (COLS) {
+      const float4 f = *reinterpret_cast<const float4*>(v + i);
+      a = mul2(s2, pair(f.x, f.y));
+      b = mul2(s2, pair(f.z, f.w));
+    }
+    fma2(acc[i / 2], pair(__uint_as_float(u[i]), __uint_as_float(u[i + 1])), a);
+    fma2(acc[i / 2 + 1], pair(__uint_as_float(u[i + 2]), __uint_as_float(u[i + 3])), b);
+  }
+}
+
 template <typename O> struct Out;
 template <> struct Out<bf16> {
   static __device__ __forceinline__ void store(bf16* p, const float* f) { *reinterpret_cast<uint4*>(p) = pack8(f); }
@@ -314,9 +359,9 @@ __global__ void __launch_bounds__(kWThreads, 1)
         sa += (size_t)ar * p.nkb;
         sb += ((size_t)t.g * nb + min(col0 / 128, nb - 1)) * p.nkb;
       }
-      float acc[128];
+      uint64_t acc[64];    // pairs of neighbouring columns
 #pragma unroll
-      for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+      for (int i = 0; i < 64; ++i) acc[i] = 0;
       float na = t.nkb > 0 ? __ldg(sa) : 0.f, nsb = t.nkb > 0 ? __ldg(sb) : 0.f;
       for (int kb = 0; kb < t.nkb; ++kb, ++it) {
         const int b = it % kWBufs;
@@ -334,39 +379,37 @@ __global__ void __launch_bounds__(kWThreads, 1)
         ok = __all_sync(0xffffffffu, ok && wait_inline(pfull0 + 8 * b, (it / kWBufs) & 1, abort_flag, p.status));
         if (ok) {
           tc_fence_after();
+          // while 32 columns are added, the next 32 are on their way
+          uint32_t u[2][32];
+          tmem_ld32(tq + b * WN, u[0]);
+          tmem_ld_wait_for(u[0]);
 #pragma unroll
-          for (int c = 0; c < 128; c += 16) {
-            uint32_t u[16];
-            tmem_ld16(tq + b * WN + c, u);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-              float4 v = make_float4(s, s, s, s);
-              if (WGRAD) {
-                v = *reinterpret_cast<const float4*>(&sm.sb[b][half * 128 + c + i]);
-                v = make_float4(s * v.x, s * v.y, s * v.z, s * v.w);
-              }
-              acc[c + i] = fmaf(__uint_as_float(u[i]), v.x, acc[c + i]);
-              acc[c + i + 1] = fmaf(__uint_as_float(u[i + 1]), v.y, acc[c + i + 1]);
-              acc[c + i + 2] = fmaf(__uint_as_float(u[i + 2]), v.z, acc[c + i + 2]);
-              acc[c + i + 3] = fmaf(__uint_as_float(u[i + 3]), v.w, acc[c + i + 3]);
+          for (int c = 0; c < 4; ++c) {
+            if (c < 3) {
+              tmem_ld32(tq + b * WN + (c + 1) * 32, u[(c + 1) & 1]);
+            } else {   // the partial is read: the MMAs after the next may have it
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(pempty0 + 8 * b);
             }
+            add_scaled<WGRAD>(acc + c * 16, u[c & 1], s, &sm.sb[b][half * 128 + c * 32]);
+            if (c < 3) tmem_ld_wait_for(u[(c + 1) & 1]);
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(pempty0 + 8 * b);
         }
       }
       if (!ok || !valid) continue;
       O* out = (O*)p.c + (WGRAD ? (size_t)t.g * p.M : (size_t)0) * p.N + (size_t)row * p.N + col0;
 #pragma unroll
       for (int i = 0; i < 128; i += 8) {
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) unpair(acc[(i + j) / 2], f[j], f[j + 1]);
         if (vec) {
-          if (col0 + i < p.N) Out<O>::store(out + i, acc + i);
+          if (col0 + i < p.N) Out<O>::store(out + i, f);
         } else {
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            if (col0 + i + j < p.N) out[i + j] = from_f<O>(acc[i + j]);
+            if (col0 + i + j < p.N) out[i + j] = from_f<O>(f[j]);
         }
       }
     }

@@ -26,13 +26,44 @@ __device__ __forceinline__ float amax8(const float* v) {
 // between two codes is still there when it is rounded to even. A block of zeros (or with a NaN) keeps 0 * v.
 __device__ __forceinline__ float code_value(float v, float m) { return m > 0.f ? __fdiv_rn(v * kE4m3Max, m) : 0.f * v; }
 __device__ __forceinline__ float block_scale(float m) { return __fdiv_rn(m, kE4m3Max); }
-__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float m) {
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(code_value(a, m), code_value(b, m)), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(code_value(c, m), code_value(d, m)), __NV_SATFINITE, __NV_E4M3);
+__device__ __forceinline__ uint32_t pack_codes4(float a, float b, float c, float d) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
   return lo | (hi << 16);
 }
+// A block's divisor. Where neither 448 v nor a remainder can leave the range of normal numbers the quotient takes
+// three operations, with one reciprocal a block: q = a r, then q + (a - q m) r, which is the correctly rounded a / m
+// when r is the correctly rounded 1 / m (Markstein, IBM J. Res. Dev. 34, 1990). Elsewhere it is a division.
+struct Divisor {
+  float m, r;
+  bool plain;
+  __device__ __forceinline__ explicit Divisor(float amax) : m(amax) {
+    plain = m >= 0x1p-100f && m < 0x1p118f;
+    r = plain ? __frcp_rn(m) : 0.f;
+  }
+  __device__ __forceinline__ float code(float v) const {
+    const float a = v * kE4m3Max, q = a * r;
+    return fmaf(fmaf(-q, m, a), r, q);
+  }
+};
+// The codes of N (a multiple of 4) values of a block with the largest magnitude m.
+template <int N>
+__device__ __forceinline__ void codes(const float* v, float m, uint32_t* out) {
+  const Divisor d(m);
+  if (d.plain) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) out[i / 4] = pack_codes4(d.code(v[i]), d.code(v[i + 1]), d.code(v[i + 2]), d.code(v[i + 3]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+      out[i / 4] = pack_codes4(code_value(v[i], m), code_value(v[i + 1], m), code_value(v[i + 2], m),
+                               code_value(v[i + 3], m));
+  }
+}
 __device__ __forceinline__ uint2 codes8(const float* v, float m) {
-  return make_uint2(codes4(v[0], v[1], v[2], v[3], m), codes4(v[4], v[5], v[6], v[7], m));
+  uint32_t w[2];
+  codes<8>(v, m, w);
+  return make_uint2(w[0], w[1]);
 }
 // Largest of the 16 lanes that hold a block (8 values each).
 __device__ __forceinline__ float half_warp_max(float m) {
@@ -41,17 +72,43 @@ __device__ __forceinline__ float half_warp_max(float m) {
   return m;
 }
 
-// 8 consecutive values of either storage type as fp32, and back.
-__device__ __forceinline__ void load8(const bf16* p, float* f) { unpack8(*reinterpret_cast<const uint4*>(p), f); }
-__device__ __forceinline__ void load8(const float* p, float* f) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+// 8 consecutive values of either storage type, as they are stored and as fp32.
+template <typename T> struct Raw8;
+template <> struct Raw8<bf16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const bf16* p) { u = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void store(bf16* p) const { *reinterpret_cast<uint4*>(p) = u; }
+  __device__ __forceinline__ void get(float* f) const { unpack8(u, f); }
+  __device__ __forceinline__ void set(const float* f) { u = pack8(f); }
+};
+template <> struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void store(float* p) const {
+    reinterpret_cast<float4*>(p)[0] = a;
+    reinterpret_cast<float4*>(p)[1] = b;
+  }
+  __device__ __forceinline__ void get(float* f) const {
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  }
+  __device__ __forceinline__ void set(const float* f) {
+    a = make_float4(f[0], f[1], f[2], f[3]);
+    b = make_float4(f[4], f[5], f[6], f[7]);
+  }
+};
+template <typename T> __device__ __forceinline__ void load8(const T* p, float* f) {
+  Raw8<T> r;
+  r.load(p);
+  r.get(f);
 }
-__device__ __forceinline__ void store8(bf16* p, const float* f) { *reinterpret_cast<uint4*>(p) = pack8(f); }
-__device__ __forceinline__ void store8(float* p, const float* f) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+template <typename T> __device__ __forceinline__ void store8(T* p, const float* f) {
+  Raw8<T> r;
+  r.set(f);
+  r.store(p);
 }
 
 }  // namespace

@@ -1,13 +1,14 @@
 // Routing from router logits (include/moe_ops.h): scores, balance bias, groups, top-k, gates and the dispatch
 // (counts, offsets, stable permutation), and the gradient of the logits.
 //
-// One warp a token; lane i holds the PER consecutive experts i*PER .. (E <= 32 PER), so the lowest lane that holds
-// a maximum also holds the lowest expert, and equal keys need no index comparison. Every round of the top-k is one
-// redux over the lanes' own maxima. Keys are computed in 32 bits. Their error bound (tau) decides whether the
+// One warp a token; lane i holds the PER consecutive experts i*PER .. (E <= 32 PER). Keys are computed in 32 bits
+// with fast exponentials and kept as unsigned integers in the floats' order, so a round of the top-k is one redux
+// over the lanes and a masked maximum over a lane's own keys. A bound of their error (tau) decides whether the
 // outcome could differ from that of 64-bit keys: every gap that the selection rests on (between neighbours of the
 // sorted selection, to the first expert left out, between the worst group kept and the best left out) has to exceed
-// it; a token where one does not is selected again with 64-bit keys. Double precision is slow on this GPU (about
-// 1/64 of the fp32 rate), and only a fraction of a percent of tokens takes that path.
+// it. Where one does not, the experts that may belong to the selection get 64-bit keys, one a lane (double precision
+// runs at about 1/64 of the fp32 rate here, so not every expert's). The gates are computed from the selected logits
+// alone, in full 32-bit precision.
 //
 // The dispatch: tokens are cut into chunks, one CTA each, at most one chunk a SM. The selecting CTA counts its
 // chunk's experts. With one chunk it also writes offsets and permutation; otherwise a second kernel adds up the
@@ -27,7 +28,7 @@ constexpr int kGateThreads = 1024, kGateWarps = kGateThreads / 32;
 constexpr int kGateTokens = 64;      // tokens of a chunk, at least
 constexpr unsigned kFull = 0xffffffffu;
 
-// Order-preserving map of floats (no NaN) to unsigned, so that redux finds the maximum in one instruction.
+// Order-preserving map of floats (no NaN) to unsigned; 0 is below every float's.
 __device__ __forceinline__ unsigned order_of(float v) {
   const unsigned u = __float_as_uint(v);
   return u >> 31 ? ~u : u | 0x80000000u;
@@ -41,185 +42,289 @@ __device__ __forceinline__ double lanes_max(double v) {
   for (int o = 16; o; o >>= 1) v = fmax(v, __shfl_xor_sync(kFull, v, o));
   return v;
 }
-template <typename F> __device__ __forceinline__ F lowest();
-template <> __device__ __forceinline__ float lowest<float>() { return -FLT_MAX; }
-template <> __device__ __forceinline__ double lowest<double>() { return -DBL_MAX; }
-template <typename F> __device__ __forceinline__ F inf_of() { return (F)INFINITY; }
+__device__ __forceinline__ double lanes_sum(double v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
 
-// Lane j < k returns the j-th selected expert. `sure` turns false where a gap that the outcome rests on is not
-// above tau.
-template <int PER, typename F>
-__device__ __forceinline__ int select_experts(F (&key)[PER], const moe_gate_config& c, F tau, bool& sure) {
+// The 64-bit score and key of an expert. m, sum: the row's largest logit and sum of exponentials (softmax).
+__device__ __forceinline__ double exact_key(const moe_gate_config& c, float l, float b, float m, double sum) {
+  double p;
+  if (c.router == MOE_ROUTER_SOFTMAX) {
+    p = sum == 0.0 ? 0.0 : exp((double)l - (double)m) / sum;
+  } else {
+    p = 1.0 / (1.0 + exp(-(double)l));
+  }
+  const double k = p + (double)b;
+  return (l == -INFINITY || isnan(k)) ? -DBL_MAX : fmax(k, -DBL_MAX);
+}
+__device__ __forceinline__ double exact_sum(const moe_gate_config& c, const float* __restrict__ logits, float m) {
+  double s = 0.0;
+  if (c.router == MOE_ROUTER_SOFTMAX)
+    for (int e = threadIdx.x & 31; e < c.E; e += 32) s += exp((double)logits[e] - (double)m);
+  return lanes_sum(s);
+}
+
+// The whole selection with 64-bit keys: lane j < k returns its j-th expert. The lowest lane that holds a maximum also
+// holds the lowest such expert, so ties need no comparison of indexes.
+template <int PER>
+__device__ __noinline__ int select_exact(const float* __restrict__ logits, const float* __restrict__ bias, float m,
+                                         const moe_gate_config& c) {
   const int lane = threadIdx.x & 31, e0 = lane * PER;
+  const double sum = exact_sum(c, logits, m);
+  double key[PER];
+#pragma unroll
+  for (int q = 0; q < PER; ++q)
+    key[q] = e0 + q < c.E ? exact_key(c, logits[e0 + q], bias ? bias[e0 + q] : 0.f, m, sum) : -INFINITY;
   if (c.topk_groups < c.n_groups) {
     const int S = c.E / c.n_groups;
-    F score = -inf_of<F>();   // lane g: group g
+    double score = -INFINITY;   // lane g: group g
     for (int g = 0; g < c.n_groups; ++g) {
-      F a = -inf_of<F>(), b = -inf_of<F>();   // this lane's two best of group g
+      double a = -INFINITY, b = -INFINITY;   // this lane's two best of group g
 #pragma unroll
       for (int q = 0; q < PER; ++q) {
         if (e0 + q >= g * S && e0 + q < (g + 1) * S) {
-          if (key[q] > a) {
-            b = a;
-            a = key[q];
-          } else if (key[q] > b) {
-            b = key[q];
-          }
+          b = fmax(b, fmin(a, key[q]));
+          a = fmax(a, key[q]);
         }
       }
-      const F m = lanes_max(a);
-      F sum = m;
+      double s = lanes_max(a);
       if (S > 1) {
-        const int owner = __ffs(__ballot_sync(kFull, a == m)) - 1;
-        sum += lanes_max(lane == owner ? b : a);
+        const int owner = __ffs(__ballot_sync(kFull, a == s)) - 1;
+        s += lanes_max(lane == owner ? b : a);
       }
-      if (lane == g) score = sum;
+      if (lane == g) score = s;
     }
     int rank = 0;
     for (int g = 0; g < c.n_groups; ++g) {
-      const F other = __shfl_sync(kFull, score, g);
+      const double other = __shfl_sync(kFull, score, g);
       rank += other > score || (other == score && g < lane);
     }
-    const bool kept = lane < c.n_groups && rank < c.topk_groups;
-    const unsigned mask = __ballot_sync(kFull, kept);
-    const F worst = -lanes_max(kept ? -score : -inf_of<F>());
-    const F best = lanes_max(lane < c.n_groups && !kept ? score : -inf_of<F>());
-    if (!(worst - best > 3 * tau)) sure = false;   // a score is a sum of two keys
-    int g = e0 / S, r = e0 - g * S;
+    const unsigned kept = __ballot_sync(kFull, lane < c.n_groups && rank < c.topk_groups);
+#pragma unroll
+    for (int q = 0; q < PER; ++q)
+      if (e0 + q < c.E && !(kept >> ((e0 + q) / S) & 1u)) key[q] = -INFINITY;
+  }
+  int mine = 0;
+  for (int j = 0; j < c.k; ++j) {
+    double top = -INFINITY;
+    int at = 0;
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
-      if (!(mask >> g & 1u)) key[q] = -inf_of<F>();
-      if (++r == S) {
-        r = 0;
-        ++g;
-        if (g > 31) g = 31;   // (past the last expert: the key is -inf already)
+      if (key[q] > top) {
+        top = key[q];
+        at = q;
       }
     }
-  }
-  int mine = 0, at = 0;
-  F top = key[0];
-#pragma unroll
-  for (int q = 1; q < PER; ++q)
-    if (key[q] > top) {
-      top = key[q];
-      at = q;
-    }
-  F last = 0;
-  for (int j = 0; j <= c.k; ++j) {
-    const F m = lanes_max(top);
-    if (j > 0 && !(last - m > tau)) sure = false;
-    if (j == c.k) break;
-    last = m;
-    const int owner = __ffs(__ballot_sync(kFull, top == m)) - 1;
+    const double best = lanes_max(top);
+    const int owner = __ffs(__ballot_sync(kFull, top == best)) - 1;
     const int e = __shfl_sync(kFull, e0 + at, owner);
     if (lane == j) mine = e;
-    if (lane == owner) {
-      F best = -inf_of<F>();
-      int b = 0;
 #pragma unroll
-      for (int q = 0; q < PER; ++q) {
-        if (q == at) key[q] = -inf_of<F>();
-        if (key[q] > best) {
-          best = key[q];
-          b = q;
-        }
-      }
-      top = best;
-      at = b;
-    }
+    for (int q = 0; q < PER; ++q)
+      if (lane == owner && q == at) key[q] = -INFINITY;
   }
   return mine;
 }
 
-template <typename F>
-__device__ __forceinline__ F key_of(F p, F b, float l) {
-  const F k = p + b;
-  return (l == -INFINITY || isnan(k)) ? lowest<F>() : fmax(k, lowest<F>());
+// Rank of lane i's expert e among those of the lanes with `in`, by 64-bit keys (equal ones: the lower expert first).
+__device__ __noinline__ int rank_exact(const float* __restrict__ logits, const float* __restrict__ bias, float m,
+                                       const moe_gate_config& c, int e, bool in) {
+  const double sum = exact_sum(c, logits, m);
+  const double key = in ? exact_key(c, logits[e], bias ? bias[e] : 0.f, m, sum) : -INFINITY;
+  int rank = 0;
+  for (unsigned left = __ballot_sync(kFull, in); left; left &= left - 1) {
+    const int i = __ffs(left) - 1;
+    const double other = __shfl_sync(kFull, key, i);
+    const int oe = __shfl_sync(kFull, e, i);
+    rank += other > key || (other == key && oe < e);
+  }
+  return rank;
 }
 
-// The selection with 64-bit keys.
+// A lane's PER consecutive values of a row, in 16-byte loads where rows are made of them.
 template <int PER>
-__device__ __noinline__ int select_exact(const float* __restrict__ logits, const float* __restrict__ bias, float m,
-                                         const moe_gate_config& c) {
+__device__ __forceinline__ void load_lane(const float* __restrict__ row, int E, float fill, float (&v)[PER]) {
   const int e0 = (threadIdx.x & 31) * PER;
-  double key[PER], sum = 0.0;
+  if (PER >= 4 && (E & 3) == 0 && ((uintptr_t)row & 15) == 0) {
 #pragma unroll
-  for (int q = 0; q < PER; ++q) {
-    key[q] = 0.0;
-    if (e0 + q < c.E) {
-      const double l = (double)logits[e0 + q];
-      key[q] = c.router == MOE_ROUTER_SOFTMAX ? exp(l - (double)m) : 1.0 / (1.0 + exp(-l));
-      sum += key[q];
+    for (int q = 0; q + 3 < PER; q += 4) {
+      float4 u = make_float4(fill, fill, fill, fill);
+      if (e0 + q < E) u = *reinterpret_cast<const float4*>(row + e0 + q);
+      v[q] = u.x;
+      v[q + 1] = u.y;
+      v[q + 2] = u.z;
+      v[q + 3] = u.w;
     }
-  }
-  if (c.router == MOE_ROUTER_SOFTMAX) {
+  } else {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+    for (int q = 0; q < PER; ++q) v[q] = e0 + q < E ? row[e0 + q] : fill;
   }
-#pragma unroll
-  for (int q = 0; q < PER; ++q) {
-    if (e0 + q < c.E) {
-      const double p = c.router == MOE_ROUTER_SOFTMAX ? (sum == 0.0 ? 0.0 : key[q] / sum) : key[q];
-      key[q] = key_of<double>(p, bias ? (double)bias[e0 + q] : 0.0, logits[e0 + q]);
-    } else {
-      key[q] = -inf_of<double>();
-    }
-  }
-  bool sure = true;
-  return select_experts<PER, double>(key, c, 0.0, sure);
 }
 
-// One token: lane j < k returns expert j of the selection and its gate.
+// The groups that stay, as bits of this lane's own experts. sure turns false where their choice rests on a gap that
+// is not above the error of a score (a sum of two keys).
 template <int PER>
-__device__ __forceinline__ int gate_token(const float* __restrict__ logits, const float* __restrict__ bias,
-                                          const moe_gate_config& c, float& gate) {
-  const int lane = threadIdx.x & 31, e0 = lane * PER;
-  float l[PER], p[PER], key[PER];
-  float m = -INFINITY;
-#pragma unroll
-  for (int q = 0; q < PER; ++q) {
-    l[q] = e0 + q < c.E ? logits[e0 + q] : -INFINITY;
-    m = fmaxf(m, l[q]);
-  }
-  float pmax = 1.f;
-  if (c.router == MOE_ROUTER_SOFTMAX) {
-    m = lanes_max(m);
-    if (m == -INFINITY) m = 0.f;   // no expert left: every score 0
-    float sum = 0.f;
+__device__ __forceinline__ unsigned kept_experts(const unsigned (&key)[PER], const moe_gate_config& c, float tau,
+                                                 bool& sure) {
+  const int lane = threadIdx.x & 31, e0 = lane * PER, S = c.E / c.n_groups, L = S / PER;
+  // Groups that fill a power of two of lanes: all at once, every lane with its own group's score. Others: group by
+  // group, lane g with group g's.
+  const bool fills = L * PER == S && (L & (L - 1)) == 0;
+  float score = -INFINITY;
+  if (fills) {
+    unsigned a = 0u, b = 0u;
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
-      p[q] = expf(l[q] - m);
+      b = max(b, min(a, key[q]));
+      a = max(a, key[q]);
+    }
+    for (int o = 1; o < L; o <<= 1) {
+      const unsigned oa = __shfl_xor_sync(kFull, a, o), ob = __shfl_xor_sync(kFull, b, o);
+      b = max(min(a, oa), max(b, ob));
+      a = max(a, oa);
+    }
+    if (e0 < c.E) score = S > 1 ? of_order(a) + of_order(b) : of_order(a);
+  } else {
+    for (int g = 0; g < c.n_groups; ++g) {
+      unsigned a = 0u, b = 0u;
+#pragma unroll
+      for (int q = 0; q < PER; ++q) {
+        if (e0 + q >= g * S && e0 + q < (g + 1) * S) {
+          b = max(b, min(a, key[q]));
+          a = max(a, key[q]);
+        }
+      }
+      const unsigned best = __reduce_max_sync(kFull, a);
+      float s = of_order(best);
+      if (S > 1) {
+        const int owner = __ffs(__ballot_sync(kFull, a == best)) - 1;
+        s += of_order(__reduce_max_sync(kFull, lane == owner ? b : a));
+      }
+      if (lane == g) score = s;
+    }
+  }
+  const int step = fills ? L : 1, g = lane / step;
+  int rank = 0;
+  for (int i = 0; i < c.n_groups; ++i) {
+    const float other = __shfl_sync(kFull, score, i * step);
+    rank += other > score || (other == score && i < g);
+  }
+  const bool in = g < c.n_groups, kept = in && rank < c.topk_groups;
+  const float worst = -lanes_max(kept ? -score : -INFINITY), best = lanes_max(in && !kept ? score : -INFINITY);
+  if (!(worst - best > 3 * tau)) sure = false;
+  if (fills) return kept ? kFull : 0u;
+  const unsigned mask = __ballot_sync(kFull, kept);
+  unsigned bits = 0u;
+#pragma unroll
+  for (int q = 0; q < PER; ++q)
+    if (e0 + q < c.E && (mask >> ((e0 + q) / S) & 1u)) bits |= 1u << q;
+  return bits;
+}
+
+// One token: lane j < k returns expert j of the selection and its gate. scr: 64 words of the warp's own.
+template <int PER>
+__device__ __forceinline__ int gate_token(const float* __restrict__ logits, const float* __restrict__ bias,
+                                          const moe_gate_config& c, unsigned* scr, float& gate) {
+  const int lane = threadIdx.x & 31, e0 = lane * PER;
+  float l[PER], p[PER], b[PER];
+  load_lane<PER>(logits, c.E, -INFINITY, l);
+#pragma unroll
+  for (int q = 0; q < PER; ++q) b[q] = 0.f;
+  if (bias) load_lane<PER>(bias, c.E, 0.f, b);
+  float m = -INFINITY, sum = 1.f, pmax = 1.f;
+  if (c.router == MOE_ROUTER_SOFTMAX) {
+#pragma unroll
+    for (int q = 0; q < PER; ++q) m = fmaxf(m, l[q]);
+    m = lanes_max(m);
+    if (m == -INFINITY) m = 0.f;   // no expert left: every score 0
+    sum = 0.f;
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+      p[q] = __expf(l[q] - m);
       sum += p[q];
     }
     sum = warp_sum(sum);
+    pmax = sum == 0.f ? 0.f : __fdividef(1.f, sum);
 #pragma unroll
-    for (int q = 0; q < PER; ++q) p[q] = sum == 0.f ? 0.f : p[q] / sum;
-    pmax = sum == 0.f ? 0.f : 1.f / sum;
+    for (int q = 0; q < PER; ++q) p[q] *= pmax;
   } else {
 #pragma unroll
-    for (int q = 0; q < PER; ++q) p[q] = 1.f / (1.f + expf(-l[q]));
+    for (int q = 0; q < PER; ++q) p[q] = __fdividef(1.f, 1.f + __expf(-l[q]));
   }
+  unsigned key[PER];               // 0: no expert, or of a group that is left out
   float kmax = 0.f;
 #pragma unroll
   for (int q = 0; q < PER; ++q) {
-    const bool in = e0 + q < c.E;
-    key[q] = in ? key_of<float>(p[q], bias ? bias[e0 + q] : 0.f, l[q]) : -INFINITY;
-    if (in && key[q] != -FLT_MAX) kmax = fmaxf(kmax, fabsf(key[q]));
+    const float k = p[q] + b[q];
+    const bool off = l[q] == -INFINITY || k != k;
+    if (!off) kmax = fmaxf(kmax, fabsf(k));
+    key[q] = e0 + q < c.E ? order_of(off ? -FLT_MAX : fmaxf(k, -FLT_MAX)) : 0u;
   }
-  kmax = lanes_max(kmax);
-  // Error of a difference of two keys: scores within 14 units in the last place of the largest score (exp, the
-  // argument's and the sum's rounding, the quotient; a sigmoid within 4), each key's addition half a unit.
+  kmax = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(kmax)));
+  // Error of a difference of two keys, in units of 2^-24. Softmax, of the largest score: 5 of each score's
+  // exponential (with its argument's rounding), 12 of the sum and 3 of the quotient, which both share. Sigmoid:
+  // p (1 - p) (4 + |l|) of the exponential and 4 p of the quotient, under 7 a score. Half of |key| each addition.
   const float tau = (c.router == MOE_ROUTER_SOFTMAX ? 0x1p-18f : 0x1p-20f) * pmax + 0x1p-22f * kmax;
-  bool sure = true;
-  int e = select_experts<PER, float>(key, c, tau, sure);
-  if (!sure) e = select_exact<PER>(logits, bias, m, c);
-  float ps = 0.f;
+  bool groups_sure = true;
+  if (c.topk_groups < c.n_groups) {
+    const unsigned keep = kept_experts<PER>(key, c, tau, groups_sure);
+#pragma unroll
+    for (int q = 0; q < PER; ++q)
+      if (!(keep >> q & 1u)) key[q] = 0u;
+  }
+  // The k + 1 largest different keys; lane j keeps the j-th. (Equal ones are told by the candidates' number below.)
+  unsigned mine = 0u, last = kFull;
+  for (int j = 0; j <= c.k; ++j) {
+    unsigned top = 0u;
+#pragma unroll
+    for (int q = 0; q < PER; ++q) top = max(top, key[q] < last ? key[q] : 0u);
+    last = __reduce_max_sync(kFull, top);
+    if (lane == j) mine = last;
+  }
+  const unsigned next = __shfl_down_sync(kFull, mine, 1);
+  const bool near = lane < c.k && next && !(of_order(mine) - of_order(next) > tau);
+  const bool sure = !__any_sync(kFull, near);
+  const unsigned kth = __shfl_sync(kFull, mine, c.k - 1);   // 0: fewer than k different keys
+  // Candidates: the selection, or where it is not sure every expert whose key may reach it.
+  const unsigned least = sure || !kth ? kth : order_of(of_order(kth) - tau);
+  int n = 0;
 #pragma unroll
   for (int q = 0; q < PER; ++q) {
-    const float v = __shfl_sync(kFull, p[q], e / PER);
-    if (e % PER == q) ps = v;
+    const bool in = key[q] && key[q] >= least;
+    const unsigned mask = __ballot_sync(kFull, in);
+    const int at = n + __popc(mask & ((1u << lane) - 1u));
+    if (in && at < 32) {
+      scr[at] = e0 + q;
+      scr[32 + at] = key[q];
+    }
+    n += __popc(mask);
   }
-  if (lane >= c.k) ps = 0.f;
+  __syncwarp();
+  int e;
+  if (!groups_sure || n > 32) {
+    e = select_exact<PER>(logits, bias, m, c);
+  } else {
+    e = lane < n ? (int)scr[lane] : 0;
+    int rank = 0;
+    if (sure && n == c.k) {
+      const unsigned k1 = lane < n ? scr[32 + lane] : 0u;
+      for (int i = 0; i < n; ++i) rank += scr[32 + i] > k1;
+    } else {
+      rank = rank_exact(logits, bias, m, c, e, lane < n);
+    }
+    __syncwarp();
+    if (lane < n) scr[rank] = e;
+    __syncwarp();
+    e = lane < c.k ? (int)scr[lane] : 0;
+  }
+  __syncwarp();   // scr is free for the next token
+  float ps = 0.f;
+  if (lane < c.k) {
+    const float x = logits[e];
+    ps = c.router == MOE_ROUTER_SIGMOID ? 1.f / (1.f + expf(-x)) : sum == 0.f ? 0.f : expf(x - m) / sum;
+  }
   gate = c.renorm ? c.route_scale * (ps / (warp_sum(ps) + 1e-20f)) : c.route_scale * ps;
   return e;
 }
@@ -242,7 +347,7 @@ __device__ __forceinline__ int scan256(int v, int* tmp) {
 
 // Shared memory of the dispatch: run[e] = next sorted position of expert e, wcnt[w][e] = counts of a pass's warps.
 struct DispatchSmem {
-  int run[kMaxE], wcnt[kGateWarps][kMaxE], tmp[8];
+  int run[kMaxE], wcnt[kGateWarps][kMaxE], tmp[8];   // (wcnt also: each warp's scratch while it selects)
 };
 
 // Sorted positions of the assignments a0 .. a1, in passes of the block's threads; run[] holds each expert's first.
@@ -295,7 +400,7 @@ __global__ void __launch_bounds__(kGateThreads) gate_kernel(const float* __restr
   const int t0 = blockIdx.x * tokens, t1 = min(T, t0 + tokens);
   for (int t = t0 + w; t < t1; t += kGateWarps) {
     float g;
-    const int e = gate_token<PER>(logits + (size_t)t * c.E, bias, c, g);
+    const int e = gate_token<PER>(logits + (size_t)t * c.E, bias, c, reinterpret_cast<unsigned*>(sm.wcnt[w]), g);
     if (lane < c.k) {
       idx[(size_t)t * c.k + lane] = e;
       gate[(size_t)t * c.k + lane] = g;

@@ -26,40 +26,45 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
 }
 
 template <typename T, int VPT>
-__global__ void __launch_bounds__(1024) norm_fwd_kernel(const T* x, long long ld_x, const T* res,
-                                                        long long ld_res, const T* __restrict__ w, int d, float eps, T* h, T* y,
-                                                        uint8_t* q, float* scale, float* rstd) {
+__global__ void __launch_bounds__(VPT == 4 ? 512 : 1024, 1) norm_fwd_kernel(const T* x, long long ld_x, const T* res,
+                                                        long long ld_res, const T* __restrict__ w, int d, float eps,
+                                                        T* h, T* y, uint8_t* q, float* scale, float* rstd) {
   __shared__ float red[32];
   griddep_wait();
   griddep_launch();
   const long long t = blockIdx.x;
   const int nv = d >> 3;
-  float v[VPT][8];
-  float ss = 0.f;
+  Raw8<T> v[VPT], e[VPT];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int c = i * blockDim.x + threadIdx.x;
-    if (c < nv) load8(x + t * ld_x + 8 * c, v[i]);
+    if (c < nv) v[i].load(x + t * ld_x + 8 * c);
   }
   if (res) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = i * blockDim.x + threadIdx.x;
-      if (c < nv) {
-        float r[8];
-        load8(res + t * ld_res + 8 * c, r);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = to_f(from_f<T>(v[i][j] + r[j]));   // the sum as it is stored
-      }
+      if (c < nv) e[i].load(res + t * ld_res + 8 * c);
     }
   }
+  float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int c = i * blockDim.x + threadIdx.x;
     if (c < nv) {
-      if (h) store8(h + t * d + 8 * c, v[i]);
+      float f[8];
+      v[i].get(f);
+      if (res) {
+        float g[8];
+        e[i].get(g);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss += v[i][j] * v[i][j];
+        for (int j = 0; j < 8; ++j) f[j] += g[j];
+        v[i].set(f);     // the sum as it is stored
+        v[i].get(f);
+      }
+      if (h) v[i].store(h + t * d + 8 * c);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss += f[j] * f[j];
     }
   }
   const float r = __frsqrt_rn(block_sum(ss, red) / (float)d + eps);
@@ -68,25 +73,29 @@ __global__ void __launch_bounds__(1024) norm_fwd_kernel(const T* x, long long ld
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int c = i * blockDim.x + threadIdx.x;
+    float f[8];
     if (c < nv) {
       float g[8];
+      v[i].get(f);
       load8(w + 8 * c, g);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * r * g[j];
-      if (y) store8(y + t * d + 8 * c, v[i]);
+      for (int j = 0; j < 8; ++j) f[j] = f[j] * r * g[j];
+      if (y) store8(y + t * d + 8 * c, f);
     }
     if (q) {   // every lane takes part in the shuffles
-      const float m = half_warp_max(c < nv ? amax8(v[i]) : 0.f);
+      const float m = half_warp_max(c < nv ? amax8(f) : 0.f);
       if (c < nv) {
-        *reinterpret_cast<uint2*>(q + t * d + 8 * c) = codes8(v[i], m);
+        *reinterpret_cast<uint2*>(q + t * d + 8 * c) = codes8(f, m);
         if ((c & 15) == 0) scale[t * ((d + kScaleBlock - 1) / kScaleBlock) + (c >> 4)] = block_scale(m);
       }
     }
   }
 }
 
+// The next row's dy and h (and dh) are loaded before this row's reduction, so that their latency passes behind it
+// (not at VPT = 2, whose 1024 threads have no registers for it).
 template <typename T, int VPT>
-__global__ void __launch_bounds__(1024) norm_bwd_kernel(const T* dy, const T* dh, const T* __restrict__ h,
+__global__ void __launch_bounds__(1024, 1) norm_bwd_kernel(const T* dy, const T* dh, const T* __restrict__ h,
                                                         const T* __restrict__ w, const float* __restrict__ rstd,
                                                         int rows, int d, T* dx, float* part) {
   __shared__ float red[2][32];
@@ -99,17 +108,36 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(const T* dy, const T* dh
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
   const float inv_d = 1.0f / (float)d;
+  Raw8<T> py[VPT], ph[VPT], pe[VPT];
+  float pr = 0.f;
+  const auto fetch = [&](long long t) {
+    if (t >= rows) return;
+    pr = rstd[t];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = i * blockDim.x + threadIdx.x;
+      if (c < nv) {
+        py[i].load(dy + t * d + 8 * c);
+        ph[i].load(h + t * d + 8 * c);
+        if (dh && VPT == 1) pe[i].load(dh + t * d + 8 * c);
+      }
+    }
+  };
+  if (VPT == 1) fetch(blockIdx.x);
   int flip = 0;
   for (long long t = blockIdx.x; t < rows; t += gridDim.x, flip ^= 1) {
-    const float r = rstd[t];
+    if (VPT > 1) fetch(t);
+    const float r = pr;
+    Raw8<T> e[VPT];
     float a[VPT][8], n[VPT][8], s = 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = i * blockDim.x + threadIdx.x;
       if (c < nv) {
-        load8(dy + t * d + 8 * c, a[i]);
-        load8(h + t * d + 8 * c, n[i]);
         float g[8];
+        py[i].get(a[i]);
+        ph[i].get(n[i]);
+        if (VPT == 1) e[i] = pe[i];
         load8(w + 8 * c, g);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -120,6 +148,7 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(const T* dy, const T* dh
         }
       }
     }
+    if (VPT == 1) fetch(t + gridDim.x);
     if (!dx) continue;
     const float mean = block_sum(s, red[flip]) * inv_d;   // two buffers: one barrier a row
 #pragma unroll
@@ -127,7 +156,8 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(const T* dy, const T* dh
       const int c = i * blockDim.x + threadIdx.x;
       if (c < nv) {
         float o[8];
-        if (dh) load8(dh + t * d + 8 * c, o);
+        if (dh && VPT > 1) e[i].load(dh + t * d + 8 * c);
+        if (dh) e[i].get(o);
 #pragma unroll
         for (int j = 0; j < 8; ++j) o[j] = (dh ? o[j] : 0.f) + r * (a[i][j] - n[i][j] * mean);
         store8(dx + t * d + 8 * c, o);
@@ -143,24 +173,22 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(const T* dy, const T* dh
   }
 }
 
-// dw[c] = sum over the parts: a CTA takes 32 columns, its 8 rows of threads every eighth part.
-__global__ void __launch_bounds__(256) norm_dw_kernel(const float* __restrict__ part, int parts, int d, float* dw) {
-  __shared__ float red[8][33];
+// dw[c] = sum over the parts: a CTA takes 32 columns, each of its 32 warps every 32nd part.
+__global__ void __launch_bounds__(1024) norm_dw_kernel(const float* __restrict__ part, int parts, int d, float* dw) {
+  __shared__ float red[32][33];
   griddep_wait();
   griddep_launch();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
   float s = 0.f;
-  if (c < d)
-#pragma unroll 8
-    for (int p = w; p < parts; p += 8) s += part[(long long)p * d + c];
+  if (c < d) {
+#pragma unroll
+    for (int i = 0; i < (kNormCtas + 31) / 32; ++i)
+      if (w + 32 * i < parts) s += part[(long long)(w + 32 * i) * d + c];
+  }
   red[w][lane] = s;
   __syncthreads();
-  if (w == 0 && c < d) {
-    float t = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) t += red[i][lane];
-    dw[c] = t;
-  }
+  s = warp_sum(red[lane][w]);
+  if (lane == 0 && blockIdx.x * 32 + w < d) dw[blockIdx.x * 32 + w] = s;
 }
 
 template <typename T, int VPT>
@@ -182,7 +210,7 @@ cudaError_t bwd(const void* dy, const void* dh, const void* h, const void* w, co
 inline int steps(int d, bool wide) {
   const int nv = d / 8;
   if (wide) return nv <= 1024 ? 1 : 2;
-  return nv <= 256 ? 1 : nv <= 512 ? 2 : 4;
+  return nv <= 256 ? 1 : nv <= 1024 ? 2 : 4;
 }
 
 }  // namespace
@@ -212,7 +240,7 @@ cudaError_t norm_backward(const moe_ops_s* o, int dtype, const void* dy, const v
   }
   if (!dw) return cudaSuccess;
   *n += 1;
-  return launch_pdl(norm_dw_kernel, dim3(ceil_div(d, 32)), dim3(256), 0, s, (const float*)part, parts, d, dw);
+  return launch_pdl(norm_dw_kernel, dim3(ceil_div(d, 32)), dim3(1024), 0, s, (const float*)part, parts, d, dw);
 }
 
 }  // namespace moe

@@ -82,8 +82,7 @@ __global__ void __launch_bounds__(256) quant_cols_kernel(const bf16* __restrict_
   m = max_nan(max_nan(red[0][col], red[1][col]), max_nan(red[2][col], red[3][col]));
   if (c0 + col >= C) return;
   uint32_t w[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = codes4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3], m);
+  codes<32>(v, m, w);
   uint4* dst = reinterpret_cast<uint4*>(q + (long long)(c0 + col) * Tp + (long long)t * kScaleBlock + part * 32);
   dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
   dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
