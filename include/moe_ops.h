@@ -128,7 +128,10 @@ moe_status moe_quant_blocks(moe_ops ops, const void* w, int G, int N, int K, voi
  * Forward: a = quantised rows, b = weights. Gradient of the rows: a = quantised dc, b = transposed weights. */
 moe_status moe_fp8_matmul(moe_ops ops, const void* a, const float* a_scale, int a_rows, const int32_t* row_index,
                           int M, const void* b, const float* b_scale, const int32_t* off, int G, int N, int K,
-                          void* c, int out_dtype, void* stream);
+                          void* c, int out_dtype, void* workspace, void* stream);
+/* Bytes of workspace (16-byte aligned; 0: it may be NULL) of a call with these sizes, gathered = 1 with a row_index:
+ * many gathered rows are put in order first. */
+moe_status moe_fp8_matmul_workspace_size(int M, int G, int K, int gathered, size_t* bytes);
 /* Gradient of the weights: c[g, n, k] = sum over the tokens t of segment g of dc[t, n] x[t, k], from moe_quant_cols
  * of both: dct [N, Tp], dct_scale [Tp/128, N], xt [K, Tp], xt_scale [Tp/128, K]; c [G, N, K], zeros for a segment
  * without tokens. T and off as they were given to moe_quant_cols. */

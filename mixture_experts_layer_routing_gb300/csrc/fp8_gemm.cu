@@ -28,11 +28,24 @@ constexpr int BK = 128;                      // bytes (values) of the reduction 
 __host__ __device__ constexpr uint32_t idesc_f8(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
+template <int CG>
 __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
+  if (CG == 1)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// Arrival, in every CTA of the group, once this thread's MMAs so far are done.
+template <int CG>
+__device__ __forceinline__ void commit(uint32_t bar) {
+  if (CG == 1) mma_commit(bar);
+  else mma_commit_pair_mc(bar, 0x3);
 }
 // Four rows r0 .. r3 of the map's matrix, 128 bytes from column c each (rows past the matrix: zeros).
 __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* tm, int c, int r0, int r1, int r2, int r3,
@@ -53,12 +66,18 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
 __device__ __forceinline__ void named_sync(int id, int nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
-template <int COLS> __device__ __forceinline__ void tmem_alloc(uint32_t slot) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "n"(COLS) : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+template <int CG, int COLS> __device__ __forceinline__ void tmem_alloc(uint32_t slot) {
+  if (CG == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "n"(COLS) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "n"(COLS) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
 }
-template <int COLS> __device__ __forceinline__ void tmem_free(uint32_t base) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "n"(COLS));
+template <int CG, int COLS> __device__ __forceinline__ void tmem_free(uint32_t base) {
+  if (CG == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "n"(COLS) : "memory");
+  else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "n"(COLS) : "memory");
 }
 // Bounded wait that does not look at the abort flag: for what a role itself has in flight when it leaves.
 __device__ __forceinline__ void wait_own(uint32_t bar, uint32_t parity, int* status) {
@@ -71,13 +90,15 @@ __device__ __forceinline__ void wait_own(uint32_t bar, uint32_t parity, int* sta
   }
 }
 
-// As mbar_wait, without a call: a call inside the epilogue's loop would have to save its 128 sums.
-__device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
-  if (mbar_try_wait(bar, parity)) return true;
+// As mbar_wait, without a call (inside the epilogue's loop a call would have to save its 128 sums), and with acquire
+// of the other CTA's arrivals in a pair.
+template <int CG>
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  if (CG == 1 ? mbar_try_wait(bar, parity) : mbar_try_wait_cluster(bar, parity)) return true;
   const uint64_t t0 = global_ns();
 #pragma unroll 1
   for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (CG == 1 ? mbar_try_wait(bar, parity) : mbar_try_wait_cluster(bar, parity)) return true;
     if ((i & 63) == 0) {
       if (*abort_flag) return false;
       if (global_ns() - t0 > kWaitLimitNs) {
@@ -87,6 +108,24 @@ __device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, volat
       }
     }
   }
+}
+
+// Until *count (written by another warp of the CTA) is at least n.
+__device__ __forceinline__ bool wait_count(const volatile int* count, int n, volatile int* abort_flag, int* status) {
+  if (*count >= n) return true;
+  const uint64_t t0 = global_ns();
+#pragma unroll 1
+  for (uint32_t i = 1; *count < n; ++i) {
+    if ((i & 63) == 0) {
+      if (*abort_flag) return false;
+      if (global_ns() - t0 > kWaitLimitNs) {
+        set_error(status, MOE_ERR_TIMEOUT);
+        *abort_flag = 1;
+        return false;
+      }
+    }
+  }
+  return true;
 }
 
 struct GemmParams {
@@ -100,6 +139,7 @@ struct GemmParams {
   int M;                  // wgrad: rows of c
   int N;
   int nkb;                // K blocks (wgrad: from the segment)
+  int vec;                // widest aligned store to c: 32 or 16 bytes, or 0
   void* c;
   int* status;
 };
@@ -127,16 +167,11 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-// Waits for this thread's TMEM loads; u is used after it.
-__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&u)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(u[0]), "+r"(u[1]), "+r"(u[2]), "+r"(u[3]), "+r"(u[4]), "+r"(u[5]), "+r"(u[6]), "+r"(u[7]),
-                 "+r"(u[8]), "+r"(u[9]), "+r"(u[10]), "+r"(u[11]), "+r"(u[12]), "+r"(u[13]), "+r"(u[14]), "+r"(u[15]),
-                 "+r"(u[16]), "+r"(u[17]), "+r"(u[18]), "+r"(u[19]), "+r"(u[20]), "+r"(u[21]), "+r"(u[22]),
-                 "+r"(u[23]), "+r"(u[24]), "+r"(u[25]), "+r"(u[26]), "+r"(u[27]), "+r"(u[28]), "+r"(u[29]),
-                 "+r"(u[30]), "+r"(u[31])
-               :
-               : "memory");
+// Waits for this thread's TMEM loads; u and v are used after it.
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&u)[32], uint32_t (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(u[i]), "+r"(v[i]));
 }
 // acc += u s (columns' scales v too, where they differ) for 32 columns.
 template <bool COLS>
@@ -155,32 +190,69 @@ __device__ __forceinline__ void add_scaled(uint64_t* acc, const uint32_t (&u)[32
   }
 }
 
-template <typename O> struct Out;
-template <> struct Out<bf16> {
-  static __device__ __forceinline__ void store(bf16* p, const float* f) { *reinterpret_cast<uint4*>(p) = pack8(f); }
-};
-template <> struct Out<float> {
-  static __device__ __forceinline__ void store(float* p, const float* f) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+// The first `left` of 16 neighbouring values of a row of c, in the widest stores its alignment allows (32 bytes: a
+// whole sector, so that no sector is written in two parts).
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+template <typename O>
+__device__ __forceinline__ void store16(O* p, const float (&f)[16], int left, int vec) {
+  constexpr bool F32 = sizeof(O) == 4;
+  if (vec == 32) {            // rows are made of 32-byte pieces
+    uint32_t w[8];
+    if (F32) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(f[i]);
+      store32(p, w);
+      if (left > 8) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(f[8 + i]);
+        store32(p + 8, w);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = pack2(f[2 * i], f[2 * i + 1]);
+      store32(p, w);
+    }
+  } else if (vec == 16) {
+#pragma unroll
+    for (int i = 0; i < 16; i += F32 ? 4 : 8) {
+      if (i < left) {
+        uint4 w;
+        if (F32) w = make_uint4(__float_as_uint(f[i]), __float_as_uint(f[i + 1]), __float_as_uint(f[i + 2]), __float_as_uint(f[i + 3]));
+        else w = pack8(f + (i & 8));
+        *reinterpret_cast<uint4*>(p + i) = w;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < left) p[i] = from_f<O>(f[i]);
   }
-};
+}
 
 // ------------------------------------------------------------------- wide
-constexpr int WM = 128, WN = 256, kWStages = 4, kWBufs = 2;
-constexpr int kWStageBytes = (WM + WN) * BK;
+constexpr int WM = 128, WN = 256, WH = 128;            // rows a CTA, columns a tile, columns a partial
+constexpr int kWBufs = 512 / WH;                       // partials in TMEM
+constexpr int kWMma = 3;                               // MMA warps
 constexpr int kWEpi = 8;                               // epilogue warps: four lane quadrants x two column halves
-constexpr int kWThreads = (4 + kWEpi) * 32;            // producer, MMA, two idle warps, epilogue
-struct WideSmem {
+constexpr int kWThreads = (1 + kWMma + kWEpi) * 32;
+// CG CTAs work on one tile of CG x 128 rows; each holds its own rows and 1 / CG of the columns' operand.
+template <int CG> constexpr int w_stage_bytes() { return (WM + WN / CG) * BK; }
+template <int CG> constexpr int w_stages() { return CG == 1 ? 4 : 6; }
+struct alignas(16) WideSmem {
+  float sb[2][WN];                                     // wgrad: column scales, by K block parity
   SegSmem seg;
-  alignas(16) float sb[kWBufs][WN];                    // wgrad: column scales of the K block in each partial
-  uint64_t full[kWStages], empty[kWStages], pfull[kWBufs], pempty[kWBufs];
+  uint64_t full[6], empty[6], pfull[kWBufs], pempty[kWBufs], drain;
   uint32_t tmem;
   int abort;
+  int issued[kWBufs];                                  // uses of each partial that have been issued
 };
-constexpr int kWSmem = kWStages * kWStageBytes + 1024 + (int)sizeof(WideSmem);
-// Registers: 384 threads are launched with 168 each; the epilogue's 256 take 216, the other 128 give down to 72.
-constexpr int kWRegs = 168, kWRegsEpi = 216, kWRegsRest = 72;
+template <int CG> constexpr int w_smem() { return w_stages<CG>() * w_stage_bytes<CG>() + 1024 + (int)sizeof(WideSmem); }
+// Registers: 384 threads are launched with 168 each; the epilogue's 256 take 224, the other 128 give down to 56.
+constexpr int kWRegs = 168, kWRegsEpi = 224, kWRegsRest = 56;
 static_assert(256 * kWRegsEpi + 128 * kWRegsRest <= kWThreads * kWRegs, "register split");
 
 struct WTile {
@@ -188,13 +260,15 @@ struct WTile {
 };
 
 // Unit L of the schedule: row tiles in groups of 16, all column tiles of a group before the next (L2 reuse).
-template <bool WGRAD>
-__device__ __forceinline__ WTile wide_tile(const GemmParams& p, const SegSmem& s, int L) {
+// row0: this CTA's rows.
+template <int CG, bool WGRAD>
+__device__ __forceinline__ WTile wide_tile(const GemmParams& p, const SegSmem& s, int L, int rank) {
+  constexpr int TM = CG * WM;
   const int nt = (p.N + WN - 1) / WN;
   WTile t;
-  int m, mt, local;
+  int mt, local;
   if (WGRAD) {
-    mt = (p.M + WM - 1) / WM;
+    mt = (p.M + TM - 1) / TM;
     t.g = L / (mt * nt);
     local = L - t.g * mt * nt;
   } else {
@@ -209,215 +283,233 @@ __device__ __forceinline__ WTile wide_tile(const GemmParams& p, const SegSmem& s
   }
   const int grp = local / (kRasterM * nt), gm = min(kRasterM, mt - grp * kRasterM);
   const int within = local - grp * kRasterM * nt;
-  m = grp * kRasterM + within % gm;
+  const int m = grp * kRasterM + within % gm;
   t.n0 = within / gm * WN;
   if (WGRAD) {
-    t.row0 = m * WM;
+    t.row0 = m * TM + rank * WM;
     t.row_end = p.M;
     t.kb0 = s.tile[t.g];
     t.nkb = s.tile[t.g + 1] - t.kb0;
   } else {
-    t.row0 = s.off[t.g] + m * WM;
+    t.row0 = s.off[t.g] + m * TM + rank * WM;
     t.row_end = s.off[t.g + 1];
     t.kb0 = 0;
     t.nkb = p.nkb;
   }
   return t;
 }
-template <bool WGRAD>
+template <int CG, bool WGRAD>
 __device__ __forceinline__ int wide_units(const GemmParams& p, const SegSmem& s) {
   const int nt = (p.N + WN - 1) / WN;
-  return (WGRAD ? p.G * ((p.M + WM - 1) / WM) : s.tile[p.G]) * nt;
+  return (WGRAD ? p.G * ((p.M + CG * WM - 1) / (CG * WM)) : s.tile[p.G]) * nt;
 }
 
-template <bool WGRAD, bool GATHER, typename O>
+// K block `it` of this CTA's run is stage it mod the ring, and its two column halves are partials 2 it and 2 it + 1
+// mod 4. The partials are issued by three warps in turn: the tensor pipe holds little more than one MMA of queued
+// work, and a thread that issues, then tests two barriers, then issues again leaves it idle for the tests. A warp
+// that is ahead of the others must not take an older phase of a partial's barrier for the one it needs (parities
+// repeat every second use), so each use is counted when it is issued, and the next waits for the count first.
+template <int CG, bool WGRAD, typename O>
 __global__ void __launch_bounds__(kWThreads, 1)
     fp8_wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, GemmParams p) {
+  constexpr int ST = w_stages<CG>(), SB = w_stage_bytes<CG>();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  WideSmem& sm = *reinterpret_cast<WideSmem*>(ring + kWStages * kWStageBytes);
+  WideSmem& sm = *reinterpret_cast<WideSmem*>(ring + ST * SB);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = CG == 2 ? (int)cluster_ctarank() : 0;
   volatile int* abort_flag = &sm.abort;
   const uint32_t full0 = smem_u32(sm.full), empty0 = smem_u32(sm.empty), pfull0 = smem_u32(sm.pfull),
-                 pempty0 = smem_u32(sm.pempty);
+                 pempty0 = smem_u32(sm.pempty), drain = smem_u32(&sm.drain);
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kWStages; ++i) {
+    for (int i = 0; i < ST; ++i) {
       mbar_init(full0 + 8 * i, 1);
-      mbar_init(empty0 + 8 * i, 1);
+      mbar_init(empty0 + 8 * i, 2);
     }
     for (int i = 0; i < kWBufs; ++i) {
       mbar_init(pfull0 + 8 * i, 1);
-      mbar_init(pempty0 + 8 * i, kWEpi);
+      mbar_init(pempty0 + 8 * i, 4 * CG);
     }
+    mbar_init(drain, kWMma);
+    for (int i = 0; i < kWBufs; ++i) sm.issued[i] = 0;
     sm.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   griddep_wait();     // before the allocation: no CTA holds TMEM while the predecessor may still want some
   griddep_launch();
-  if (warp == 1) tmem_alloc<512>(smem_u32(&sm.tmem));
-  load_segments(sm.seg, p.off, p.G, p.rows, WGRAD ? BK : WM, p.status);
+  if (warp == 1) tmem_alloc<CG, 512>(smem_u32(&sm.tmem));
+  load_segments(sm.seg, p.off, p.G, p.rows, WGRAD ? BK : CG * WM, p.status);
   tc_fence_before();
   __syncthreads();
+  if (CG == 2) cluster_sync();   // the other CTA's barriers are initialised
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
-  const int units = wide_units<WGRAD>(p, sm.seg);
+  const int units = wide_units<CG, WGRAD>(p, sm.seg);
+  const int first = blockIdx.x / CG, step = gridDim.x / CG;
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWRegsRest));
     if (warp == 0) {
-      // ---------------------------------------------------------------- producer
+      // ------------------------------------------------------- producer (lane 0)
       int it = 0;
       bool ok = true;
-      for (int L = blockIdx.x; L < units && ok; L += gridDim.x) {
-        const WTile t = wide_tile<WGRAD>(p, sm.seg, L);
-        int r[4];
-        if (GATHER) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int m = t.row0 + 4 * lane + i;
-            r[i] = gather_row(p, m, t.row_end);
-          }
-        }
-        const int brow = WGRAD ? t.n0 : t.g * p.N + t.n0;
+      const uint32_t lead = CG == 2 ? mapa_shared(full0, 0) : full0;   // both CTAs' copies count on rank 0's barrier
+      for (int L = first; L < units && ok && lane == 0; L += step) {
+        const WTile t = wide_tile<CG, WGRAD>(p, sm.seg, L, rank);
+        const int brow = (WGRAD ? t.n0 : t.g * p.N + t.n0) + rank * (WH / CG);
         for (int kb = 0; kb < t.nkb; ++kb, ++it) {
-          const int s = it % kWStages;
-          ok = __all_sync(0xffffffffu,
-                          mbar_wait(empty0 + 8 * s, ((it / kWStages) & 1) ^ 1, abort_flag, p.status));
+          const int s = it % ST;
+          ok = mbar_wait(empty0 + 8 * s, ((it / ST) & 1) ^ 1, abort_flag, p.status);
           if (!ok) break;
-          const uint32_t a = smem_u32(ring + s * kWStageBytes), fb = full0 + 8 * s;
+          const uint32_t a = smem_u32(ring + s * SB), b = a + WM * BK;
           const int k = (t.kb0 + kb) * BK;
-          if (lane == 0) {
-            mbar_arrive_expect_tx(fb, kWStageBytes);
-            tma_load_2d(a + WM * BK, &tmB, k, brow, fb);
-            if (!GATHER) tma_load_2d(a, &tmA, k, t.row0, fb);
-          }
-          if (GATHER) {
-            __syncwarp();
-            tma_gather4(a + lane * 4 * BK, &tmA, k, r[0], r[1], r[2], r[3], fb);
+          if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * s, CG * SB);
+          if (CG == 1) {
+            tma_load_2d(b, &tmB, k, brow, lead + 8 * s);
+            tma_load_2d(a, &tmA, k, t.row0, lead + 8 * s);
+          } else {   // this CTA's half of each partial's columns
+            tma_load_2d_pair(b, &tmB, k, brow, lead + 8 * s);
+            tma_load_2d_pair(a, &tmA, k, t.row0, lead + 8 * s);
+            tma_load_2d_pair(b + WH / CG * BK, &tmB, k, brow + WH, lead + 8 * s);
           }
         }
       }
-      if (!ok && lane == 0) {   // the copies still in flight
-        for (int i = max(0, it - kWStages); i < it; ++i)
-          wait_own(full0 + 8 * (i % kWStages), (i / kWStages) & 1, p.status);
+      if (!ok && rank == 0) {   // the copies still in flight (lane 0)
+        for (int i = max(0, it - ST); i < it; ++i) wait_own(full0 + 8 * (i % ST), (i / ST) & 1, p.status);
       }
       __syncwarp();
-    } else if (warp == 1) {
-      // --------------------------------------------------------------------- MMA (lane 0 issues)
-      int it = 0, last = -1;
-      bool ok = true;
-      for (int L = blockIdx.x; L < units && ok && lane == 0; L += gridDim.x) {
-        const WTile t = wide_tile<WGRAD>(p, sm.seg, L);
-        for (int kb = 0; kb < t.nkb; ++kb, ++it) {
-          const int s = it % kWStages, b = it % kWBufs;
-          ok = mbar_wait(pempty0 + 8 * b, ((it / kWBufs) & 1) ^ 1, abort_flag, p.status) &&
-               mbar_wait(full0 + 8 * s, (it / kWStages) & 1, abort_flag, p.status);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t a = smem_u32(ring + s * kWStageBytes);
-          const uint64_t da = desc_kmajor(a), db = desc_kmajor(a + WM * BK);
+    } else {
+      // --------------------------------------------- MMA (lane 0; rank 0 for a pair)
+      if (lane == 0 && rank == 0) {
+        int it = 0, turn = warp - 1;   // partials until this warp's next one
+        bool ok = true;
+        for (int L = first; L < units && ok; L += step) {
+          const WTile t = wide_tile<CG, WGRAD>(p, sm.seg, L, rank);
+          for (int kb = 0; kb < t.nkb && ok; ++kb, ++it) {
 #pragma unroll
-          for (int k = 0; k < BK / 32; ++k)
-            mma_f8(tmem + b * WN, da + 2 * k, db + 2 * k, idesc_f8(WM, WN), k > 0 ? 1u : 0u);
-          mma_commit(empty0 + 8 * s);
-          mma_commit(pfull0 + 8 * b);
-          last = it;
+            for (int h = 0; h < 2; ++h) {
+              if (turn > 0) {
+                --turn;
+                continue;
+              }
+              turn = kWMma - 1;
+              const int s = it % ST, b = (2 * it + h) % kWBufs;
+              ok = mbar_wait(full0 + 8 * s, (it / ST) & 1, abort_flag, p.status) &&
+                   wait_count(&sm.issued[b], it / 2, abort_flag, p.status) &&
+                   wait_for<CG>(pempty0 + 8 * b, ((it / 2) & 1) ^ 1, abort_flag, p.status);
+              if (!ok) break;
+              tc_fence_after();
+              const uint32_t a = smem_u32(ring + s * SB);
+              const uint64_t da = desc_kmajor(a), db = desc_kmajor(a + WM * BK + h * (WH / CG) * BK);
+#pragma unroll
+              for (int k = 0; k < BK / 32; ++k)
+                mma_f8<CG>(tmem + b * WH, da + 2 * k, db + 2 * k, idesc_f8(CG * WM, WH), k > 0 ? 1u : 0u);
+              commit<CG>(pfull0 + 8 * b);
+              commit<CG>(empty0 + 8 * s);
+              *(volatile int*)&sm.issued[b] = it / 2 + 1;
+            }
+          }
         }
+        // nothing of this CTA's is in flight when its TMEM is given back
+        if (CG == 1) mma_commit(drain);
+        else mma_commit_pair(drain);
+        wait_own(drain, 0, p.status);
       }
-      // the last MMAs' arrival: nothing of this CTA's is in flight when its TMEM is given back
-      if (last >= 0) wait_own(pfull0 + 8 * (last % kWBufs), (last / kWBufs) & 1, p.status);
       __syncwarp();
     }
   } else {
-    // -------------------------------------------------------------------- epilogue
+    // ----------------------------------------------------------------- epilogue
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWRegsEpi));
     const int quad = warp & 3, half = (warp - 4) >> 2;
     const int r = quad * 32 + lane, ht = threadIdx.x & 127;   // row of the tile; thread of this column half
-    const uint32_t tq = tmem + half * 128 + ((uint32_t)(quad * 32) << 16);
-    const int nb = (p.N + 127) / 128;
-    const bool vec = p.N % 8 == 0;
+    const uint32_t tq = tmem + half * WH + ((uint32_t)(quad * 32) << 16);
+    const uint32_t back0 = (CG == 2 ? mapa_shared(pempty0, 0) : pempty0) + 8 * half;
     int it = 0;
     bool ok = true;   // after a failed wait: no more waiting or storing, every named barrier still reached
-    for (int L = blockIdx.x; L < units; L += gridDim.x) {
-      const WTile t = wide_tile<WGRAD>(p, sm.seg, L);
-      const int row = t.row0 + r, col0 = t.n0 + half * 128;
-      const bool valid = row < t.row_end;
-      const float *sa = p.sa, *sb = p.sb;
-      int sa_step = 1;
-      bool zero = false;   // a row index out of range reads zeros
-      if (WGRAD) {
-        sa += (size_t)t.kb0 * p.M + (valid ? row : 0);
-        sa_step = p.M;
-        sb += (size_t)t.kb0 * p.N + min(col0 + ht, p.N - 1);
-      } else {
-        int ar = valid ? (GATHER ? p.row_index[row] : row) : 0;
-        if ((unsigned)ar >= (unsigned)p.a_rows) {
-          set_error(p.status, MOE_ERR_DEVICE_INDEX);
-          ar = 0;
-          zero = true;
-        }
-        sa += (size_t)ar * p.nkb;
-        sb += ((size_t)t.g * nb + min(col0 / 128, nb - 1)) * p.nkb;
-      }
-      uint64_t acc[64];    // pairs of neighbouring columns
+    for (int L = first; L < units; L += step) {
+      uint64_t acc[WH / 2];    // pairs of neighbouring columns
 #pragma unroll
-      for (int i = 0; i < 64; ++i) acc[i] = 0;
-      float na = t.nkb > 0 ? __ldg(sa) : 0.f, nsb = t.nkb > 0 ? __ldg(sb) : 0.f;
-      for (int kb = 0; kb < t.nkb; ++kb, ++it) {
-        const int b = it % kWBufs;
-        float s = zero ? 0.f : na;
+      for (int i = 0; i < WH / 2; ++i) acc[i] = 0;
+      {
+        const WTile t = wide_tile<CG, WGRAD>(p, sm.seg, L, rank);
+        const int row = t.row0 + r, col0 = t.n0 + half * WH;
+        const bool valid = row < t.row_end;
+        const float *sa = p.sa, *sb = p.sb;
         if (WGRAD) {
-          sm.sb[b][half * 128 + ht] = nsb;
-          named_sync(1 + half, 128);
+          sa += (size_t)t.kb0 * p.M + (valid ? row : 0);
+          sb += (size_t)t.kb0 * p.N + min(col0 + ht, p.N - 1);
         } else {
-          s *= nsb;
+          const int nb = (p.N + 127) / 128;
+          sa += (size_t)(valid ? row : 0) * p.nkb;
+          sb += ((size_t)t.g * nb + min(col0 / 128, nb - 1)) * p.nkb;
         }
-        if (kb + 1 < t.nkb) {
-          na = __ldg(sa + (size_t)(kb + 1) * sa_step);
-          nsb = __ldg(sb + (size_t)(kb + 1) * (WGRAD ? p.N : 1));
+        float na = 0.f, nsb = 0.f;
+        if (t.nkb > 0) {
+          na = __ldg(sa);
+          nsb = __ldg(sb);
         }
-        ok = __all_sync(0xffffffffu, ok && wait_inline(pfull0 + 8 * b, (it / kWBufs) & 1, abort_flag, p.status));
-        if (ok) {
-          tc_fence_after();
-          // while 32 columns are added, the next 32 are on their way
-          uint32_t u[2][32];
-          tmem_ld32(tq + b * WN, u[0]);
-          tmem_ld_wait_for(u[0]);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if (c < 3) {
-              tmem_ld32(tq + b * WN + (c + 1) * 32, u[(c + 1) & 1]);
-            } else {   // the partial is read: the MMAs after the next may have it
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(pempty0 + 8 * b);
+        for (int kb = t.nkb; kb > 0; --kb, ++it) {
+          const int par = it & 1;
+          float s = na;
+          if (WGRAD) {
+            sm.sb[par][threadIdx.x - 128] = nsb;
+            named_sync(1 + half, 128);
+          } else {
+            s *= nsb;
+          }
+          if (kb > 1) {
+            sa += WGRAD ? p.M : 1;
+            sb += WGRAD ? p.N : 1;
+            na = __ldg(sa);
+            nsb = __ldg(sb);
+          }
+          ok = __all_sync(0xffffffffu, ok && wait_for<CG>(pfull0 + 8 * (2 * par + half), (it >> 1) & 1, abort_flag, p.status));
+          if (ok) {
+            tc_fence_after();
+            // 64 columns at a time; the partial is given back before its last ones are added
+            uint32_t u[32], v[32];
+            const uint32_t tc = tq + par * 2 * WH;
+            const float* cs = &sm.sb[par][half * WH];
+            tmem_ld32(tc, u);
+            tmem_ld32(tc + 32, v);
+            tmem_ld_wait_for(u, v);
+            add_scaled<WGRAD>(acc, u, s, cs);
+            add_scaled<WGRAD>(acc + 16, v, s, cs + 32);
+            tmem_ld32(tc + 64, u);
+            tmem_ld32(tc + 96, v);
+            tmem_ld_wait_for(u, v);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if (CG == 1) mbar_arrive(back0 + 16 * par);
+              else mbar_arrive_cluster(back0 + 16 * par);
             }
-            add_scaled<WGRAD>(acc + c * 16, u[c & 1], s, &sm.sb[b][half * 128 + c * 32]);
-            if (c < 3) tmem_ld_wait_for(u[(c + 1) & 1]);
+            add_scaled<WGRAD>(acc + 32, u, s, cs + 64);
+            add_scaled<WGRAD>(acc + 48, v, s, cs + 96);
           }
         }
       }
-      if (!ok || !valid) continue;
-      O* out = (O*)p.c + (WGRAD ? (size_t)t.g * p.M : (size_t)0) * p.N + (size_t)row * p.N + col0;
+      const WTile t = wide_tile<CG, WGRAD>(p, sm.seg, L, rank);
+      const int row = t.row0 + r, col0 = t.n0 + half * WH;
+      if (ok && row < t.row_end) {
+      O* out = (O*)p.c + ((WGRAD ? (size_t)t.g * p.M : (size_t)0) + row) * p.N + col0;
+      const int cols = min(WH, p.N - col0);
 #pragma unroll
-      for (int i = 0; i < 128; i += 8) {
-        float f[8];
+      for (int i = 0; i < WH; i += 16) {
+        float f[16];
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) unpair(acc[(i + j) / 2], f[j], f[j + 1]);
-        if (vec) {
-          if (col0 + i < p.N) Out<O>::store(out + i, f);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (col0 + i + j < p.N) out[i + j] = from_f<O>(f[j]);
-        }
+        for (int j = 0; j < 16; j += 2) unpair(acc[(i + j) / 2], f[j], f[j + 1]);
+        if (i < cols) store16(out + i, f, cols - i, p.vec);
       }
+      }
+      __syncwarp();
     }
   }
   tc_fence_before();
   __syncthreads();
+  if (CG == 2) cluster_sync();   // neither CTA leaves while the pair's MMAs or arrivals may touch it
   tc_fence_after();
-  if (warp == 1) tmem_free<512>(tmem);
+  if (warp == 1) tmem_free<CG, 512>(tmem);
 }
 
 // ----------------------------------------------------------------- narrow
@@ -468,7 +560,7 @@ __global__ void __launch_bounds__(kNThreads)
   }
   griddep_wait();     // before the allocation, as in the wide kernel
   griddep_launch();
-  if (warp == 1) tmem_alloc<COLS>(smem_u32(&sm.tmem));
+  if (warp == 1) tmem_alloc<1, COLS>(smem_u32(&sm.tmem));
   load_segments(sm.seg, p.off, p.G, p.rows, NT, p.status);
   tc_fence_before();
   __syncthreads();
@@ -551,7 +643,7 @@ __global__ void __launch_bounds__(kNThreads)
         const uint64_t da = desc_kmajor(a), db = desc_kmajor(a + 128 * BK);
 #pragma unroll
         for (int k = 0; k < BK / 32; ++k)
-          mma_f8(tmem + b * NT, da + 2 * k, db + 2 * k, idesc_f8(128, NT), k > 0 ? 1u : 0u);
+          mma_f8<1>(tmem + b * NT, da + 2 * k, db + 2 * k, idesc_f8(128, NT), k > 0 ? 1u : 0u);
         mma_commit(empty0 + 8 * s);
         mma_commit(pfull0 + 8 * b);
         last = kb;
@@ -607,7 +699,7 @@ __global__ void __launch_bounds__(kNThreads)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_free<COLS>(tmem);
+  if (warp == 1) tmem_free<1, COLS>(tmem);
   if (S > 1) {
     // add the parts in rank order; the CTAs share out the tokens
     cluster_sync();
@@ -626,7 +718,7 @@ __global__ void __launch_bounds__(kNThreads)
 
 // -------------------------------------------------------------------- host
 constexpr int kMaxSmem = 227 * 1024, kNarrowMaxKb = 128;
-static_assert(kWSmem <= kMaxSmem && n_smem<64>(kNarrowMaxKb) <= kMaxSmem && n_smem<16>(kNarrowMaxKb) <= kMaxSmem &&
+static_assert(w_smem<1>() <= kMaxSmem && w_smem<2>() <= kMaxSmem && n_smem<64>(kNarrowMaxKb) <= kMaxSmem && n_smem<16>(kNarrowMaxKb) <= kMaxSmem &&
                   n_smem<32>(kNarrowMaxKb) <= kMaxSmem,
               "shared memory per CTA");
 
@@ -634,9 +726,9 @@ template <typename K>
 cudaError_t set_smem(K kern) {
   return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
 }
-template <bool WGRAD, bool GATHER, typename O>
+template <int CG, bool WGRAD, typename O>
 cudaError_t init_wide() {
-  auto kern = fp8_wide_kernel<WGRAD, GATHER, O>;
+  auto kern = fp8_wide_kernel<CG, WGRAD, O>;
   cudaFuncAttributes at;
   MOE_TRY(cudaFuncGetAttributes(&at, kern));
   if (at.numRegs != kWRegs) return cudaErrorInvalidKernelImage;   // what the epilogue's registers are taken out of
@@ -650,12 +742,53 @@ cudaError_t init_narrow() {
   return set_smem(fp8_narrow_kernel<NT, true, float>);
 }
 
-template <bool WGRAD, bool GATHER, typename O>
+template <int CG, bool WGRAD, typename O>
 cudaError_t launch_wide(const moe_ops_s* o, const CUtensorMap& a, const CUtensorMap& b, const GemmParams& p,
                         long long units, cudaStream_t s) {
-  auto kern = fp8_wide_kernel<WGRAD, GATHER, O>;
-  const int grid = (int)(units < o->sms ? units : o->sms);
-  return launch_pdl(kern, dim3(grid), dim3(kWThreads), kWSmem, s, a, b, p);
+  auto kern = fp8_wide_kernel<CG, WGRAD, O>;
+  if (CG == 1) return launch_pdl(kern, dim3((unsigned)(units < o->sms ? units : o->sms)), dim3(kWThreads), w_smem<CG>(), s, a, b, p);
+  // as many pairs as run at once
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * (unsigned)(units < o->pairs ? units : o->pairs));
+  cfg.blockDim = dim3(kWThreads);
+  cfg.dynamicSmemBytes = w_smem<CG>();
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, a, b, p);
+}
+template <bool WGRAD>
+cudaError_t pick_wide(const moe_ops_s* o, int cg, const CUtensorMap& a, const CUtensorMap& b, const GemmParams& p,
+                      long long units, bool fp32, cudaStream_t s) {
+  if (cg == 1)
+    return fp32 ? launch_wide<1, WGRAD, float>(o, a, b, p, units, s) : launch_wide<1, WGRAD, bf16>(o, a, b, p, units, s);
+  return fp32 ? launch_wide<2, WGRAD, float>(o, a, b, p, units, s) : launch_wide<2, WGRAD, bf16>(o, a, b, p, units, s);
+}
+
+// Rows of a (and their scales) in the order of c's rows, one warp a row; an index out of range gives zeros.
+__global__ void __launch_bounds__(256) gather_rows_kernel(const uint8_t* __restrict__ a, const float* __restrict__ sa,
+                                                          const int* __restrict__ row_index, int M, int a_rows, int K,
+                                                          int nkb, uint8_t* __restrict__ out, float* __restrict__ so,
+                                                          int* status) {
+  griddep_wait();
+  griddep_launch();
+  const int lane = threadIdx.x & 31, m = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (m >= M) return;
+  const int r = row_index[m];
+  const bool in = (unsigned)r < (unsigned)a_rows;
+  if (!in) set_error(status, MOE_ERR_DEVICE_INDEX);
+  const uint4* src = reinterpret_cast<const uint4*>(a + (size_t)(in ? r : 0) * K);
+  uint4* dst = reinterpret_cast<uint4*>(out + (size_t)m * K);
+#pragma unroll 4
+  for (int i = lane; i < K / 16; i += 32) dst[i] = in ? src[i] : make_uint4(0u, 0u, 0u, 0u);
+  for (int i = lane; i < nkb; i += 32) so[(size_t)m * nkb + i] = in ? sa[(size_t)r * nkb + i] : 0.f;
 }
 
 template <int NT, bool GATHER, typename O>
@@ -688,23 +821,50 @@ cudaError_t pick_narrow(const CUtensorMap& a, const CUtensorMap& b, const GemmPa
   return fp32 ? launch_narrow<NT, false, float>(a, b, p, units, S, s) : launch_narrow<NT, false, bf16>(a, b, p, units, S, s);
 }
 
+int out_vec(const void* c, long long n, int fp32) {
+  const long long bytes = n * (fp32 ? 4 : 2);
+  const uintptr_t at = (uintptr_t)c;
+  return bytes % 32 == 0 && at % 32 == 0 ? 32 : bytes % 16 == 0 && at % 16 == 0 ? 16 : 0;
+}
+// Few rows a segment: the weights' bytes decide, and the narrow kernel fills its MMAs with them.
+bool use_narrow(int M, int G, int K) { return ceil_div(M, G) <= 64 && ceil_div(K, BK) <= kNarrowMaxKb; }
+
 }  // namespace
 
-cudaError_t fp8_init() {
-  MOE_TRY((init_wide<false, false, bf16>()));
-  MOE_TRY((init_wide<false, false, float>()));
-  MOE_TRY((init_wide<false, true, bf16>()));
-  MOE_TRY((init_wide<false, true, float>()));
-  MOE_TRY((init_wide<true, false, bf16>()));
-  MOE_TRY((init_wide<true, false, float>()));
+cudaError_t fp8_init(int* pairs) {
+  MOE_TRY((init_wide<1, false, bf16>()));
+  MOE_TRY((init_wide<1, false, float>()));
+  MOE_TRY((init_wide<1, true, bf16>()));
+  MOE_TRY((init_wide<1, true, float>()));
+  MOE_TRY((init_wide<2, false, bf16>()));
+  MOE_TRY((init_wide<2, false, float>()));
+  MOE_TRY((init_wide<2, true, bf16>()));
+  MOE_TRY((init_wide<2, true, float>()));
   MOE_TRY(init_narrow<16>());
   MOE_TRY(init_narrow<32>());
-  return init_narrow<64>();
+  MOE_TRY(init_narrow<64>());
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(1024);
+  cfg.blockDim = dim3(kWThreads);
+  cfg.dynamicSmemBytes = w_smem<2>();
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaOccupancyMaxActiveClusters(pairs, (fp8_wide_kernel<2, false, bf16>), &cfg);
+}
+
+size_t fp8_matmul_workspace(int M, int G, int K, bool gathered) {
+  if (!gathered || use_narrow(M, G, K)) return 0;
+  return (size_t)M * K + 16 + sizeof(float) * (size_t)M * ceil_div(K, BK);
 }
 
 cudaError_t fp8_matmul(const moe_ops_s* o, const void* a, const float* sa, int a_rows, const int* row_index, int M,
                        const void* b, const float* sb, const int* off, int G, int N, int K, void* c, int out_fp32,
-                       cudaStream_t s, long long* n) {
+                       void* ws, cudaStream_t s, long long* n) {
   GemmParams p = {};
   p.sa = sa;
   p.sb = sb;
@@ -715,13 +875,12 @@ cudaError_t fp8_matmul(const moe_ops_s* o, const void* a, const float* sa, int a
   p.a_rows = a_rows;
   p.N = N;
   p.nkb = ceil_div(K, BK);
+  p.vec = out_vec(c, N, out_fp32);
   p.c = c;
   p.status = o->status;
   CUtensorMap ta, tb;
-  const int avg = ceil_div(M, G);
-  *n += 1;
-  if (avg <= 64 && p.nkb <= kNarrowMaxKb) {
-    const int NT = avg <= 12 ? 16 : avg <= 24 ? 32 : 64;
+  if (use_narrow(M, G, K)) {
+    const int avg = ceil_div(M, G), NT = avg <= 12 ? 16 : avg <= 24 ? 32 : 64;
     if (!make_tmap(&ta, a, K, a_rows, BK, row_index ? 1 : NT, 1) ||
         !make_tmap(&tb, b, K, (uint64_t)G * N, BK, 128, 1))
       return cudaErrorInvalidValue;
@@ -730,18 +889,28 @@ cudaError_t fp8_matmul(const moe_ops_s* o, const void* a, const float* sa, int a
     const long long most = (G < M ? G : M), units = (M / NT + most < M ? M / NT + most : M) * (long long)nt;
     int S = 1;
     while (S < 8 && 2 * S <= p.nkb && units * S * 2 <= 2 * o->sms) S *= 2;
+    *n += 1;
     return NT == 16 ? pick_narrow<16>(ta, tb, p, units, S, out_fp32, s)
            : NT == 32 ? pick_narrow<32>(ta, tb, p, units, S, out_fp32, s)
                       : pick_narrow<64>(ta, tb, p, units, S, out_fp32, s);
   }
-  if (!make_tmap(&ta, a, K, a_rows, BK, row_index ? 1 : WM, 1) || !make_tmap(&tb, b, K, (uint64_t)G * N, BK, WN, 1))
+  if (row_index) {
+    // Gathered rows are put in order once. (TMA gathers inside the product fetch them again for every column tile,
+    // and one of four 128-byte rows takes about 80 cycles: 2,600 cycles a stage of 128 rows, whose MMAs take 512.)
+    float* so = (float*)((char*)ws + ((size_t)M * K + 15) / 16 * 16);
+    *n += 1;
+    MOE_TRY(launch_pdl(gather_rows_kernel, dim3(ceil_div(M, 8)), dim3(256), 0, s, (const uint8_t*)a, sa, row_index, M,
+                       a_rows, K, p.nkb, (uint8_t*)ws, so, o->status));
+    a = ws;
+    p.sa = so;
+    p.a_rows = a_rows = M;
+  }
+  const int cg = ceil_div(M, G) > WM ? 2 : 1;
+  if (!make_tmap(&ta, a, K, a_rows, BK, WM, 1) || !make_tmap(&tb, b, K, (uint64_t)G * N, BK, cg == 2 ? WH / 2 : WN, 1))
     return cudaErrorInvalidValue;
-  const long long units = ((long long)ceil_div(M, WM) + (G > 1 ? G : 0)) * ceil_div(N, WN);
-  if (row_index)
-    return out_fp32 ? launch_wide<false, true, float>(o, ta, tb, p, units, s)
-                    : launch_wide<false, true, bf16>(o, ta, tb, p, units, s);
-  return out_fp32 ? launch_wide<false, false, float>(o, ta, tb, p, units, s)
-                  : launch_wide<false, false, bf16>(o, ta, tb, p, units, s);
+  const long long units = ((long long)ceil_div(M, cg * WM) + (G > 1 ? G : 0)) * ceil_div(N, WN);
+  *n += 1;
+  return pick_wide<false>(o, cg, ta, tb, p, units, out_fp32, s);
 }
 
 cudaError_t fp8_wgrad(const moe_ops_s* o, const void* dct, const float* sdct, const void* xt, const float* sxt, int T,
@@ -754,15 +923,16 @@ cudaError_t fp8_wgrad(const moe_ops_s* o, const void* dct, const float* sdct, co
   p.rows = T;
   p.M = N;
   p.N = K;
+  p.vec = out_vec(c, K, out_fp32);
   p.c = c;
   p.status = o->status;
-  const int Tp = quant_cols_rows(T, G);
+  const int Tp = quant_cols_rows(T, G), cg = N > WM ? 2 : 1;
   CUtensorMap ta, tb;
-  if (!make_tmap(&ta, dct, Tp, N, BK, WM, 1) || !make_tmap(&tb, xt, Tp, K, BK, WN, 1)) return cudaErrorInvalidValue;
-  const long long units = (long long)G * ceil_div(N, WM) * ceil_div(K, WN);
+  if (!make_tmap(&ta, dct, Tp, N, BK, WM, 1) || !make_tmap(&tb, xt, Tp, K, BK, cg == 2 ? WH / 2 : WN, 1))
+    return cudaErrorInvalidValue;
+  const long long units = (long long)G * ceil_div(N, cg * WM) * ceil_div(K, WN);
   *n += 1;
-  return out_fp32 ? launch_wide<true, false, float>(o, ta, tb, p, units, s)
-                  : launch_wide<true, false, bf16>(o, ta, tb, p, units, s);
+  return pick_wide<true>(o, cg, ta, tb, p, units, out_fp32, s);
 }
 
 }  // namespace moe

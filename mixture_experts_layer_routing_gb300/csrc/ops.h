@@ -9,6 +9,7 @@
 struct moe_ops_s {
   int device;
   int sms;
+  int pairs;              // two-CTA clusters of the wide products that run at once
   int* status;            // device word: the first device-side error
   long long launches;
 };
@@ -45,10 +46,11 @@ cudaError_t quant_cols(const moe_ops_s* o, const void* src, long long ld, int sr
 cudaError_t quant_blocks(const moe_ops_s* o, const void* w, int G, int N, int K, void* q, float* scale, void* qt,
                          float* scale_t, cudaStream_t s, long long* n);
 
-cudaError_t fp8_init();             // kernel attributes on the current device
+cudaError_t fp8_init(int* pairs);   // kernel attributes on the current device
+size_t fp8_matmul_workspace(int M, int G, int K, bool gathered);
 cudaError_t fp8_matmul(const moe_ops_s* o, const void* a, const float* sa, int a_rows, const int* row_index, int M,
                        const void* b, const float* sb, const int* off, int G, int N, int K, void* c, int out_fp32,
-                       cudaStream_t s, long long* n);
+                       void* ws, cudaStream_t s, long long* n);
 cudaError_t fp8_wgrad(const moe_ops_s* o, const void* dct, const float* sdct, const void* xt, const float* sxt, int T,
                       const int* off, int G, int N, int K, void* c, int out_fp32, cudaStream_t s, long long* n);
 

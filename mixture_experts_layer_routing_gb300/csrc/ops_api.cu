@@ -58,7 +58,7 @@ moe_status moe_ops_create(moe_ops* out) {
   CHECK(o, MOE_ERR_CUDA);
   if (cudaGetDevice(&o->device) != cudaSuccess ||
       cudaDeviceGetAttribute(&o->sms, cudaDevAttrMultiProcessorCount, o->device) != cudaSuccess ||
-      fp8_init() != cudaSuccess || cudaMalloc(&o->status, sizeof(int)) != cudaSuccess) {
+      fp8_init(&o->pairs) != cudaSuccess || o->pairs < 1 || cudaMalloc(&o->status, sizeof(int)) != cudaSuccess) {
     cudaGetLastError();
     delete o;
     return MOE_ERR_CUDA;
@@ -234,9 +234,15 @@ moe_status moe_quant_blocks(moe_ops ops, const void* w, int G, int N, int K, voi
   DONE(quant_blocks(ops, w, G, N, K, q, scale, qt, scale_t, (cudaStream_t)stream, &n_));
 }
 
+moe_status moe_fp8_matmul_workspace_size(int M, int G, int K, int gathered, size_t* bytes) {
+  CHECK(M >= 0 && G >= 1 && K >= 1 && bytes, MOE_ERR_INVALID_ARG);
+  *bytes = fp8_matmul_workspace(M, G, K, gathered != 0);
+  return MOE_OK;
+}
+
 moe_status moe_fp8_matmul(moe_ops ops, const void* a, const float* a_scale, int a_rows, const int32_t* row_index,
                           int M, const void* b, const float* b_scale, const int32_t* off, int G, int N, int K, void* c,
-                          int out_dtype, void* stream) {
+                          int out_dtype, void* workspace, void* stream) {
   CHECK(ops && M >= 0 && a_rows >= 0 && N >= 1 && K >= 1 && G >= 1, MOE_ERR_INVALID_ARG);
   CHECK(off || G == 1, MOE_ERR_INVALID_ARG);
   CHECK(row_index || a_rows >= M, MOE_ERR_INVALID_ARG);
@@ -247,8 +253,10 @@ moe_status moe_fp8_matmul(moe_ops ops, const void* a, const float* a_scale, int 
   CHECK(a && a_scale && a_rows >= 1 && b && b_scale && c, MOE_ERR_INVALID_ARG);
   CHECK(aligned(a, 16) && aligned(b, 16) && aligned(c, 16) && aligned(a_scale, 4) && aligned(b_scale, 4),
         MOE_ERR_UNSUPPORTED);
+  CHECK(fp8_matmul_workspace(M, G, K, row_index != nullptr) == 0 || (workspace && aligned(workspace, 16)),
+        MOE_ERR_WORKSPACE);
   HANDLE(ops);
-  DONE(fp8_matmul(ops, a, a_scale, a_rows, row_index, M, b, b_scale, off, G, N, K, c, out_dtype == MOE_FP32,
+  DONE(fp8_matmul(ops, a, a_scale, a_rows, row_index, M, b, b_scale, off, G, N, K, c, out_dtype == MOE_FP32, workspace,
                   (cudaStream_t)stream, &n_));
 }
 

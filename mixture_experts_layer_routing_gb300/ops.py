@@ -17,7 +17,7 @@ from . import (MOE_BF16, MOE_FP32, MOE_ROUTER_SIGMOID, MOE_ROUTER_SOFTMAX, MoeEr
 OPS_EXPORTED = ("moe_ops_create", "moe_ops_destroy", "moe_ops_get_status", "moe_ops_launch_count",
                 "moe_norm_forward", "moe_norm_workspace_size", "moe_norm_backward", "moe_gate_workspace_size",
                 "moe_gate_forward", "moe_gate_backward", "moe_quant_rows", "moe_quant_cols_rows", "moe_quant_cols",
-                "moe_quant_blocks", "moe_fp8_matmul", "moe_fp8_wgrad")
+                "moe_quant_blocks", "moe_fp8_matmul", "moe_fp8_matmul_workspace_size", "moe_fp8_wgrad")
 
 BLOCK = 128                     # values that share a scale
 F8 = torch.float8_e4m3fn
@@ -56,7 +56,8 @@ def _lib():
     lib.moe_quant_cols_rows.argtypes = [i32, i32, P(i32)]
     lib.moe_quant_cols.argtypes = [vp, vp, i64, i32, i32, i32, vp, i32, vp, vp, vp, vp]
     lib.moe_quant_blocks.argtypes = [vp, vp, i32, i32, i32] + [vp] * 5
-    lib.moe_fp8_matmul.argtypes = [vp, vp, vp, i32, vp, i32, vp, vp, vp, i32, i32, i32, vp, i32, vp]
+    lib.moe_fp8_matmul.argtypes = [vp, vp, vp, i32, vp, i32, vp, vp, vp, i32, i32, i32, vp, i32, vp, vp]
+    lib.moe_fp8_matmul_workspace_size.argtypes = [i32, i32, i32, i32, P(sz)]
     lib.moe_fp8_wgrad.argtypes = [vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, vp, i32, vp]
     for name in OPS_EXPORTED:
         getattr(lib, name).restype = i32
@@ -347,9 +348,15 @@ class MoeOps:
         if out.dtype not in _DTYPES:
             raise TypeError(f"out: bf16 or fp32 expected, got {out.dtype}")
         _want(out, "out", out.dtype, (M, N), dev)
+        ws = None
+        if row_index is not None:
+            n = ctypes.c_size_t()
+            _check(self._lib.moe_fp8_matmul_workspace_size(M, G, K, 1, ctypes.byref(n)),
+                   "moe_fp8_matmul_workspace_size")
+            ws = self._scratch(n.value, stream) if n.value else None
         _check(self._lib.moe_fp8_matmul(self.h, a.data_ptr(), a_scale.data_ptr(), rows, _ptr(row_index), M,
                                         b.data_ptr(), b_scale.data_ptr(), _ptr(off), G, N, K, out.data_ptr(),
-                                        _DTYPES[out.dtype], self._stream(stream)), "moe_fp8_matmul")
+                                        _DTYPES[out.dtype], _ptr(ws), self._stream(stream)), "moe_fp8_matmul")
         return out
 
     def fp8_wgrad(self, dct, dct_scale, xt, xt_scale, off=None, tokens=None, out=None, out_dtype=torch.bfloat16,

@@ -178,6 +178,39 @@ def test_many_experts(ops, per):
     assert ops.status() == 0
 
 
+@pytest.mark.parametrize("M,N,K,cnt", [(100, 40000, 2048, None), (700, 16384, 2176, None),
+                                       (1500, 8192, 1536, [200, 0, 700, 130, 470])])
+def test_many_tiles_a_cta(ops, M, N, K, cnt):
+    """Several tiles for every CTA of the wide kernel, each of many blocks of the reduction (rows sampled)."""
+    q, s, w, A, B = operands(ops, M, N, K, len(cnt) if cnt else 0, seed=30)
+    off = make_off(cnt).tolist() if cnt else [0, M]
+    got = ops.fp8_matmul(q, s, w["q"], w["scale"], off=make_off(cnt).cuda() if cnt else None)
+    assert ops.status() == 0
+    for g, (lo, hi) in enumerate(zip(off[:-1], off[1:])):
+        rows = np.unique(np.linspace(lo, hi - 1, 7).astype(int)) if hi > lo else []
+        if len(rows):
+            b = B[g] if cnt else B
+            near(got[torch.from_numpy(rows).cuda()], A[rows] @ b.T, np.abs(A[rows]) @ np.abs(b).T, -(-K // 128))
+
+
+def test_many_tiles_of_weight_gradients(ops):
+    cnt, N, K = [900, 0, 300, 1500], 1024, 4096
+    off = make_off(cnt)
+    dc, x = rnd(2700, N, seed=31), rnd(2700, K, seed=32)
+    dq, ds = ops.quant_cols(dc.cuda(), off=off.cuda())
+    xq, xs = ops.quant_cols(x.cuda(), off=off.cuda())
+    got = ops.fp8_wgrad(dq, ds, xq, xs, off=off.cuda(), tokens=2700)
+    assert ops.status() == 0
+    rows = np.arange(0, N, 37)
+    for g, (lo, hi) in enumerate(zip(off[:-1].tolist(), off[1:].tolist())):
+        if lo == hi:
+            assert not got[g].any()
+            continue
+        d = oo.values(*oo.quantise(f64(dc)[lo:hi][:, rows], 0), 0)
+        v = oo.values(*oo.quantise(f64(x)[lo:hi], 0), 0)
+        near(got[g][torch.from_numpy(rows).cuda()], d.T @ v, np.abs(d).T @ np.abs(v), -(-(hi - lo) // 128))
+
+
 def test_rows_of_no_segment_stay(ops):
     q, s, w, A, B = operands(ops, 300, 128, 256, 3, seed=8)
     for off in ([0, 10, 12, 40], [0, 100, 230, 260]):

@@ -102,7 +102,7 @@ def test_gate_refuses_arguments(lib, over, code):
 
 
 MM = dict(ops=P, a=P, sa=P, a_rows=64, row_index=None, M=64, b=P, sb=P, off=None, G=1, N=128, K=256, c=P, out=1,
-          stream=None)
+          workspace=None, stream=None)
 
 
 @pytest.mark.parametrize("over,code", [
@@ -111,6 +111,7 @@ MM = dict(ops=P, a=P, sa=P, a_rows=64, row_index=None, M=64, b=P, sb=P, off=None
     (dict(a=None), ARG), (dict(sa=None), ARG), (dict(b=None), ARG), (dict(sb=None), ARG), (dict(c=None), ARG),
     (dict(a=P + 8), UNSUP), (dict(b=P + 8), UNSUP), (dict(c=P + 8), UNSUP),
     (dict(G=256, off=P, N=1 << 24), UNSUP),
+    (dict(M=200, row_index=P), WS), (dict(M=200, row_index=P, workspace=P + 8), WS),
 ])
 def test_matmul_refuses(lib, over, code):
     assert call(lib, "moe_fp8_matmul", MM, over) == code
