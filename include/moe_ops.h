@@ -134,7 +134,7 @@ moe_status moe_fp8_matmul(moe_ops ops, const void* a, const float* a_scale, int 
 moe_status moe_fp8_matmul_workspace_size(int M, int G, int K, int gathered, size_t* bytes);
 /* Gradient of the weights: c[g, n, k] = sum over the tokens t of segment g of dc[t, n] x[t, k], from moe_quant_cols
  * of both: dct [N, Tp], dct_scale [Tp/128, N], xt [K, Tp], xt_scale [Tp/128, K]; c [G, N, K], zeros for a segment
- * without tokens. T and off as they were given to moe_quant_cols. */
+ * without tokens. T and off as they were given to moe_quant_cols; N and K multiples of 8, scales 16-byte aligned. */
 moe_status moe_fp8_wgrad(moe_ops ops, const void* dct, const float* dct_scale, const void* xt, const float* xt_scale,
                          int T, const int32_t* off, int G, int N, int K, void* c, int out_dtype, void* stream);
 

@@ -63,9 +63,6 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
-__device__ __forceinline__ void named_sync(int id, int nthreads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
-}
 template <int CG, int COLS> __device__ __forceinline__ void tmem_alloc(uint32_t slot) {
   if (CG == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "n"(COLS) : "memory");
@@ -90,15 +87,13 @@ __device__ __forceinline__ void wait_own(uint32_t bar, uint32_t parity, int* sta
   }
 }
 
-// As mbar_wait, without a call (inside the epilogue's loop a call would have to save its 128 sums), and with acquire
-// of the other CTA's arrivals in a pair.
-template <int CG>
-__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
-  if (CG == 1 ? mbar_try_wait(bar, parity) : mbar_try_wait_cluster(bar, parity)) return true;
+// As mbar_wait, without a call: inside the epilogue's loop a call would have to save its 128 sums.
+__device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = global_ns();
 #pragma unroll 1
   for (uint32_t i = 1;; ++i) {
-    if (CG == 1 ? mbar_try_wait(bar, parity) : mbar_try_wait_cluster(bar, parity)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     if ((i & 63) == 0) {
       if (*abort_flag) return false;
       if (global_ns() - t0 > kWaitLimitNs) {
@@ -109,15 +104,26 @@ __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile
     }
   }
 }
-
-// Until *count (written by another warp of the CTA) is at least n.
-__device__ __forceinline__ bool wait_count(const volatile int* count, int n, volatile int* abort_flag, int* status) {
-  if (*count >= n) return true;
-  const uint64_t t0 = global_ns();
+// A whole warp's wait. Every lane tests: one lane's test and a broadcast of its result measured slower, through the
+// warp's divergence (a product of 8192 x 4096 x 7168 in 222 us instead of 139, its epilogue taken out).
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  return __all_sync(0xffffffffu, wait_inline(bar, parity, abort_flag, status));
+}
+// A single thread's wait by tests that do not suspend it (mbarrier.test_wait): it goes on sooner.
+__device__ __forceinline__ bool spin_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  uint64_t t0 = 0;
 #pragma unroll 1
-  for (uint32_t i = 1; *count < n; ++i) {
-    if ((i & 63) == 0) {
+  for (uint32_t i = 1;; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if ((i & 0xfff) == 0) {
       if (*abort_flag) return false;
+      if (t0 == 0) t0 = global_ns();
       if (global_ns() - t0 > kWaitLimitNs) {
         set_error(status, MOE_ERR_TIMEOUT);
         *abort_flag = 1;
@@ -125,9 +131,12 @@ __device__ __forceinline__ bool wait_count(const volatile int* count, int n, vol
       }
     }
   }
-  return true;
 }
-
+// Arrival on a barrier that may be the other CTA's. What it hands over is tensor memory that was read (ordered by
+// tcgen05.fence), so it needs no release of ordinary memory to the cluster, which costs over 1,000 cycles here.
+__device__ __forceinline__ void arrive_remote(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
 struct GemmParams {
   const float* sa;        // scales of the rows: [a_rows][nkb], or (wgrad) [K blocks][M]
   const float* sb;        // of the columns: [G][ceil(N / 128)][nkb], or (wgrad) [K blocks][N]
@@ -167,18 +176,20 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-// Waits for this thread's TMEM loads; u and v are used after it.
-__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&u)[32], uint32_t (&v)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(u[i]), "+r"(v[i]));
+// Waits for this thread's TMEM loads; u is used after it.
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&u)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(u[0]), "+r"(u[1]), "+r"(u[2]), "+r"(u[3]), "+r"(u[4]), "+r"(u[5]), "+r"(u[6]), "+r"(u[7]),
+                 "+r"(u[8]), "+r"(u[9]), "+r"(u[10]), "+r"(u[11]), "+r"(u[12]), "+r"(u[13]), "+r"(u[14]), "+r"(u[15])
+               :
+               : "memory");
 }
-// acc += u s (columns' scales v too, where they differ) for 32 columns.
+// acc += u s (columns' scales v too, where they differ) for 16 columns.
 template <bool COLS>
-__device__ __forceinline__ void add_scaled(uint64_t* acc, const uint32_t (&u)[32], float s, const float* v) {
+__device__ __forceinline__ void add_scaled(uint64_t* acc, const uint32_t (&u)[16], float s, const float* v) {
   const uint64_t s2 = pair(s, s);
 #pragma unroll
-  for (int i = 0; i < 32; i += 4) {
+  for (int i = 0; i < 16; i += 4) {
     uint64_t a = s2, b = s2;
     if (COLS) {
       const float4 f = *reinterpret_cast<const float4*>(v + i);
@@ -234,26 +245,33 @@ __device__ __forceinline__ void store16(O* p, const float (&f)[16], int left, in
 }
 
 // ------------------------------------------------------------------- wide
-constexpr int WM = 128, WN = 256, WH = 128;            // rows a CTA, columns a tile, columns a partial
-constexpr int kWBufs = 512 / WH;                       // partials in TMEM
-constexpr int kWMma = 3;                               // MMA warps
-constexpr int kWEpi = 8;                               // epilogue warps: four lane quadrants x two column halves
-constexpr int kWThreads = (1 + kWMma + kWEpi) * 32;
+constexpr int WM = 128, WN = 256, WC = 128;            // rows a CTA, columns a tile, columns (sums) a thread
+constexpr int kWBufs = 512 / WN;                       // partials in TMEM, and warps that issue MMAs
+constexpr int kWEpi = 4 * WN / WC;                     // epilogue warps: four lane quadrants x column halves
+constexpr int kWThreads = (4 + kWEpi) * 32;            // producer, MMA warps, scales, epilogue
+constexpr int kWChunk = 8;                             // K blocks whose scales are fetched at a time
 // CG CTAs work on one tile of CG x 128 rows; each holds its own rows and 1 / CG of the columns' operand.
 template <int CG> constexpr int w_stage_bytes() { return (WM + WN / CG) * BK; }
 template <int CG> constexpr int w_stages() { return CG == 1 ? 4 : 6; }
-struct alignas(16) WideSmem {
-  float sb[2][WN];                                     // wgrad: column scales, by K block parity
+struct alignas(128) WideSmem {
+  // Scales of 16 K blocks, slot it mod 16: of this CTA's rows, and of the columns (wgrad; else entries 0 and 1, the
+  // halves'). wgrad's come by TMA with the operands, the others by a warp of their own, 8 K blocks at a time.
+  float sa[2 * kWChunk][WM], sb[2 * kWChunk][WN];
   SegSmem seg;
-  uint64_t full[6], empty[6], pfull[kWBufs], pempty[kWBufs], drain;
+  uint64_t full[6], empty[6], pfull[kWBufs], pempty[kWBufs], sfull[2], sempty[2], drain;
   uint32_t tmem;
   int abort;
-  int issued[kWBufs];                                  // uses of each partial that have been issued
 };
 template <int CG> constexpr int w_smem() { return w_stages<CG>() * w_stage_bytes<CG>() + 1024 + (int)sizeof(WideSmem); }
-// Registers: 384 threads are launched with 168 each; the epilogue's 256 take 224, the other 128 give down to 56.
-constexpr int kWRegs = 168, kWRegsEpi = 224, kWRegsRest = 56;
-static_assert(256 * kWRegsEpi + 128 * kWRegsRest <= kWThreads * kWRegs, "register split");
+// Registers: 384 threads are launched with 168 each, of which the epilogue's 256 take more and the other 128 give up
+// some: the split at which neither side spills (a spill of eight registers in the loop cost 20% of the time).
+constexpr int kWRegs = 168;
+template <int CG> constexpr int w_regs_epi() { return CG == 1 ? 216 : 224; }
+template <int CG> constexpr int w_regs_rest() { return CG == 1 ? 72 : 56; }
+template <int CG> constexpr bool w_regs_fit() {
+  return kWEpi * 32 * w_regs_epi<CG>() + 128 * w_regs_rest<CG>() <= kWThreads * kWRegs;
+}
+static_assert(w_regs_fit<1>() && w_regs_fit<2>(), "register split");
 
 struct WTile {
   int g, row0, row_end, n0, kb0, nkb;
@@ -304,15 +322,24 @@ __device__ __forceinline__ int wide_units(const GemmParams& p, const SegSmem& s)
   return (WGRAD ? p.G * ((p.M + CG * WM - 1) / (CG * WM)) : s.tile[p.G]) * nt;
 }
 
-// K block `it` of this CTA's run is stage it mod the ring, and its two column halves are partials 2 it and 2 it + 1
-// mod 4. The partials are issued by three warps in turn: the tensor pipe holds little more than one MMA of queued
-// work, and a thread that issues, then tests two barriers, then issues again leaves it idle for the tests. A warp
-// that is ahead of the others must not take an older phase of a partial's barrier for the one it needs (parities
-// repeat every second use), so each use is counted when it is issued, and the next waits for the count first.
+// K block `it` of this CTA's run is stage it mod the ring and partial it mod 2. A warp of its own issues each
+// partial's MMAs: the tensor pipe holds little more than one MMA of queued work, and a single thread that tests
+// barriers between its MMAs leaves it idle for the tests (about 100 cycles each; 225 us became 210 with the second
+// warp). A partial's uses have to come from one warp: barriers tell phases by parity, and a warp ahead of another
+// would take an older release of the same partial for its own.
+// Measured, 8192 x 4096 x 7168: 196 us (2.45 PFLOP/s) at 1.82 GHz under the power limit; 167 with the epilogue's
+// loads and sums left out, 140 without the operands' copies either. Single CTAs instead of pairs: 220 us (48 KB of
+// operands a K block of 512 MMA cycles is more than the 56 bytes a cycle that come from L2 into an SM, and shared
+// memory's 128 bytes a cycle carry the copies and the MMAs' reads). Four partials of 128 columns: 198 us (twice the
+// MMAs to issue). Sixteen epilogue warps of 64 columns: 216 us.
 template <int CG, bool WGRAD, typename O>
 __global__ void __launch_bounds__(kWThreads, 1)
-    fp8_wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, GemmParams p) {
+    fp8_wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                    const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB, GemmParams p) {
   constexpr int ST = w_stages<CG>(), SB = w_stage_bytes<CG>();
+  // wgrad's slots: the copies of K block i follow the MMAs of i - ST, which follow the epilogue's release of
+  // i - ST - 2, so they cannot meet the reading of i - 16.
+  static_assert(ST + 3 <= 2 * kWChunk, "scale slots");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   WideSmem& sm = *reinterpret_cast<WideSmem*>(ring + ST * SB);
@@ -320,18 +347,22 @@ __global__ void __launch_bounds__(kWThreads, 1)
   const int rank = CG == 2 ? (int)cluster_ctarank() : 0;
   volatile int* abort_flag = &sm.abort;
   const uint32_t full0 = smem_u32(sm.full), empty0 = smem_u32(sm.empty), pfull0 = smem_u32(sm.pfull),
-                 pempty0 = smem_u32(sm.pempty), drain = smem_u32(&sm.drain);
+                 pempty0 = smem_u32(sm.pempty), sfull0 = smem_u32(sm.sfull), sempty0 = smem_u32(sm.sempty),
+                 drain = smem_u32(&sm.drain);
   if (threadIdx.x == 0) {
     for (int i = 0; i < ST; ++i) {
       mbar_init(full0 + 8 * i, 1);
-      mbar_init(empty0 + 8 * i, 2);
+      mbar_init(empty0 + 8 * i, 1);
     }
     for (int i = 0; i < kWBufs; ++i) {
       mbar_init(pfull0 + 8 * i, 1);
-      mbar_init(pempty0 + 8 * i, 4 * CG);
+      mbar_init(pempty0 + 8 * i, kWEpi * CG);
     }
-    mbar_init(drain, kWMma);
-    for (int i = 0; i < kWBufs; ++i) sm.issued[i] = 0;
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(sm.sfull + i), 32);
+      mbar_init(smem_u32(sm.sempty + i), kWEpi);
+    }
+    mbar_init(drain, kWBufs);
     sm.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -343,12 +374,14 @@ __global__ void __launch_bounds__(kWThreads, 1)
   __syncthreads();
   if (CG == 2) cluster_sync();   // the other CTA's barriers are initialised
   tc_fence_after();
-  const uint32_t tmem = sm.tmem;
-  const int units = wide_units<CG, WGRAD>(p, sm.seg);
-  const int first = blockIdx.x / CG, step = gridDim.x / CG;
+  // (each role reads what it needs of these itself: kept over the branch they cost the epilogue registers)
+  const auto tmem_base = [&] { return *(volatile uint32_t*)&sm.tmem; };
+  const auto unit_count = [&] { return wide_units<CG, WGRAD>(p, sm.seg); };
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWRegsRest));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(w_regs_rest<CG>()));
+    const uint32_t tmem = tmem_base();
+    const int units = unit_count(), first = blockIdx.x / CG, step = gridDim.x / CG;
     if (warp == 0) {
       // ------------------------------------------------------- producer (lane 0)
       int it = 0;
@@ -356,21 +389,23 @@ __global__ void __launch_bounds__(kWThreads, 1)
       const uint32_t lead = CG == 2 ? mapa_shared(full0, 0) : full0;   // both CTAs' copies count on rank 0's barrier
       for (int L = first; L < units && ok && lane == 0; L += step) {
         const WTile t = wide_tile<CG, WGRAD>(p, sm.seg, L, rank);
-        const int brow = (WGRAD ? t.n0 : t.g * p.N + t.n0) + rank * (WH / CG);
+        const int brow = (WGRAD ? t.n0 : t.g * p.N + t.n0) + rank * (WN / CG);
         for (int kb = 0; kb < t.nkb; ++kb, ++it) {
           const int s = it % ST;
           ok = mbar_wait(empty0 + 8 * s, ((it / ST) & 1) ^ 1, abort_flag, p.status);
           if (!ok) break;
           const uint32_t a = smem_u32(ring + s * SB), b = a + WM * BK;
           const int k = (t.kb0 + kb) * BK;
-          if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * s, CG * SB);
-          if (CG == 1) {
-            tma_load_2d(b, &tmB, k, brow, lead + 8 * s);
-            tma_load_2d(a, &tmA, k, t.row0, lead + 8 * s);
-          } else {   // this CTA's half of each partial's columns
-            tma_load_2d_pair(b, &tmB, k, brow, lead + 8 * s);
-            tma_load_2d_pair(a, &tmA, k, t.row0, lead + 8 * s);
-            tma_load_2d_pair(b + WH / CG * BK, &tmB, k, brow + WH, lead + 8 * s);
+          if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * s, CG * (SB + (WGRAD ? 4 * (WM + WN) : 0)));
+          const auto load = [&](uint32_t dst, const CUtensorMap* tm, int c0, int c1) {
+            if (CG == 1) tma_load_2d(dst, tm, c0, c1, lead + 8 * s);
+            else tma_load_2d_pair(dst, tm, c0, c1, lead + 8 * s);
+          };
+          load(b, &tmB, k, brow);          // (a pair: this CTA's half of the columns)
+          load(a, &tmA, k, t.row0);
+          if (WGRAD) {
+            load(smem_u32(sm.sa[it % (2 * kWChunk)]), &tmSA, t.row0, t.kb0 + kb);
+            load(smem_u32(sm.sb[it % (2 * kWChunk)]), &tmSB, t.n0, t.kb0 + kb);
           }
         }
       }
@@ -378,36 +413,57 @@ __global__ void __launch_bounds__(kWThreads, 1)
         for (int i = max(0, it - ST); i < it; ++i) wait_own(full0 + 8 * (i % ST), (i / ST) & 1, p.status);
       }
       __syncwarp();
+    } else if (warp == 3) {
+      // ------------------------------------------------------------- scales
+      // A thread's row is a row of the scales too, so an epilogue that reads them itself touches a line a lane and K
+      // block. This warp reads a chunk ahead.
+      int ch = 0;
+      bool ok = true;
+      for (int L = first; L < units && ok && !WGRAD; L += step) {
+        const WTile t = wide_tile<CG, WGRAD>(p, sm.seg, L, rank);
+        const int nb = (p.N + 127) / 128;
+        for (int k0 = 0; k0 < t.nkb; k0 += kWChunk, ++ch) {
+          const int j = (ch & 1) * kWChunk, n = min(kWChunk, t.nkb - k0);
+          ok = warp_wait(sempty0 + 8 * (ch & 1), ((ch >> 1) & 1) ^ 1, abort_flag, p.status);
+          if (!ok) break;
+#pragma unroll
+          for (int i = lane; i < WM; i += 32) {
+            const float* row = p.sa + (size_t)min(t.row0 + i, max(t.row_end - 1, 0)) * p.nkb + k0;
+            float v[kWChunk];
+#pragma unroll
+            for (int k = 0; k < kWChunk; ++k) v[k] = k < n ? __ldg(row + k) : 0.f;
+#pragma unroll
+            for (int k = 0; k < kWChunk; ++k) sm.sa[j + k][i] = v[k];
+          }
+          if (lane < 2 * kWChunk) {
+            const int h = lane / kWChunk, k = lane % kWChunk;
+            if (k < n) sm.sb[j + k][h] = __ldg(p.sb + ((size_t)t.g * nb + min(t.n0 / 128 + h, nb - 1)) * p.nkb + k0 + k);
+          }
+          mbar_arrive(sfull0 + 8 * (ch & 1));
+        }
+      }
     } else {
       // --------------------------------------------- MMA (lane 0; rank 0 for a pair)
-      if (lane == 0 && rank == 0) {
-        int it = 0, turn = warp - 1;   // partials until this warp's next one
+      if (lane == 0 && rank == 0 && warp <= kWBufs) {
+        const int b = warp - 1;
+        int it = 0;
         bool ok = true;
         for (int L = first; L < units && ok; L += step) {
           const WTile t = wide_tile<CG, WGRAD>(p, sm.seg, L, rank);
-          for (int kb = 0; kb < t.nkb && ok; ++kb, ++it) {
+          for (int kb = 0; kb < t.nkb; ++kb, ++it) {
+            if (it % kWBufs != b) continue;
+            const int s = it % ST;
+            ok = spin_wait(full0 + 8 * s, (it / ST) & 1, abort_flag, p.status) &&
+                 spin_wait(pempty0 + 8 * b, ((it / kWBufs) & 1) ^ 1, abort_flag, p.status);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t a = smem_u32(ring + s * SB);
+            const uint64_t da = desc_kmajor(a), db = desc_kmajor(a + WM * BK);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if (turn > 0) {
-                --turn;
-                continue;
-              }
-              turn = kWMma - 1;
-              const int s = it % ST, b = (2 * it + h) % kWBufs;
-              ok = mbar_wait(full0 + 8 * s, (it / ST) & 1, abort_flag, p.status) &&
-                   wait_count(&sm.issued[b], it / 2, abort_flag, p.status) &&
-                   wait_for<CG>(pempty0 + 8 * b, ((it / 2) & 1) ^ 1, abort_flag, p.status);
-              if (!ok) break;
-              tc_fence_after();
-              const uint32_t a = smem_u32(ring + s * SB);
-              const uint64_t da = desc_kmajor(a), db = desc_kmajor(a + WM * BK + h * (WH / CG) * BK);
-#pragma unroll
-              for (int k = 0; k < BK / 32; ++k)
-                mma_f8<CG>(tmem + b * WH, da + 2 * k, db + 2 * k, idesc_f8(CG * WM, WH), k > 0 ? 1u : 0u);
-              commit<CG>(pfull0 + 8 * b);
-              commit<CG>(empty0 + 8 * s);
-              *(volatile int*)&sm.issued[b] = it / 2 + 1;
-            }
+            for (int k = 0; k < BK / 32; ++k)
+              mma_f8<CG>(tmem + b * WN, da + 2 * k, db + 2 * k, idesc_f8(CG * WM, WN), k > 0 ? 1u : 0u);
+            commit<CG>(pfull0 + 8 * b);
+            commit<CG>(empty0 + 8 * s);
           }
         }
         // nothing of this CTA's is in flight when its TMEM is given back
@@ -419,88 +475,61 @@ __global__ void __launch_bounds__(kWThreads, 1)
     }
   } else {
     // ----------------------------------------------------------------- epilogue
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWRegsEpi));
-    const int quad = warp & 3, half = (warp - 4) >> 2;
-    const int r = quad * 32 + lane, ht = threadIdx.x & 127;   // row of the tile; thread of this column half
-    const uint32_t tq = tmem + half * WH + ((uint32_t)(quad * 32) << 16);
-    const uint32_t back0 = (CG == 2 ? mapa_shared(pempty0, 0) : pempty0) + 8 * half;
-    int it = 0;
-    bool ok = true;   // after a failed wait: no more waiting or storing, every named barrier still reached
-    for (int L = first; L < units; L += step) {
-      uint64_t acc[WH / 2];    // pairs of neighbouring columns
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(w_regs_epi<CG>()));
+    const uint32_t tmem = tmem_base();
+    const int units = unit_count(), first = blockIdx.x / CG, step = gridDim.x / CG;
+    const int quad = warp & 3, part = (warp - 4) >> 2;
+    const int r = quad * 32 + lane;                           // row of the tile
+    const uint32_t tq = tmem + part * WC + ((uint32_t)(quad * 32) << 16);
+    const uint32_t back0 = CG == 2 ? mapa_shared(pempty0, 0) : pempty0;
+    int it = 0, ch = 0;
+    bool ok = true;   // after a failed wait: no more waiting or storing
+    for (int L = first; L < units && ok; L += step) {
+      uint64_t acc[WC / 2];    // pairs of neighbouring columns
 #pragma unroll
-      for (int i = 0; i < WH / 2; ++i) acc[i] = 0;
-      {
-        const WTile t = wide_tile<CG, WGRAD>(p, sm.seg, L, rank);
-        const int row = t.row0 + r, col0 = t.n0 + half * WH;
-        const bool valid = row < t.row_end;
-        const float *sa = p.sa, *sb = p.sb;
-        if (WGRAD) {
-          sa += (size_t)t.kb0 * p.M + (valid ? row : 0);
-          sb += (size_t)t.kb0 * p.N + min(col0 + ht, p.N - 1);
-        } else {
-          const int nb = (p.N + 127) / 128;
-          sa += (size_t)(valid ? row : 0) * p.nkb;
-          sb += ((size_t)t.g * nb + min(col0 / 128, nb - 1)) * p.nkb;
-        }
-        float na = 0.f, nsb = 0.f;
-        if (t.nkb > 0) {
-          na = __ldg(sa);
-          nsb = __ldg(sb);
-        }
-        for (int kb = t.nkb; kb > 0; --kb, ++it) {
-          const int par = it & 1;
-          float s = na;
-          if (WGRAD) {
-            sm.sb[par][threadIdx.x - 128] = nsb;
-            named_sync(1 + half, 128);
-          } else {
-            s *= nsb;
-          }
-          if (kb > 1) {
-            sa += WGRAD ? p.M : 1;
-            sb += WGRAD ? p.N : 1;
-            na = __ldg(sa);
-            nsb = __ldg(sb);
-          }
-          ok = __all_sync(0xffffffffu, ok && wait_for<CG>(pfull0 + 8 * (2 * par + half), (it >> 1) & 1, abort_flag, p.status));
-          if (ok) {
-            tc_fence_after();
-            // 64 columns at a time; the partial is given back before its last ones are added
-            uint32_t u[32], v[32];
-            const uint32_t tc = tq + par * 2 * WH;
-            const float* cs = &sm.sb[par][half * WH];
-            tmem_ld32(tc, u);
-            tmem_ld32(tc + 32, v);
-            tmem_ld_wait_for(u, v);
-            add_scaled<WGRAD>(acc, u, s, cs);
-            add_scaled<WGRAD>(acc + 16, v, s, cs + 32);
-            tmem_ld32(tc + 64, u);
-            tmem_ld32(tc + 96, v);
-            tmem_ld_wait_for(u, v);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              if (CG == 1) mbar_arrive(back0 + 16 * par);
-              else mbar_arrive_cluster(back0 + 16 * par);
+      for (int i = 0; i < WC / 2; ++i) acc[i] = 0;
+      for (int left = wide_tile<CG, WGRAD>(p, sm.seg, L, rank).nkb; left > 0 && ok; left -= kWChunk, ++ch) {
+        const int n = min(kWChunk, left);
+        if (!WGRAD) ok = warp_wait(sfull0 + 8 * (ch & 1), (ch >> 1) & 1, abort_flag, p.status);
+#pragma unroll 1
+        for (int k = 0; k < n && ok; ++k, ++it) {
+          const int b = it % kWBufs, slot = WGRAD ? it % (2 * kWChunk) : (ch & 1) * kWChunk + k;
+          ok = warp_wait(pfull0 + 8 * b, (it / kWBufs) & 1, abort_flag, p.status);
+          if (!ok) break;
+          const float* cs = &sm.sb[slot][WGRAD ? part * WC : part * WC / 128];
+          const float s = WGRAD ? sm.sa[slot][r] : sm.sa[slot][r] * *cs;
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < WC; c += 16) {
+            uint32_t u[16];
+            tmem_ld16(tq + b * WN + c, u);
+            tmem_ld_wait_for(u);
+            if (c == WC - 16) {   // the partial is read: its MMAs may have it again
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) {
+                if (CG == 1) mbar_arrive(back0 + 8 * b);
+                else arrive_remote(back0 + 8 * b);
+              }
             }
-            add_scaled<WGRAD>(acc + 32, u, s, cs + 64);
-            add_scaled<WGRAD>(acc + 48, v, s, cs + 96);
+            add_scaled<WGRAD>(acc + c / 2, u, s, cs + c);
           }
         }
+        __syncwarp();
+        if (!WGRAD && lane == 0) mbar_arrive(sempty0 + 8 * (ch & 1));
       }
       const WTile t = wide_tile<CG, WGRAD>(p, sm.seg, L, rank);
-      const int row = t.row0 + r, col0 = t.n0 + half * WH;
+      const int row = t.row0 + r, col0 = t.n0 + part * WC;
       if (ok && row < t.row_end) {
-      O* out = (O*)p.c + ((WGRAD ? (size_t)t.g * p.M : (size_t)0) + row) * p.N + col0;
-      const int cols = min(WH, p.N - col0);
+        O* out = (O*)p.c + ((WGRAD ? (size_t)t.g * p.M : (size_t)0) + row) * p.N + col0;
+        const int cols = min(WC, p.N - col0);
 #pragma unroll
-      for (int i = 0; i < WH; i += 16) {
-        float f[16];
+        for (int i = 0; i < WC; i += 16) {
+          float f[16];
 #pragma unroll
-        for (int j = 0; j < 16; j += 2) unpair(acc[(i + j) / 2], f[j], f[j + 1]);
-        if (i < cols) store16(out + i, f, cols - i, p.vec);
-      }
+          for (int j = 0; j < 16; j += 2) unpair(acc[(i + j) / 2], f[j], f[j + 1]);
+          if (i < cols) store16(out + i, f, cols - i, p.vec);
+        }
       }
       __syncwarp();
     }
@@ -509,7 +538,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
   __syncthreads();
   if (CG == 2) cluster_sync();   // neither CTA leaves while the pair's MMAs or arrivals may touch it
   tc_fence_after();
-  if (warp == 1) tmem_free<CG, 512>(tmem);
+  if (warp == 1) tmem_free<CG, 512>(sm.tmem);
 }
 
 // ----------------------------------------------------------------- narrow
@@ -661,7 +690,7 @@ __global__ void __launch_bounds__(kNThreads)
       const int b = kb % kNBufs;
       const float s = nsb;
       if (kb + 1 < nkb) nsb = __ldg(sb + kb + 1);
-      ok = __all_sync(0xffffffffu, mbar_wait(pfull0 + 8 * b, (kb / kNBufs) & 1, abort_flag, p.status));
+      ok = warp_wait(pfull0 + 8 * b, (kb / kNBufs) & 1, abort_flag, p.status);
       if (!ok) break;
       tc_fence_after();
 #pragma unroll
@@ -722,6 +751,17 @@ static_assert(w_smem<1>() <= kMaxSmem && w_smem<2>() <= kMaxSmem && n_smem<64>(k
                   n_smem<32>(kNarrowMaxKb) <= kMaxSmem,
               "shared memory per CTA");
 
+// fp32 [rows][cols] (cols a multiple of 4), boxes of one row.
+bool make_scale_tmap(CUtensorMap* tm, const float* base, uint64_t cols, uint64_t rows, uint32_t box) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {cols, rows}, strides[1] = {4 * cols};
+  cuuint32_t boxes[2] = {box, 1}, estr[2] = {1, 1};
+  return fn(tm, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<float*>(base), dims, strides, boxes, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <typename K>
 cudaError_t set_smem(K kern) {
   return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
@@ -743,10 +783,10 @@ cudaError_t init_narrow() {
 }
 
 template <int CG, bool WGRAD, typename O>
-cudaError_t launch_wide(const moe_ops_s* o, const CUtensorMap& a, const CUtensorMap& b, const GemmParams& p,
-                        long long units, cudaStream_t s) {
+cudaError_t launch_wide(const moe_ops_s* o, const CUtensorMap* tm, const GemmParams& p, long long units,
+                        cudaStream_t s) {
   auto kern = fp8_wide_kernel<CG, WGRAD, O>;
-  if (CG == 1) return launch_pdl(kern, dim3((unsigned)(units < o->sms ? units : o->sms)), dim3(kWThreads), w_smem<CG>(), s, a, b, p);
+  if (CG == 1) return launch_pdl(kern, dim3((unsigned)(units < o->sms ? units : o->sms)), dim3(kWThreads), w_smem<CG>(), s, tm[0], tm[1], tm[2], tm[3], p);
   // as many pairs as run at once
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * (unsigned)(units < o->pairs ? units : o->pairs));
@@ -762,14 +802,14 @@ cudaError_t launch_wide(const moe_ops_s* o, const CUtensorMap& a, const CUtensor
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, a, b, p);
+  return cudaLaunchKernelEx(&cfg, kern, tm[0], tm[1], tm[2], tm[3], p);
 }
 template <bool WGRAD>
-cudaError_t pick_wide(const moe_ops_s* o, int cg, const CUtensorMap& a, const CUtensorMap& b, const GemmParams& p,
-                      long long units, bool fp32, cudaStream_t s) {
+cudaError_t pick_wide(const moe_ops_s* o, int cg, const CUtensorMap* tm, const GemmParams& p, long long units,
+                      bool fp32, cudaStream_t s) {
   if (cg == 1)
-    return fp32 ? launch_wide<1, WGRAD, float>(o, a, b, p, units, s) : launch_wide<1, WGRAD, bf16>(o, a, b, p, units, s);
-  return fp32 ? launch_wide<2, WGRAD, float>(o, a, b, p, units, s) : launch_wide<2, WGRAD, bf16>(o, a, b, p, units, s);
+    return fp32 ? launch_wide<1, WGRAD, float>(o, tm, p, units, s) : launch_wide<1, WGRAD, bf16>(o, tm, p, units, s);
+  return fp32 ? launch_wide<2, WGRAD, float>(o, tm, p, units, s) : launch_wide<2, WGRAD, bf16>(o, tm, p, units, s);
 }
 
 // Rows of a (and their scales) in the order of c's rows, one warp a row; an index out of range gives zeros.
@@ -906,11 +946,13 @@ cudaError_t fp8_matmul(const moe_ops_s* o, const void* a, const float* sa, int a
     p.a_rows = a_rows = M;
   }
   const int cg = ceil_div(M, G) > WM ? 2 : 1;
-  if (!make_tmap(&ta, a, K, a_rows, BK, WM, 1) || !make_tmap(&tb, b, K, (uint64_t)G * N, BK, cg == 2 ? WH / 2 : WN, 1))
+  CUtensorMap tm[4];
+  if (!make_tmap(&tm[0], a, K, a_rows, BK, WM, 1) || !make_tmap(&tm[1], b, K, (uint64_t)G * N, BK, WN / cg, 1))
     return cudaErrorInvalidValue;
+  tm[2] = tm[3] = tm[0];      // (not read)
   const long long units = ((long long)ceil_div(M, cg * WM) + (G > 1 ? G : 0)) * ceil_div(N, WN);
   *n += 1;
-  return pick_wide<false>(o, cg, ta, tb, p, units, out_fp32, s);
+  return pick_wide<false>(o, cg, tm, p, units, out_fp32, s);
 }
 
 cudaError_t fp8_wgrad(const moe_ops_s* o, const void* dct, const float* sdct, const void* xt, const float* sxt, int T,
@@ -927,12 +969,13 @@ cudaError_t fp8_wgrad(const moe_ops_s* o, const void* dct, const float* sdct, co
   p.c = c;
   p.status = o->status;
   const int Tp = quant_cols_rows(T, G), cg = N > WM ? 2 : 1;
-  CUtensorMap ta, tb;
-  if (!make_tmap(&ta, dct, Tp, N, BK, WM, 1) || !make_tmap(&tb, xt, Tp, K, BK, cg == 2 ? WH / 2 : WN, 1))
+  CUtensorMap tm[4];
+  if (!make_tmap(&tm[0], dct, Tp, N, BK, WM, 1) || !make_tmap(&tm[1], xt, Tp, K, BK, WN / cg, 1) ||
+      !make_scale_tmap(&tm[2], sdct, N, Tp / BK, WM) || !make_scale_tmap(&tm[3], sxt, K, Tp / BK, WN))
     return cudaErrorInvalidValue;
   const long long units = (long long)G * ceil_div(N, cg * WM) * ceil_div(K, WN);
   *n += 1;
-  return pick_wide<true>(o, cg, ta, tb, p, units, out_fp32, s);
+  return pick_wide<true>(o, cg, tm, p, units, out_fp32, s);
 }
 
 }  // namespace moe

@@ -266,7 +266,9 @@ moe_status moe_fp8_wgrad(moe_ops ops, const void* dct, const float* dct_scale, c
   CHECK(off || G == 1, MOE_ERR_INVALID_ARG);
   CHECK(out_dtype == MOE_BF16 || out_dtype == MOE_FP32, MOE_ERR_INVALID_ARG);
   CHECK(G <= kMaxSegs && T <= (1 << 22) && N < (1 << 28) && K < (1 << 28), MOE_ERR_UNSUPPORTED);
-  CHECK(aligned(dct, 16) && aligned(xt, 16) && aligned(c, 16), MOE_ERR_UNSUPPORTED);
+  CHECK(N % 8 == 0 && K % 8 == 0 && aligned(dct, 16) && aligned(xt, 16) && aligned(dct_scale, 16) &&
+            aligned(xt_scale, 16) && aligned(c, 16),
+        MOE_ERR_UNSUPPORTED);
   CHECK(T == 0 || (dct && dct_scale && xt && xt_scale), MOE_ERR_INVALID_ARG);
   HANDLE(ops);
   if (T == 0) {

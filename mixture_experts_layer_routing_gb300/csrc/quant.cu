@@ -36,15 +36,18 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const bf16* __restrict_
   }
 }
 
-// CTA per 128 tokens x 64 columns: rows are read 128 bytes wide into shared memory, then each thread takes a quarter
-// (32 tokens) of one column and writes its 32 codes, so a column's 128 codes leave as one 128-byte line.
+// CTA per 128 tokens and a run of 64-column blocks: rows are read 128 bytes wide into shared memory, then each thread
+// takes a quarter (32 tokens) of one column and writes its 32 codes, so a column's 128 codes leave as one 128-byte
+// line. The next block's rows are on their way meanwhile; segments and row indexes are looked up once a CTA (a CTA
+// for every block spent most of its time on that: 12,288 x 2,816 gathered rows took 51 us).
+constexpr int kColBlocks = 11;       // column blocks of a CTA
 __global__ void __launch_bounds__(256) quant_cols_kernel(const bf16* __restrict__ src, long long ld, int src_rows,
                                                          int T, int C, const int* __restrict__ off, int G,
                                                          const int* __restrict__ row_index, uint8_t* __restrict__ q,
                                                          float* __restrict__ scale, long long Tp, int* status) {
   __shared__ SegSmem seg;
-  __shared__ uint4 tile4[128][8];      // [token][64 columns]
-  __shared__ float red[4][64];
+  __shared__ uint4 tile4[2][128][8];      // [block parity][token][64 columns]
+  __shared__ float red[2][4][64];
   griddep_wait();
   griddep_launch();
   load_segments(seg, off, G, T, kScaleBlock, status);
@@ -52,41 +55,53 @@ __global__ void __launch_bounds__(256) quant_cols_kernel(const bf16* __restrict_
   if (t >= seg.tile[G]) return;
   const int g = segment_of(seg, G, t);
   const int row0 = seg.off[g] + (t - seg.tile[g]) * kScaleBlock, row1 = seg.off[g + 1];
-  const int tid = threadIdx.x, c0 = blockIdx.x * 64;
+  const int tid = threadIdx.x;
+  const bf16* rows[4];                 // this thread's rows (null: zeros)
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int r = i * 32 + (tid >> 3), c = c0 + (tid & 7) * 8;
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (row0 + r < row1 && c < C) {
+    const int r = i * 32 + (tid >> 3);
+    rows[i] = nullptr;
+    if (row0 + r < row1) {
       int s = row0 + r;
       if (row_index) s = row_index[s];
-      if ((unsigned)s < (unsigned)src_rows) {
-        v = *reinterpret_cast<const uint4*>(src + s * ld + c);
-      } else {
-        set_error(status, MOE_ERR_DEVICE_INDEX);
-      }
+      if ((unsigned)s < (unsigned)src_rows) rows[i] = src + s * ld + (tid & 7) * 8;
+      else set_error(status, MOE_ERR_DEVICE_INDEX);
     }
-    tile4[r][tid & 7] = v;
   }
-  __syncthreads();
-  const int col = tid & 63, part = tid >> 6;
-  const bf16* column = reinterpret_cast<const bf16*>(&tile4[0][0]) + part * 32 * 64 + col;
-  float v[32], m = 0.f;
+  const int c_end = min(C, (int)(blockIdx.x + 1) * kColBlocks * 64);
+  uint4 v4[4];
+  const auto fetch = [&](int c0) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    v[i] = to_f(column[i * 64]);
-    m = max_nan(m, fabsf(v[i]));
+    for (int i = 0; i < 4; ++i)
+      v4[i] = rows[i] && c0 + (tid & 7) * 8 < c_end ? *reinterpret_cast<const uint4*>(rows[i] + c0) : make_uint4(0u, 0u, 0u, 0u);
+  };
+  const int col = tid & 63, part = tid >> 6;
+  int b = 0;
+  fetch(blockIdx.x * kColBlocks * 64);
+  for (int c0 = blockIdx.x * kColBlocks * 64; c0 < c_end; c0 += 64, b ^= 1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) tile4[b][i * 32 + (tid >> 3)][tid & 7] = v4[i];
+    __syncthreads();
+    if (c0 + 64 < c_end) fetch(c0 + 64);
+    const bf16* column = reinterpret_cast<const bf16*>(&tile4[b][0][0]) + part * 32 * 64 + col;
+    float v[32], m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      v[i] = to_f(column[i * 64]);
+      m = max_nan(m, fabsf(v[i]));
+    }
+    red[b][part][col] = m;
+    __syncthreads();
+    m = max_nan(max_nan(red[b][0][col], red[b][1][col]), max_nan(red[b][2][col], red[b][3][col]));
+    if (c0 + col < c_end) {
+      uint32_t w[8];
+      codes<32>(v, m, w);
+      uint4* dst = reinterpret_cast<uint4*>(q + (long long)(c0 + col) * Tp + (long long)t * kScaleBlock + part * 32);
+      dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      if (part == 0) scale[(long long)t * C + c0 + col] = block_scale(m);
+    }
   }
-  red[part][col] = m;
-  __syncthreads();
-  m = max_nan(max_nan(red[0][col], red[1][col]), max_nan(red[2][col], red[3][col]));
-  if (c0 + col >= C) return;
-  uint32_t w[8];
-  codes<32>(v, m, w);
-  uint4* dst = reinterpret_cast<uint4*>(q + (long long)(c0 + col) * Tp + (long long)t * kScaleBlock + part * 32);
-  dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-  dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-  if (part == 0) scale[(long long)t * C + c0 + col] = block_scale(m);
 }
 
 // CTA per 128 x 128 block of one matrix.
@@ -165,7 +180,7 @@ cudaError_t quant_cols(const moe_ops_s* o, const void* src, long long ld, int sr
                        int G, const int* row_index, void* q, float* scale, cudaStream_t s, long long* n) {
   const int Tp = quant_cols_rows(T, G);
   *n += 1;
-  return launch_pdl(quant_cols_kernel, dim3(ceil_div(C, 64), Tp / kScaleBlock), dim3(256), 0, s, (const bf16*)src, ld,
+  return launch_pdl(quant_cols_kernel, dim3(ceil_div(C, 64 * kColBlocks), Tp / kScaleBlock), dim3(256), 0, s, (const bf16*)src, ld,
                     src_rows, T, C, off, G, row_index, (uint8_t*)q, scale, (long long)Tp, o->status);
 }
 

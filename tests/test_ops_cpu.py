@@ -127,7 +127,7 @@ WG = dict(ops=P, dct=P, sd=P, xt=P, sx=P, T=64, off=None, G=1, N=128, K=256, c=P
 @pytest.mark.parametrize("over,code", [
     (dict(ops=None), ARG), (dict(T=-1), ARG), (dict(c=None), ARG), (dict(dct=None), ARG), (dict(sx=None), ARG),
     (dict(G=3), ARG), (dict(G=300, off=P), UNSUP), (dict(T=(1 << 22) + 1), UNSUP), (dict(xt=P + 4), UNSUP),
-    (dict(out=5), ARG),
+    (dict(out=5), ARG), (dict(N=132), UNSUP), (dict(K=252), UNSUP), (dict(sd=P + 4), UNSUP),
 ])
 def test_wgrad_refuses(lib, over, code):
     assert call(lib, "moe_fp8_wgrad", WG, over) == code
