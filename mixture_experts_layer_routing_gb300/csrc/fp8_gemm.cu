@@ -137,6 +137,18 @@ __device__ __forceinline__ bool spin_wait(uint32_t bar, uint32_t parity, volatil
 __device__ __forceinline__ void arrive_remote(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
+// n / d for n < 2^31 by a multiplication (Granlund and Montgomery, PLDI 1994). A unit's place takes several divisions,
+// which cost a warp some 500 cycles as divisions.
+struct FastDiv {
+  unsigned d, mul, shift;
+  FastDiv() = default;
+  explicit FastDiv(unsigned by) : d(by), mul(0), shift(0) {
+    while ((1ull << shift) < d) ++shift;
+    mul = (unsigned)(((1ull << 32) * ((1ull << shift) - d)) / d + 1);
+  }
+  __device__ __forceinline__ unsigned div(unsigned n) const { return (__umulhi(n, mul) + n) >> shift; }
+};
+
 struct GemmParams {
   const float* sa;        // scales of the rows: [a_rows][nkb], or (wgrad) [K blocks][M]
   const float* sb;        // of the columns: [G][ceil(N / 128)][nkb], or (wgrad) [K blocks][N]
@@ -149,6 +161,8 @@ struct GemmParams {
   int N;
   int nkb;                // K blocks (wgrad: from the segment)
   int vec;                // widest aligned store to c: 32 or 16 bytes, or 0
+  FastDiv nt, mnt, rnt;   // wide: column tiles; (wgrad) tiles of a segment; tiles of a group of kRasterM row tiles
+  FastDiv last;           // (wgrad) row tiles of a segment's last such group
   void* c;
   int* status;
 };
@@ -184,20 +198,18 @@ __device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&u)[16]) {
                :
                : "memory");
 }
-// acc += u s (columns' scales v too, where they differ) for 16 columns.
+// Scales of 16 columns as pairs: the row's s, times the columns' own v where they differ.
 template <bool COLS>
-__device__ __forceinline__ void add_scaled(uint64_t* acc, const uint32_t (&u)[16], float s, const float* v) {
+__device__ __forceinline__ void pair_scales(uint64_t (&w)[8], float s, const float* v) {
   const uint64_t s2 = pair(s, s);
 #pragma unroll
-  for (int i = 0; i < 16; i += 4) {
-    uint64_t a = s2, b = s2;
+  for (int i = 0; i < 8; i += 2) {
+    w[i] = w[i + 1] = s2;
     if (COLS) {
-      const float4 f = *reinterpret_cast<const float4*>(v + i);
-      a = mul2(s2, pair(f.x, f.y));
-      b = mul2(s2, pair(f.z, f.w));
+      const float4 f = *reinterpret_cast<const float4*>(v + 2 * i);
+      w[i] = mul2(s2, pair(f.x, f.y));
+      w[i + 1] = mul2(s2, pair(f.z, f.w));
     }
-    fma2(acc[i / 2], pair(__uint_as_float(u[i]), __uint_as_float(u[i + 1])), a);
-    fma2(acc[i / 2 + 1], pair(__uint_as_float(u[i + 2]), __uint_as_float(u[i + 3])), b);
   }
 }
 
@@ -252,22 +264,30 @@ constexpr int kWThreads = (4 + kWEpi) * 32;            // producer, MMA warps, s
 constexpr int kWChunk = 8;                             // K blocks whose scales are fetched at a time
 // CG CTAs work on one tile of CG x 128 rows; each holds its own rows and 1 / CG of the columns' operand.
 template <int CG> constexpr int w_stage_bytes() { return (WM + WN / CG) * BK; }
-template <int CG> constexpr int w_stages() { return CG == 1 ? 4 : 6; }
+template <int CG> constexpr int w_stages() { return 4; }
 struct alignas(128) WideSmem {
-  // Scales of 16 K blocks, slot it mod 16: of this CTA's rows, and of the columns (wgrad; else entries 0 and 1, the
-  // halves'). wgrad's come by TMA with the operands, the others by a warp of their own, 8 K blocks at a time.
-  float sa[2 * kWChunk][WM], sb[2 * kWChunk][WN];
+  // Scales of the K blocks: of this CTA's rows, and of the columns. wgrad's come by TMA with the operands (slot it mod
+  // 8, a scale for each column), the others by a warp of their own, in two chunks of 8 K blocks (a scale for each
+  // half of the columns: sbh).
+  float sa[2 * kWChunk][WM], sb[kWChunk][WN], sbh[2 * kWChunk][2];
   SegSmem seg;
   uint64_t full[6], empty[6], pfull[kWBufs], pempty[kWBufs], sfull[2], sempty[2], drain;
   uint32_t tmem;
   int abort;
 };
-template <int CG> constexpr int w_smem() { return w_stages<CG>() * w_stage_bytes<CG>() + 1024 + (int)sizeof(WideSmem); }
+// Output staging of a pair's CTA: each epilogue warp writes 32 rows x 128 bytes at a time (128-byte swizzle) and sends
+// them by TMA. Rows stored directly, a row a lane, took 32 wavefronts an instruction and bound the weight gradients
+// (89% of L1's throughput); single CTAs have no room for it.
+constexpr int kWOutBufs = 2, kWOutBytes = 32 * 128;
+template <int CG> constexpr int w_out_bytes() { return CG == 1 ? 0 : kWEpi * kWOutBufs * kWOutBytes; }
+template <int CG> constexpr int w_smem() {
+  return w_stages<CG>() * w_stage_bytes<CG>() + w_out_bytes<CG>() + 1024 + (int)sizeof(WideSmem);
+}
 // Registers: 384 threads are launched with 168 each, of which the epilogue's 256 take more and the other 128 give up
 // some: the split at which neither side spills (a spill of eight registers in the loop cost 20% of the time).
 constexpr int kWRegs = 168;
-template <int CG> constexpr int w_regs_epi() { return CG == 1 ? 216 : 224; }
-template <int CG> constexpr int w_regs_rest() { return CG == 1 ? 72 : 56; }
+template <int CG> constexpr int w_regs_epi() { return 208; }
+template <int CG> constexpr int w_regs_rest() { return 88; }
 template <int CG> constexpr bool w_regs_fit() {
   return kWEpi * 32 * w_regs_epi<CG>() + 128 * w_regs_rest<CG>() <= kWThreads * kWRegs;
 }
@@ -282,27 +302,26 @@ struct WTile {
 template <int CG, bool WGRAD>
 __device__ __forceinline__ WTile wide_tile(const GemmParams& p, const SegSmem& s, int L, int rank) {
   constexpr int TM = CG * WM;
-  const int nt = (p.N + WN - 1) / WN;
   WTile t;
   int mt, local;
   if (WGRAD) {
+    t.g = p.mnt.div(L);
+    local = L - t.g * p.mnt.d;
     mt = (p.M + TM - 1) / TM;
-    t.g = L / (mt * nt);
-    local = L - t.g * mt * nt;
   } else {
     int lo = 0, hi = p.G;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (s.tile[mid] * nt <= L) lo = mid; else hi = mid;
+      if (s.tile[mid] * (int)p.nt.d <= L) lo = mid; else hi = mid;
     }
     t.g = lo;
     mt = s.tile[lo + 1] - s.tile[lo];
-    local = L - s.tile[lo] * nt;
+    local = L - s.tile[lo] * p.nt.d;
   }
-  const int grp = local / (kRasterM * nt), gm = min(kRasterM, mt - grp * kRasterM);
-  const int within = local - grp * kRasterM * nt;
-  const int m = grp * kRasterM + within % gm;
-  t.n0 = within / gm * WN;
+  const int grp = p.rnt.div(local), within = local - grp * p.rnt.d, gm = mt - grp * kRasterM;
+  const int n = gm >= kRasterM ? within / kRasterM : WGRAD ? (int)p.last.div(within) : within / gm;
+  const int m = grp * kRasterM + within - n * min(gm, kRasterM);
+  t.n0 = n * WN;
   if (WGRAD) {
     t.row0 = m * TM + rank * WM;
     t.row_end = p.M;
@@ -335,14 +354,16 @@ __device__ __forceinline__ int wide_units(const GemmParams& p, const SegSmem& s)
 template <int CG, bool WGRAD, typename O>
 __global__ void __launch_bounds__(kWThreads, 1)
     fp8_wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                    const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB, GemmParams p) {
+                    const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
+                    const __grid_constant__ CUtensorMap tmC, GemmParams p) {
   constexpr int ST = w_stages<CG>(), SB = w_stage_bytes<CG>();
   // wgrad's slots: the copies of K block i follow the MMAs of i - ST, which follow the epilogue's release of
-  // i - ST - 2, so they cannot meet the reading of i - 16.
-  static_assert(ST + 3 <= 2 * kWChunk, "scale slots");
+  // i - ST - 2, so they cannot meet the reading of i - 8.
+  static_assert(ST + 3 <= kWChunk, "scale slots");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  WideSmem& sm = *reinterpret_cast<WideSmem*>(ring + ST * SB);
+  uint8_t* staging = ring + ST * SB;
+  WideSmem& sm = *reinterpret_cast<WideSmem*>(staging + w_out_bytes<CG>());
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = CG == 2 ? (int)cluster_ctarank() : 0;
   volatile int* abort_flag = &sm.abort;
@@ -404,8 +425,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
           load(b, &tmB, k, brow);          // (a pair: this CTA's half of the columns)
           load(a, &tmA, k, t.row0);
           if (WGRAD) {
-            load(smem_u32(sm.sa[it % (2 * kWChunk)]), &tmSA, t.row0, t.kb0 + kb);
-            load(smem_u32(sm.sb[it % (2 * kWChunk)]), &tmSB, t.n0, t.kb0 + kb);
+            load(smem_u32(sm.sa[it % kWChunk]), &tmSA, t.row0, t.kb0 + kb);
+            load(smem_u32(sm.sb[it % kWChunk]), &tmSB, t.n0, t.kb0 + kb);
           }
         }
       }
@@ -437,7 +458,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
           }
           if (lane < 2 * kWChunk) {
             const int h = lane / kWChunk, k = lane % kWChunk;
-            if (k < n) sm.sb[j + k][h] = __ldg(p.sb + ((size_t)t.g * nb + min(t.n0 / 128 + h, nb - 1)) * p.nkb + k0 + k);
+            if (k < n) sm.sbh[j + k][h] = __ldg(p.sb + ((size_t)t.g * nb + min(t.n0 / 128 + h, nb - 1)) * p.nkb + k0 + k);
           }
           mbar_arrive(sfull0 + 8 * (ch & 1));
         }
@@ -493,17 +514,20 @@ __global__ void __launch_bounds__(kWThreads, 1)
         if (!WGRAD) ok = warp_wait(sfull0 + 8 * (ch & 1), (ch >> 1) & 1, abort_flag, p.status);
 #pragma unroll 1
         for (int k = 0; k < n && ok; ++k, ++it) {
-          const int b = it % kWBufs, slot = WGRAD ? it % (2 * kWChunk) : (ch & 1) * kWChunk + k;
+          const int b = it % kWBufs, slot = WGRAD ? it % kWChunk : (ch & 1) * kWChunk + k;
           ok = warp_wait(pfull0 + 8 * b, (it / kWBufs) & 1, abort_flag, p.status);
           if (!ok) break;
-          const float* cs = &sm.sb[slot][WGRAD ? part * WC : part * WC / 128];
-          const float s = WGRAD ? sm.sa[slot][r] : sm.sa[slot][r] * *cs;
+          const float* cs = &sm.sb[WGRAD ? slot : 0][part * WC];
+          const float s = WGRAD ? sm.sa[slot][r] : sm.sa[slot][r] * sm.sbh[slot][part * WC / 128];
           tc_fence_after();
 #pragma unroll
           for (int c = 0; c < WC; c += 16) {
             uint32_t u[16];
+            uint64_t w[8];
             tmem_ld16(tq + b * WN + c, u);
+            if (WGRAD) pair_scales<true>(w, s, cs + c);   // while they come
             tmem_ld_wait_for(u);
+            if (!WGRAD) pair_scales<false>(w, s, cs);
             if (c == WC - 16) {   // the partial is read: its MMAs may have it again
               tc_fence_before();
               __syncwarp();
@@ -512,7 +536,9 @@ __global__ void __launch_bounds__(kWThreads, 1)
                 else arrive_remote(back0 + 8 * b);
               }
             }
-            add_scaled<WGRAD>(acc + c / 2, u, s, cs + c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              fma2(acc[c / 2 + i], pair(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])), w[i]);
           }
         }
         __syncwarp();
@@ -520,7 +546,41 @@ __global__ void __launch_bounds__(kWThreads, 1)
       }
       const WTile t = wide_tile<CG, WGRAD>(p, sm.seg, L, rank);
       const int row = t.row0 + r, col0 = t.n0 + part * WC;
-      if (ok && row < t.row_end) {
+      // by TMA where it cannot reach rows of another segment (its map ends with c's rows, wgrad's with a segment's)
+      if (CG == 2 && ok && p.vec && (WGRAD || t.row0 + quad * 32 + 32 <= t.row_end)) {
+        constexpr int SC = 128 / sizeof(O);      // columns of a piece
+        uint8_t* buf = staging + (warp - 4) * kWOutBufs * kWOutBytes;
+#pragma unroll
+        for (int i0 = 0; i0 < WC; i0 += kWOutBufs * SC) {
+          if (col0 + i0 >= p.N || t.row0 + quad * 32 >= t.row_end) break;
+          if (lane == 0) bulk_wait_read<0>();    // what was sent from here before
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < kWOutBufs * SC; i += SC) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {        // 16 bytes each
+              float f[8];
+#pragma unroll
+              for (int q = 0; q < 16 / (int)sizeof(O); q += 2)
+                unpair(acc[(i0 + i + j * (SC / 8) + q) / 2], f[q], f[q + 1]);
+              uint4 w;
+              if (sizeof(O) == 4) w = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+              else w = pack8(f);
+              *reinterpret_cast<uint4*>(buf + i / SC * kWOutBytes + lane * 128 + ((j ^ (lane & 7)) << 4)) = w;
+            }
+          }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) {
+#pragma unroll
+            for (int i = 0; i < kWOutBufs * SC; i += SC)
+              if (col0 + i0 + i < p.N)
+                tma_store_3d_hint(&tmC, col0 + i0 + i, t.row0 + quad * 32, WGRAD ? t.g : 0,
+                                  smem_u32(buf + i / SC * kWOutBytes), policy_evict_first());
+            bulk_commit();
+          }
+        }
+      } else if (ok && row < t.row_end) {
         O* out = (O*)p.c + ((WGRAD ? (size_t)t.g * p.M : (size_t)0) + row) * p.N + col0;
         const int cols = min(WC, p.N - col0);
 #pragma unroll
@@ -533,6 +593,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
       }
       __syncwarp();
     }
+    if (CG == 2 && lane == 0) bulk_wait<0>();
   }
   tc_fence_before();
   __syncthreads();
@@ -762,6 +823,18 @@ bool make_scale_tmap(CUtensorMap* tm, const float* base, uint64_t cols, uint64_t
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// c [G][rows][cols] for stores of 32 rows x 128 bytes.
+bool make_out_tmap(CUtensorMap* tm, void* c, uint64_t cols, uint64_t rows, uint64_t G, int fp32) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const uint64_t e = fp32 ? 4 : 2;
+  cuuint64_t dims[3] = {cols, rows, G}, strides[2] = {cols * e, cols * rows * e};
+  cuuint32_t box[3] = {(cuuint32_t)(128 / e), 32, 1}, estr[3] = {1, 1, 1};
+  return fn(tm, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, c, dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <typename K>
 cudaError_t set_smem(K kern) {
   return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
@@ -786,7 +859,7 @@ template <int CG, bool WGRAD, typename O>
 cudaError_t launch_wide(const moe_ops_s* o, const CUtensorMap* tm, const GemmParams& p, long long units,
                         cudaStream_t s) {
   auto kern = fp8_wide_kernel<CG, WGRAD, O>;
-  if (CG == 1) return launch_pdl(kern, dim3((unsigned)(units < o->sms ? units : o->sms)), dim3(kWThreads), w_smem<CG>(), s, tm[0], tm[1], tm[2], tm[3], p);
+  if (CG == 1) return launch_pdl(kern, dim3((unsigned)(units < o->sms ? units : o->sms)), dim3(kWThreads), w_smem<CG>(), s, tm[0], tm[1], tm[2], tm[3], tm[4], p);
   // as many pairs as run at once
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * (unsigned)(units < o->pairs ? units : o->pairs));
@@ -802,11 +875,16 @@ cudaError_t launch_wide(const moe_ops_s* o, const CUtensorMap* tm, const GemmPar
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, tm[0], tm[1], tm[2], tm[3], p);
+  return cudaLaunchKernelEx(&cfg, kern, tm[0], tm[1], tm[2], tm[3], tm[4], p);
 }
 template <bool WGRAD>
-cudaError_t pick_wide(const moe_ops_s* o, int cg, const CUtensorMap* tm, const GemmParams& p, long long units,
-                      bool fp32, cudaStream_t s) {
+cudaError_t pick_wide(const moe_ops_s* o, int cg, const CUtensorMap* tm, GemmParams p, long long units, bool fp32,
+                      cudaStream_t s) {
+  const int nt = ceil_div(p.N, WN), mt = WGRAD ? ceil_div(p.M, cg * WM) : 1;
+  p.nt = FastDiv(nt);
+  p.mnt = FastDiv(mt * nt);
+  p.rnt = FastDiv(kRasterM * nt);
+  p.last = FastDiv(mt % kRasterM ? mt % kRasterM : kRasterM);
   if (cg == 1)
     return fp32 ? launch_wide<1, WGRAD, float>(o, tm, p, units, s) : launch_wide<1, WGRAD, bf16>(o, tm, p, units, s);
   return fp32 ? launch_wide<2, WGRAD, float>(o, tm, p, units, s) : launch_wide<2, WGRAD, bf16>(o, tm, p, units, s);
@@ -946,10 +1024,11 @@ cudaError_t fp8_matmul(const moe_ops_s* o, const void* a, const float* sa, int a
     p.a_rows = a_rows = M;
   }
   const int cg = ceil_div(M, G) > WM ? 2 : 1;
-  CUtensorMap tm[4];
+  CUtensorMap tm[5];
   if (!make_tmap(&tm[0], a, K, a_rows, BK, WM, 1) || !make_tmap(&tm[1], b, K, (uint64_t)G * N, BK, WN / cg, 1))
     return cudaErrorInvalidValue;
-  tm[2] = tm[3] = tm[0];      // (not read)
+  tm[2] = tm[3] = tm[4] = tm[0];      // (not read where they are not made)
+  if (cg == 2 && p.vec && !make_out_tmap(&tm[4], c, N, M, 1, out_fp32)) return cudaErrorInvalidValue;
   const long long units = ((long long)ceil_div(M, cg * WM) + (G > 1 ? G : 0)) * ceil_div(N, WN);
   *n += 1;
   return pick_wide<false>(o, cg, tm, p, units, out_fp32, s);
@@ -969,10 +1048,12 @@ cudaError_t fp8_wgrad(const moe_ops_s* o, const void* dct, const float* sdct, co
   p.c = c;
   p.status = o->status;
   const int Tp = quant_cols_rows(T, G), cg = N > WM ? 2 : 1;
-  CUtensorMap tm[4];
+  CUtensorMap tm[5];
   if (!make_tmap(&tm[0], dct, Tp, N, BK, WM, 1) || !make_tmap(&tm[1], xt, Tp, K, BK, WN / cg, 1) ||
       !make_scale_tmap(&tm[2], sdct, N, Tp / BK, WM) || !make_scale_tmap(&tm[3], sxt, K, Tp / BK, WN))
     return cudaErrorInvalidValue;
+  tm[4] = tm[0];
+  if (cg == 2 && p.vec && !make_out_tmap(&tm[4], c, K, N, G, out_fp32)) return cudaErrorInvalidValue;
   const long long units = (long long)G * ceil_div(N, cg * WM) * ceil_div(K, WN);
   *n += 1;
   return pick_wide<true>(o, cg, tm, p, units, out_fp32, s);

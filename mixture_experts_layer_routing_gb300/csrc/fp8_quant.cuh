@@ -65,6 +65,33 @@ __device__ __forceinline__ uint2 codes8(const float* v, float m) {
   codes<8>(v, m, w);
   return make_uint2(w[0], w[1]);
 }
+// Pairs of fp32 values, for the two-wide operations.
+__device__ __forceinline__ uint64_t f32x2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void f32x2_get(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t f32x2_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f32x2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// Two values over two divisors' m and r at once (Divisor::code; -m in neg_m).
+__device__ __forceinline__ uint64_t code2(uint64_t v, uint64_t r, uint64_t neg_m) {
+  const uint64_t a = f32x2_mul(v, f32x2(kE4m3Max, kE4m3Max)), q = f32x2_mul(a, r);
+  return f32x2_fma(f32x2_fma(q, neg_m, a), r, q);
+}
+// The larger magnitudes of bf16 pairs: without their signs they compare as integers, and a NaN is above all others.
+__device__ __forceinline__ uint32_t bf16x2_amax(uint32_t m, uint32_t w) { return __vmaxu2(m, w & 0x7fff7fffu); }
+
 // Largest of the 16 lanes that hold a block (8 values each).
 __device__ __forceinline__ float half_warp_max(float m) {
 #pragma unroll

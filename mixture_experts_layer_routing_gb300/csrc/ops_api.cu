@@ -199,7 +199,7 @@ moe_status moe_quant_rows(moe_ops ops, const void* src, long long ld, int T, int
   CHECK(src && q && scale, MOE_ERR_INVALID_ARG);
   CHECK(T >= 0 && C >= 1 && ld >= (swiglu ? 2ll : 1ll) * C, MOE_ERR_INVALID_ARG);
   CHECK(C % 8 == 0 && ld % 8 == 0 && aligned(src, 16) && aligned(q, 8), MOE_ERR_UNSUPPORTED);
-  CHECK((long long)T * ceil_div(C, kScaleBlock) < (1ll << 34), MOE_ERR_UNSUPPORTED);
+  CHECK((long long)T * ceil_div(C, kScaleBlock) < (1ll << 31), MOE_ERR_UNSUPPORTED);
   HANDLE(ops);
   DONE(quant_rows(ops, src, ld, T, C, swiglu, q, scale, (cudaStream_t)stream, &n_));
 }
@@ -249,6 +249,7 @@ moe_status moe_fp8_matmul(moe_ops ops, const void* a, const float* a_scale, int 
   CHECK(out_dtype == MOE_BF16 || out_dtype == MOE_FP32, MOE_ERR_INVALID_ARG);
   CHECK(G <= kMaxSegs && K % 16 == 0, MOE_ERR_UNSUPPORTED);
   CHECK(M < (1 << 30) && (long long)G * N < (1ll << 31) && N < (1 << 28) && K < (1 << 28), MOE_ERR_UNSUPPORTED);
+  CHECK((ceil_div(M, 128) + (long long)G) * ceil_div(N, 128) < (1ll << 27), MOE_ERR_UNSUPPORTED);   // tiles
   if (M == 0) return MOE_OK;
   CHECK(a && a_scale && a_rows >= 1 && b && b_scale && c, MOE_ERR_INVALID_ARG);
   CHECK(aligned(a, 16) && aligned(b, 16) && aligned(c, 16) && aligned(a_scale, 4) && aligned(b_scale, 4),
@@ -269,6 +270,7 @@ moe_status moe_fp8_wgrad(moe_ops ops, const void* dct, const float* dct_scale, c
   CHECK(N % 8 == 0 && K % 8 == 0 && aligned(dct, 16) && aligned(xt, 16) && aligned(dct_scale, 16) &&
             aligned(xt_scale, 16) && aligned(c, 16),
         MOE_ERR_UNSUPPORTED);
+  CHECK((long long)ceil_div(N, 128) * ceil_div(K, 128) < (1ll << 27) / G, MOE_ERR_UNSUPPORTED);
   CHECK(T == 0 || (dct && dct_scale && xt && xt_scale), MOE_ERR_INVALID_ARG);
   HANDLE(ops);
   if (T == 0) {

@@ -8,26 +8,23 @@
 namespace moe {
 namespace {
 
-// Half a warp a block: item i is block i % nb of row i / nb.
-template <bool SWIGLU>
-__global__ void __launch_bounds__(256) quant_rows_kernel(const bf16* __restrict__ src, long long ld, long long items,
-                                                         int nb, int C, uint8_t* __restrict__ q,
-                                                         float* __restrict__ scale) {
+// SwiGLU, half a warp a block: item i is block i % nb of row i / nb.
+__global__ void __launch_bounds__(256) quant_swiglu_kernel(const bf16* __restrict__ src, long long ld, unsigned items,
+                                                           int nb, int C, uint8_t* __restrict__ q,
+                                                           float* __restrict__ scale) {
   griddep_wait();
   griddep_launch();
-  const long long i = (long long)blockIdx.x * 16 + (threadIdx.x >> 4);
-  const long long row = i / nb;
-  const int b = (int)(i - row * nb), c = b * kScaleBlock + (threadIdx.x & 15) * 8;
+  const unsigned i = blockIdx.x * 16 + (threadIdx.x >> 4), r = i / (unsigned)nb;
+  const long long row = r;
+  const int c = (int)(i - r * nb) * kScaleBlock + (threadIdx.x & 15) * 8;
   const bool in = i < items && c < C;
   float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   if (in) {
+    float u[8];
     load8(src + row * ld + c, v);
-    if (SWIGLU) {
-      float u[8];
-      load8(src + row * ld + C + c, u);
+    load8(src + row * ld + C + c, u);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = silu_f(v[j]) * u[j];
-    }
+    for (int j = 0; j < 8; ++j) v[j] = silu_f(v[j]) * u[j];
   }
   const float m = half_warp_max(amax8(v));
   if (in) {
@@ -36,18 +33,75 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const bf16* __restrict_
   }
 }
 
-// CTA per 128 tokens and a run of 64-column blocks: rows are read 128 bytes wide into shared memory, then each thread
-// takes a quarter (32 tokens) of one column and writes its 32 codes, so a column's 128 codes leave as one 128-byte
-// line. The next block's rows are on their way meanwhile; segments and row indexes are looked up once a CTA (a CTA
-// for every block spent most of its time on that: 12,288 x 2,816 gathered rows took 51 us).
-constexpr int kColBlocks = 11;       // column blocks of a CTA
-__global__ void __launch_bounds__(256) quant_cols_kernel(const bf16* __restrict__ src, long long ld, int src_rows,
+// Rows of bf16 values, eight lanes a block of 128 (16 values each, so that what a block needs once, its maximum, its
+// reciprocal and its scale, is shared by more of them: with 8 values a lane the kernel was bound by its instructions).
+__global__ void __launch_bounds__(256) quant_rows_kernel(const bf16* __restrict__ src, long long ld, unsigned items,
+                                                         int nb, int C, uint8_t* __restrict__ q,
+                                                         float* __restrict__ scale) {
+  griddep_wait();
+  griddep_launch();
+  const unsigned i = blockIdx.x * 32 + (threadIdx.x >> 3), r = i / (unsigned)nb;
+  const long long row = r;
+  const int c = (int)(i - r * nb) * kScaleBlock + (threadIdx.x & 7) * 16;
+  const bool in = i < items && c < C, two = c + 8 < C;   // C is a multiple of 8
+  uint4 w[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+  if (in) {
+    const uint4* p = reinterpret_cast<const uint4*>(src + row * ld + c);
+    w[0] = p[0];
+    if (two) w[1] = p[1];
+  }
+  uint32_t m2 = 0u;
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    m2 = bf16x2_amax(bf16x2_amax(bf16x2_amax(bf16x2_amax(m2, w[k].x), w[k].y), w[k].z), w[k].w);
+#pragma unroll
+  for (int o = 4; o; o >>= 1) m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, o));
+  const float m = __uint_as_float(max(m2 << 16, m2 & 0xffff0000u));
+  if (!in) return;
+  const Divisor d(m);
+  uint2 u[2];
+  if (d.plain) {
+    const uint64_t rr = f32x2(d.r, d.r), nm = f32x2(-m, -m);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t x[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+      float f[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        f32x2_get(code2(f32x2(__uint_as_float(x[j] << 16), __uint_as_float(x[j] & 0xffff0000u)), rr, nm), f[2 * j], f[2 * j + 1]);
+      u[k] = make_uint2(pack_codes4(f[0], f[1], f[2], f[3]), pack_codes4(f[4], f[5], f[6], f[7]));
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float f[8];
+      unpack8(w[k], f);
+      u[k] = codes8(f, m);
+    }
+  }
+  uint2* dst = reinterpret_cast<uint2*>(q + row * C + c);
+  if (two && ((uintptr_t)dst & 15) == 0) {
+    *reinterpret_cast<uint4*>(dst) = make_uint4(u[0].x, u[0].y, u[1].x, u[1].y);
+  } else {
+    dst[0] = u[0];
+    if (two) dst[1] = u[1];
+  }
+  if ((threadIdx.x & 7) == 0) scale[i] = block_scale(m);
+}
+
+// CTA per 128 tokens and a run of 64-column blocks: rows are read 128 bytes wide into shared memory (the next block's
+// while this one is worked on), a warp takes 16 tokens and a lane two neighbouring columns of them, and the codes go
+// back through shared memory so that a column's 128 leave as one 128-byte line. Segments and row indexes are looked up
+// once a CTA.
+constexpr int kColBlocks = 8;        // column blocks of a CTA
+__global__ void __launch_bounds__(256, 3) quant_cols_kernel(const bf16* __restrict__ src, long long ld, int src_rows,
                                                          int T, int C, const int* __restrict__ off, int G,
                                                          const int* __restrict__ row_index, uint8_t* __restrict__ q,
                                                          float* __restrict__ scale, long long Tp, int* status) {
   __shared__ SegSmem seg;
-  __shared__ uint4 tile4[2][128][8];      // [block parity][token][64 columns]
-  __shared__ float red[2][4][64];
+  __shared__ uint4 tile[128][8];                 // [token][64 columns]
+  __shared__ uint32_t red[8][32];                // [warp][column pair]
+  __shared__ __align__(16) uint8_t out[64][144]; // [column of a pair, pair][token], rows 16 bytes apart in the banks
   griddep_wait();
   griddep_launch();
   load_segments(seg, off, G, T, kScaleBlock, status);
@@ -55,7 +109,7 @@ __global__ void __launch_bounds__(256) quant_cols_kernel(const bf16* __restrict_
   if (t >= seg.tile[G]) return;
   const int g = segment_of(seg, G, t);
   const int row0 = seg.off[g] + (t - seg.tile[g]) * kScaleBlock, row1 = seg.off[g + 1];
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bf16* rows[4];                 // this thread's rows (null: zeros)
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -68,38 +122,68 @@ __global__ void __launch_bounds__(256) quant_cols_kernel(const bf16* __restrict_
       else set_error(status, MOE_ERR_DEVICE_INDEX);
     }
   }
-  const int c_end = min(C, (int)(blockIdx.x + 1) * kColBlocks * 64);
+  const int c_first = blockIdx.x * kColBlocks * 64, c_end = min(C, c_first + kColBlocks * 64);
   uint4 v4[4];
   const auto fetch = [&](int c0) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       v4[i] = rows[i] && c0 + (tid & 7) * 8 < c_end ? *reinterpret_cast<const uint4*>(rows[i] + c0) : make_uint4(0u, 0u, 0u, 0u);
   };
-  const int col = tid & 63, part = tid >> 6;
-  int b = 0;
-  fetch(blockIdx.x * kColBlocks * 64);
-  for (int c0 = blockIdx.x * kColBlocks * 64; c0 < c_end; c0 += 64, b ^= 1) {
+  fetch(c_first);
+  for (int c0 = c_first; c0 < c_end; c0 += 64) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) tile4[b][i * 32 + (tid >> 3)][tid & 7] = v4[i];
+    for (int i = 0; i < 4; ++i) tile[i * 32 + (tid >> 3)][tid & 7] = v4[i];
     __syncthreads();
     if (c0 + 64 < c_end) fetch(c0 + 64);
-    const bf16* column = reinterpret_cast<const bf16*>(&tile4[b][0][0]) + part * 32 * 64 + col;
-    float v[32], m = 0.f;
+    const uint32_t* mine = reinterpret_cast<const uint32_t*>(&tile[warp * 16][0]) + lane;
+    uint32_t x[16], m2 = 0u;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      v[i] = to_f(column[i * 64]);
-      m = max_nan(m, fabsf(v[i]));
+    for (int i = 0; i < 16; ++i) {
+      x[i] = mine[i * 32];
+      m2 = bf16x2_amax(m2, x[i]);
     }
-    red[b][part][col] = m;
+    red[warp][lane] = m2;
     __syncthreads();
-    m = max_nan(max_nan(red[b][0][col], red[b][1][col]), max_nan(red[b][2][col], red[b][3][col]));
-    if (c0 + col < c_end) {
-      uint32_t w[8];
-      codes<32>(v, m, w);
-      uint4* dst = reinterpret_cast<uint4*>(q + (long long)(c0 + col) * Tp + (long long)t * kScaleBlock + part * 32);
-      dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-      dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-      if (part == 0) scale[(long long)t * C + c0 + col] = block_scale(m);
+    m2 = red[0][lane];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m2 = __vmaxu2(m2, red[i][lane]);
+    const float ma = __uint_as_float(m2 << 16), mb = __uint_as_float(m2 & 0xffff0000u);
+    const Divisor da(ma), db(mb);
+    uint32_t wa[4], wb[4];
+    const bool plain = da.plain && db.plain;
+    const uint64_t rr = f32x2(da.r, db.r), nm = f32x2(-ma, -mb);
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      float a[4], b[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        a[j] = __uint_as_float(x[i + j] << 16);
+        b[j] = __uint_as_float(x[i + j] & 0xffff0000u);
+        if (plain) {
+          f32x2_get(code2(f32x2(a[j], b[j]), rr, nm), a[j], b[j]);
+        } else {
+          a[j] = code_value(a[j], ma);
+          b[j] = code_value(b[j], mb);
+        }
+      }
+      wa[i / 4] = pack_codes4(a[0], a[1], a[2], a[3]);
+      wb[i / 4] = pack_codes4(b[0], b[1], b[2], b[3]);
+    }
+    *reinterpret_cast<uint4*>(&out[lane][warp * 16]) = make_uint4(wa[0], wa[1], wa[2], wa[3]);
+    *reinterpret_cast<uint4*>(&out[32 + lane][warp * 16]) = make_uint4(wb[0], wb[1], wb[2], wb[3]);
+    const int cl = c0 + 2 * lane;
+    if (warp == 0 && cl < c_end) {     // C is even
+      float* s = scale + (long long)t * C + cl;
+      s[0] = block_scale(ma);
+      s[1] = block_scale(mb);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = i * 32 + (tid >> 3), col = c0 + 2 * (r & 31) + i;
+      if (col < c_end)
+        *reinterpret_cast<uint4*>(q + (long long)col * Tp + (long long)t * kScaleBlock + (tid & 7) * 16) =
+            *reinterpret_cast<const uint4*>(&out[r][(tid & 7) * 16]);
     }
   }
 }
@@ -172,8 +256,11 @@ cudaError_t quant_rows(const moe_ops_s*, const void* src, long long ld, int T, i
   const int nb = ceil_div(C, kScaleBlock);
   const long long items = (long long)T * nb;
   *n += 1;
-  return launch_pdl(swiglu ? quant_rows_kernel<true> : quant_rows_kernel<false>, dim3((unsigned)((items + 15) / 16)),
-                    dim3(256), 0, s, (const bf16*)src, ld, items, nb, C, (uint8_t*)q, scale);
+  if (swiglu)
+    return launch_pdl(quant_swiglu_kernel, dim3((unsigned)((items + 15) / 16)), dim3(256), 0, s, (const bf16*)src, ld,
+                      (unsigned)items, nb, C, (uint8_t*)q, scale);
+  return launch_pdl(quant_rows_kernel, dim3((unsigned)((items + 31) / 32)), dim3(256), 0, s, (const bf16*)src, ld,
+                    (unsigned)items, nb, C, (uint8_t*)q, scale);
 }
 
 cudaError_t quant_cols(const moe_ops_s* o, const void* src, long long ld, int src_rows, int T, int C, const int* off,
