@@ -90,7 +90,7 @@ typedef struct {
  * Outputs: idx [T, k] int32, gate [T, k] fp32 (required), and the dispatch of
  * moe_route, all four or none: cnt [E], off [E+1], perm [T*k], inv [T*k].
  * workspace (moe_gate_workspace_size bytes, 16-byte aligned; NULL without a
- * dispatch). T * k < 2^30. */
+ * dispatch or where that is 0). T * k < 2^30. */
 moe_status moe_gate_workspace_size(const moe_gate_config* cfg, int T, size_t* bytes);
 moe_status moe_gate_forward(moe_ops ops, const moe_gate_config* cfg, const float* logits, const float* bias, int T,
                             int32_t* idx, float* gate, int32_t* cnt, int32_t* off, int32_t* perm, int32_t* inv,

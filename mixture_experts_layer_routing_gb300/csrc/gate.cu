@@ -571,8 +571,10 @@ cudaError_t bwd(const float* logits, const int* idx, const float* dgate, int T, 
 
 }  // namespace
 
-// One count of every expert for each chunk; chunks number at most one for each 64 tokens.
-size_t gate_workspace(const moe_gate_config& c, int T) { return sizeof(int) * (size_t)c.E * ceil_div(T, kGateTokens); }
+// One count of every expert for each chunk (at most one chunk for each 64 tokens); a single chunk needs none.
+size_t gate_workspace(const moe_gate_config& c, int T) {
+  return T <= kGateTokens ? 0 : sizeof(int) * (size_t)c.E * ceil_div(T, kGateTokens);
+}
 
 cudaError_t gate_forward(const moe_ops_s* o, const moe_gate_config& c, const float* logits, const float* bias, int T,
                          int* idx, float* gate, int* cnt, int* off, int* perm, int* inv, void* ws, cudaStream_t s,

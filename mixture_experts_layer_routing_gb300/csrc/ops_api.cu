@@ -169,7 +169,7 @@ moe_status moe_gate_forward(moe_ops ops, const moe_gate_config* cfg, const float
   const int given = (cnt != nullptr) + (off != nullptr) + (perm != nullptr) + (inv != nullptr);
   if (T > 0) {
     CHECK(logits && idx && gate && (given == 0 || given == 4), MOE_ERR_INVALID_ARG);
-    CHECK(given == 0 || (workspace && aligned(workspace, 16)), MOE_ERR_WORKSPACE);
+    CHECK(given == 0 || gate_workspace(*cfg, T) == 0 || (workspace && aligned(workspace, 16)), MOE_ERR_WORKSPACE);
   }
   HANDLE(ops);
   if (T == 0) {   // perm and inv have no entries

@@ -92,7 +92,7 @@ GATE = dict(ops=P, cfg=None, logits=P, bias=None, T=4, idx=P, gate=P, cnt=P, off
 @pytest.mark.parametrize("over,code", [
     (dict(ops=None), ARG), (dict(T=-1), ARG), (dict(T=1 << 28), UNSUP), (dict(logits=None), ARG),
     (dict(idx=None), ARG), (dict(gate=None), ARG), (dict(cnt=None), ARG), (dict(inv=None), ARG),
-    (dict(workspace=None), WS),
+    (dict(T=65, workspace=None), WS), (dict(T=65, workspace=P + 4), WS),
 ])
 def test_gate_refuses_arguments(lib, over, code):
     c = cfg()
