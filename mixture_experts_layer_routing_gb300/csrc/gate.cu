@@ -37,10 +37,19 @@ __device__ __forceinline__ float of_order(unsigned u) {
   return __uint_as_float(u >> 31 ? u & 0x7fffffffu : ~u);
 }
 __device__ __forceinline__ float lanes_max(float v) { return of_order(__reduce_max_sync(kFull, order_of(v))); }
-__device__ __forceinline__ double lanes_max(double v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v = fmax(v, __shfl_xor_sync(kFull, v, o));
-  return v;
+// The same for doubles: compared as integers, in the integer pipe.
+typedef unsigned long long u64;
+__device__ __forceinline__ u64 order_of(double v) {
+  const u64 u = (u64)__double_as_longlong(v);
+  return u >> 63 ? ~u : u | 0x8000000000000000ull;
+}
+__device__ __forceinline__ double of_order(u64 u) {
+  return __longlong_as_double((long long)(u >> 63 ? u & 0x7fffffffffffffffull : ~u));
+}
+__device__ __forceinline__ u64 lanes_max(u64 v) {
+  const unsigned hi = __reduce_max_sync(kFull, (unsigned)(v >> 32));
+  const unsigned lo = __reduce_max_sync(kFull, (unsigned)(v >> 32) == hi ? (unsigned)v : 0u);
+  return (u64)hi << 32 | lo;
 }
 __device__ __forceinline__ double lanes_sum(double v) {
 #pragma unroll
@@ -48,21 +57,21 @@ __device__ __forceinline__ double lanes_sum(double v) {
   return v;
 }
 
-// The 64-bit score and key of an expert. m, sum: the row's largest logit and sum of exponentials (softmax).
-__device__ __forceinline__ double exact_key(const moe_gate_config& c, float l, float b, float m, double sum) {
-  double p;
-  if (c.router == MOE_ROUTER_SOFTMAX) {
-    p = sum == 0.0 ? 0.0 : exp((double)l - (double)m) / sum;
-  } else {
-    p = 1.0 / (1.0 + exp(-(double)l));
-  }
+// The 64-bit path is rarely taken, so its instructions come from far: it is written for few of them (no unrolling, one
+// copy of each double-precision function), not for speed once they are there.
+__device__ __noinline__ double exact_exp(double x) { return exp(x); }
+// The 64-bit key of an expert, in order. m, sum: the row's largest logit and sum of exponentials (softmax).
+__device__ __noinline__ u64 exact_key(int softmax, float l, float b, float m, double sum) {
+  const double t = exact_exp(softmax ? (double)l - (double)m : -(double)l);
+  const double p = softmax && sum == 0.0 ? 0.0 : (softmax ? t : 1.0) / (softmax ? sum : 1.0 + t);
   const double k = p + (double)b;
-  return (l == -INFINITY || isnan(k)) ? -DBL_MAX : fmax(k, -DBL_MAX);
+  return order_of((l == -INFINITY || isnan(k)) ? -DBL_MAX : fmax(k, -DBL_MAX));
 }
 __device__ __forceinline__ double exact_sum(const moe_gate_config& c, const float* __restrict__ logits, float m) {
   double s = 0.0;
-  if (c.router == MOE_ROUTER_SOFTMAX)
-    for (int e = threadIdx.x & 31; e < c.E; e += 32) s += exp((double)logits[e] - (double)m);
+  if (c.router != MOE_ROUTER_SOFTMAX) return s;
+#pragma unroll 1
+  for (int e = threadIdx.x & 31; e < c.E; e += 32) s += exact_exp((double)logits[e] - (double)m);
   return lanes_sum(s);
 }
 
@@ -73,57 +82,62 @@ __device__ __noinline__ int select_exact(const float* __restrict__ logits, const
                                          const moe_gate_config& c) {
   const int lane = threadIdx.x & 31, e0 = lane * PER;
   const double sum = exact_sum(c, logits, m);
-  double key[PER];
-#pragma unroll
+  u64 key[PER];
+#pragma unroll 1
   for (int q = 0; q < PER; ++q)
-    key[q] = e0 + q < c.E ? exact_key(c, logits[e0 + q], bias ? bias[e0 + q] : 0.f, m, sum) : -INFINITY;
+    key[q] = e0 + q < c.E ? exact_key(c.router == MOE_ROUTER_SOFTMAX, logits[e0 + q], bias ? bias[e0 + q] : 0.f, m, sum)
+                          : 0ull;
   if (c.topk_groups < c.n_groups) {
     const int S = c.E / c.n_groups;
-    double score = -INFINITY;   // lane g: group g
+    u64 score = 0ull;   // lane g: group g
+#pragma unroll 1
     for (int g = 0; g < c.n_groups; ++g) {
-      double a = -INFINITY, b = -INFINITY;   // this lane's two best of group g
-#pragma unroll
+      u64 a = 0ull, b = 0ull;   // this lane's two best of group g
+#pragma unroll 1
       for (int q = 0; q < PER; ++q) {
         if (e0 + q >= g * S && e0 + q < (g + 1) * S) {
-          b = fmax(b, fmin(a, key[q]));
-          a = fmax(a, key[q]);
+          b = max(b, min(a, key[q]));
+          a = max(a, key[q]);
         }
       }
-      double s = lanes_max(a);
+      const u64 first = lanes_max(a);
+      u64 s = first;
       if (S > 1) {
-        const int owner = __ffs(__ballot_sync(kFull, a == s)) - 1;
-        s += lanes_max(lane == owner ? b : a);
+        const int owner = __ffs(__ballot_sync(kFull, a == first)) - 1;
+        s = order_of(of_order(first) + of_order(lanes_max(lane == owner ? b : a)));
       }
       if (lane == g) score = s;
     }
     int rank = 0;
+#pragma unroll 1
     for (int g = 0; g < c.n_groups; ++g) {
-      const double other = __shfl_sync(kFull, score, g);
+      const u64 other = __shfl_sync(kFull, score, g);
       rank += other > score || (other == score && g < lane);
     }
     const unsigned kept = __ballot_sync(kFull, lane < c.n_groups && rank < c.topk_groups);
-#pragma unroll
+#pragma unroll 1
     for (int q = 0; q < PER; ++q)
-      if (e0 + q < c.E && !(kept >> ((e0 + q) / S) & 1u)) key[q] = -INFINITY;
+      if (e0 + q < c.E && !(kept >> ((e0 + q) / S) & 1u)) key[q] = 0ull;
   }
   int mine = 0;
+#pragma unroll 1
   for (int j = 0; j < c.k; ++j) {
-    double top = -INFINITY;
+    u64 top = 0ull;
     int at = 0;
-#pragma unroll
+#pragma unroll 1
     for (int q = 0; q < PER; ++q) {
       if (key[q] > top) {
         top = key[q];
         at = q;
       }
     }
-    const double best = lanes_max(top);
+    const u64 best = lanes_max(top);
     const int owner = __ffs(__ballot_sync(kFull, top == best)) - 1;
     const int e = __shfl_sync(kFull, e0 + at, owner);
     if (lane == j) mine = e;
-#pragma unroll
+#pragma unroll 1
     for (int q = 0; q < PER; ++q)
-      if (lane == owner && q == at) key[q] = -INFINITY;
+      if (lane == owner && q == at) key[q] = 0ull;
   }
   return mine;
 }
@@ -132,15 +146,43 @@ __device__ __noinline__ int select_exact(const float* __restrict__ logits, const
 __device__ __noinline__ int rank_exact(const float* __restrict__ logits, const float* __restrict__ bias, float m,
                                        const moe_gate_config& c, int e, bool in) {
   const double sum = exact_sum(c, logits, m);
-  const double key = in ? exact_key(c, logits[e], bias ? bias[e] : 0.f, m, sum) : -INFINITY;
+  const u64 key = in ? exact_key(c.router == MOE_ROUTER_SOFTMAX, logits[e], bias ? bias[e] : 0.f, m, sum) : 0ull;
   int rank = 0;
+#pragma unroll 1
   for (unsigned left = __ballot_sync(kFull, in); left; left &= left - 1) {
     const int i = __ffs(left) - 1;
-    const double other = __shfl_sync(kFull, key, i);
+    const u64 other = __shfl_sync(kFull, key, i);
     const int oe = __shfl_sync(kFull, e, i);
     rank += other > key || (other == key && oe < e);
   }
   return rank;
+}
+
+// The groups that stay (a bit each), from the experts that can be one of their group's two best: lane i's e where `in`.
+__device__ __noinline__ unsigned groups_exact(const float* __restrict__ logits, const float* __restrict__ bias,
+                                              float m, const moe_gate_config& c, int e, bool in) {
+  const int lane = threadIdx.x & 31, S = c.E / c.n_groups;
+  const double sum = exact_sum(c, logits, m);
+  const u64 key = in ? exact_key(c.router == MOE_ROUTER_SOFTMAX, logits[e], bias ? bias[e] : 0.f, m, sum) : 0ull;
+  const int mine = in ? e / S : -1;
+  u64 score = 0ull;   // lane g: group g
+#pragma unroll 1
+  for (int g = 0; g < c.n_groups; ++g) {
+    const u64 k = mine == g ? key : 0ull, first = lanes_max(k);
+    u64 s = first;
+    if (S > 1) {
+      const int owner = __ffs(__ballot_sync(kFull, k == first)) - 1;
+      s = order_of(of_order(first) + of_order(lanes_max(lane == owner ? 0ull : k)));
+    }
+    if (lane == g) score = s;
+  }
+  int rank = 0;
+#pragma unroll 1
+  for (int g = 0; g < c.n_groups; ++g) {
+    const u64 other = __shfl_sync(kFull, score, g);
+    rank += other > score || (other == score && g < lane);
+  }
+  return __ballot_sync(kFull, lane < c.n_groups && rank < c.topk_groups);
 }
 
 // A lane's PER consecutive values of a row, in 16-byte loads where rows are made of them.
@@ -163,16 +205,18 @@ __device__ __forceinline__ void load_lane(const float* __restrict__ row, int E, 
   }
 }
 
-// The groups that stay, as bits of this lane's own experts. sure turns false where their choice rests on a gap that
-// is not above the error of a score (a sum of two keys).
+// The groups that stay, a bit each. Where their choice rests on a gap that is not above the error of a score (a sum of
+// two keys), by 64-bit keys of the experts that can be one of their group's two best; sure turns false if these are
+// more than a warp holds. scr: 32 words.
 template <int PER>
-__device__ __forceinline__ unsigned kept_experts(const unsigned (&key)[PER], const moe_gate_config& c, float tau,
-                                                 bool& sure) {
+__device__ __forceinline__ unsigned kept_groups(const unsigned (&key)[PER], const moe_gate_config& c, float tau,
+                                                const float* __restrict__ logits, const float* __restrict__ bias,
+                                                float m, unsigned* scr, bool& sure) {
   const int lane = threadIdx.x & 31, e0 = lane * PER, S = c.E / c.n_groups, L = S / PER;
-  // Groups that fill a power of two of lanes: all at once, every lane with its own group's score. Others: group by
-  // group, lane g with group g's.
+  // Groups that fill a power of two of lanes: all at once, every lane with its own group's. Others: group by group,
+  // lane g with group g's.
   const bool fills = L * PER == S && (L & (L - 1)) == 0;
-  float score = -INFINITY;
+  float score = -INFINITY, second = -INFINITY;
   if (fills) {
     unsigned a = 0u, b = 0u;
 #pragma unroll
@@ -185,7 +229,10 @@ __device__ __forceinline__ unsigned kept_experts(const unsigned (&key)[PER], con
       b = max(min(a, oa), max(b, ob));
       a = max(a, oa);
     }
-    if (e0 < c.E) score = S > 1 ? of_order(a) + of_order(b) : of_order(a);
+    if (e0 < c.E) {
+      second = of_order(S > 1 ? b : a);
+      score = S > 1 ? of_order(a) + second : second;
+    }
   } else {
     for (int g = 0; g < c.n_groups; ++g) {
       unsigned a = 0u, b = 0u;
@@ -197,12 +244,16 @@ __device__ __forceinline__ unsigned kept_experts(const unsigned (&key)[PER], con
         }
       }
       const unsigned best = __reduce_max_sync(kFull, a);
-      float s = of_order(best);
+      float s = of_order(best), s2 = s;
       if (S > 1) {
         const int owner = __ffs(__ballot_sync(kFull, a == best)) - 1;
-        s += of_order(__reduce_max_sync(kFull, lane == owner ? b : a));
+        s2 = of_order(__reduce_max_sync(kFull, lane == owner ? b : a));
+        s += s2;
       }
-      if (lane == g) score = s;
+      if (lane == g) {
+        score = s;
+        second = s2;
+      }
     }
   }
   const int step = fills ? L : 1, g = lane / step;
@@ -213,14 +264,33 @@ __device__ __forceinline__ unsigned kept_experts(const unsigned (&key)[PER], con
   }
   const bool in = g < c.n_groups, kept = in && rank < c.topk_groups;
   const float worst = -lanes_max(kept ? -score : -INFINITY), best = lanes_max(in && !kept ? score : -INFINITY);
-  if (!(worst - best > 3 * tau)) sure = false;
-  if (fills) return kept ? kFull : 0u;
-  const unsigned mask = __ballot_sync(kFull, kept);
-  unsigned bits = 0u;
+  if (worst - best > 3 * tau) {
+    // bit g of a ballot of the lanes that speak for the groups
+    const unsigned mask = __ballot_sync(kFull, kept && lane == g * step);
+    if (step == 1) return mask;
+    unsigned bits = 0u;
+    for (int i = 0; i < c.n_groups; ++i) bits |= (mask >> (i * step) & 1u) << i;
+    return bits;
+  }
+  int n = 0;
 #pragma unroll
-  for (int q = 0; q < PER; ++q)
-    if (e0 + q < c.E && (mask >> ((e0 + q) / S) & 1u)) bits |= 1u << q;
-  return bits;
+  for (int q = 0; q < PER; ++q) {
+    const int mine = min((e0 + q) / S, c.n_groups - 1);
+    const float limit = __shfl_sync(kFull, second, mine * step) - tau;
+    const bool cand = key[q] && !(of_order(key[q]) < limit);
+    const unsigned mask = __ballot_sync(kFull, cand);
+    const int at = n + __popc(mask & ((1u << lane) - 1u));
+    if (cand && at < 32) scr[at] = e0 + q;
+    n += __popc(mask);
+  }
+  __syncwarp();
+  if (n > 32) {
+    sure = false;
+    return 0u;
+  }
+  const int e = lane < n ? (int)scr[lane] : 0;
+  __syncwarp();
+  return groups_exact(logits, bias, m, c, e, lane < n);
 }
 
 // One token: lane j < k returns expert j of the selection and its gate. scr: 64 words of the warp's own.
@@ -269,10 +339,17 @@ __device__ __forceinline__ int gate_token(const float* __restrict__ logits, cons
   const float tau = (c.router == MOE_ROUTER_SOFTMAX ? 0x1p-18f : 0x1p-20f) * pmax + 0x1p-22f * kmax;
   bool groups_sure = true;
   if (c.topk_groups < c.n_groups) {
-    const unsigned keep = kept_experts<PER>(key, c, tau, groups_sure);
+    const unsigned keep = kept_groups<PER>(key, c, tau, logits, bias, m, scr, groups_sure);
+    const int S = c.E / c.n_groups;
+    int g = e0 / S, left = (g + 1) * S - e0;     // experts until the next group
 #pragma unroll
-    for (int q = 0; q < PER; ++q)
-      if (!(keep >> q & 1u)) key[q] = 0u;
+    for (int q = 0; q < PER; ++q) {
+      if (!(keep >> g & 1u)) key[q] = 0u;
+      if (--left == 0) {
+        left = S;
+        g = min(g + 1, 31);                      // (past the last expert the key is 0 already)
+      }
+    }
   }
   // The k + 1 largest different keys; lane j keeps the j-th. (Equal ones are told by the candidates' number below.)
   unsigned mine = 0u, last = kFull;
@@ -438,7 +515,7 @@ __global__ void __launch_bounds__(kGateThreads) dispatch_kernel(const int* __res
   const int e = tid & (kMaxE - 1), part = tid / kMaxE;
   int all = 0, before = 0;
   if (e < E) {
-#pragma unroll 8
+#pragma unroll 16
     for (int i = part; i < nch; i += kGateThreads / kMaxE) {
       const int n = hist[i * E + e];
       all += n;
