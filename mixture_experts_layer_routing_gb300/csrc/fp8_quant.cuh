@@ -107,6 +107,11 @@ template <> struct Raw8<bf16> {
   __device__ __forceinline__ void store(bf16* p) const { *reinterpret_cast<uint4*>(p) = u; }
   __device__ __forceinline__ void get(float* f) const { unpack8(u, f); }
   __device__ __forceinline__ void set(const float* f) { u = pack8(f); }
+  __device__ __forceinline__ void pairs(uint64_t* p) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = f32x2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  }
 };
 template <> struct Raw8<float> {
   float4 a, b;
@@ -121,6 +126,12 @@ template <> struct Raw8<float> {
   __device__ __forceinline__ void get(float* f) const {
     f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
     f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  }
+  __device__ __forceinline__ void pairs(uint64_t* p) const {
+    p[0] = f32x2(a.x, a.y);
+    p[1] = f32x2(a.z, a.w);
+    p[2] = f32x2(b.x, b.y);
+    p[3] = f32x2(b.z, b.w);
   }
   __device__ __forceinline__ void set(const float* f) {
     a = make_float4(f[0], f[1], f[2], f[3]);

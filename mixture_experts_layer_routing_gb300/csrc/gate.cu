@@ -31,7 +31,7 @@ constexpr unsigned kFull = 0xffffffffu;
 // Order-preserving map of floats (no NaN) to unsigned; 0 is below every float's.
 __device__ __forceinline__ unsigned order_of(float v) {
   const unsigned u = __float_as_uint(v);
-  return u >> 31 ? ~u : u | 0x80000000u;
+  return u ^ ((unsigned)((int)u >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float of_order(unsigned u) {
   return __uint_as_float(u >> 31 ? u & 0x7fffffffu : ~u);
@@ -205,17 +205,36 @@ __device__ __forceinline__ void load_lane(const float* __restrict__ row, int E, 
   }
 }
 
+// Where a lane's experts lie among the groups (integer divisions, once a warp).
+struct Place {
+  int S;          // experts of a group
+  int step;       // lanes of a group where its experts fill a power of two of lanes, else 1
+  bool fills;
+  int g, left;    // group of the lane's first expert, and experts until the next group
+  int mine;       // group that the lane speaks for
+  __device__ __forceinline__ Place(const moe_gate_config& c, int per) {
+    const int lane = threadIdx.x & 31, e0 = lane * per;
+    S = c.E / c.n_groups;
+    const int L = S / per;
+    fills = L * per == S && (L & (L - 1)) == 0;
+    step = fills ? L : 1;
+    g = e0 / S;
+    left = (g + 1) * S - e0;
+    mine = fills ? g : lane;
+  }
+};
+
 // The groups that stay, a bit each. Where their choice rests on a gap that is not above the error of a score (a sum of
 // two keys), by 64-bit keys of the experts that can be one of their group's two best; sure turns false if these are
 // more than a warp holds. scr: 32 words.
 template <int PER>
-__device__ __forceinline__ unsigned kept_groups(const unsigned (&key)[PER], const moe_gate_config& c, float tau,
-                                                const float* __restrict__ logits, const float* __restrict__ bias,
-                                                float m, unsigned* scr, bool& sure) {
-  const int lane = threadIdx.x & 31, e0 = lane * PER, S = c.E / c.n_groups, L = S / PER;
+__device__ __forceinline__ unsigned kept_groups(const unsigned (&key)[PER], const moe_gate_config& c,
+                                                const Place& at_, float tau, const float* __restrict__ logits,
+                                                const float* __restrict__ bias, float m, unsigned* scr, bool& sure) {
+  const int lane = threadIdx.x & 31, e0 = lane * PER, S = at_.S, L = at_.step;
   // Groups that fill a power of two of lanes: all at once, every lane with its own group's. Others: group by group,
   // lane g with group g's.
-  const bool fills = L * PER == S && (L & (L - 1)) == 0;
+  const bool fills = at_.fills;
   float score = -INFINITY, second = -INFINITY;
   if (fills) {
     unsigned a = 0u, b = 0u;
@@ -256,7 +275,7 @@ __device__ __forceinline__ unsigned kept_groups(const unsigned (&key)[PER], cons
       }
     }
   }
-  const int step = fills ? L : 1, g = lane / step;
+  const int step = at_.step, g = at_.mine;
   int rank = 0;
   for (int i = 0; i < c.n_groups; ++i) {
     const float other = __shfl_sync(kFull, score, i * step);
@@ -296,7 +315,7 @@ __device__ __forceinline__ unsigned kept_groups(const unsigned (&key)[PER], cons
 // One token: lane j < k returns expert j of the selection and its gate. scr: 64 words of the warp's own.
 template <int PER>
 __device__ __forceinline__ int gate_token(const float* __restrict__ logits, const float* __restrict__ bias,
-                                          const moe_gate_config& c, unsigned* scr, float& gate) {
+                                          const moe_gate_config& c, const Place& place, unsigned* scr, float& gate) {
   const int lane = threadIdx.x & 31, e0 = lane * PER;
   float l[PER], p[PER], b[PER];
   load_lane<PER>(logits, c.E, -INFINITY, l);
@@ -328,9 +347,14 @@ __device__ __forceinline__ int gate_token(const float* __restrict__ logits, cons
 #pragma unroll
   for (int q = 0; q < PER; ++q) {
     const float k = p[q] + b[q];
-    const bool off = l[q] == -INFINITY || k != k;
-    if (!off) kmax = fmaxf(kmax, fabsf(k));
-    key[q] = e0 + q < c.E ? order_of(off ? -FLT_MAX : fmaxf(k, -FLT_MAX)) : 0u;
+    const bool on = l[q] > -INFINITY && k == k;      // neither masked nor NaN
+    kmax = fmaxf(kmax, on ? fabsf(k) : 0.f);
+    key[q] = order_of(on ? fmaxf(k, -FLT_MAX) : -FLT_MAX);
+  }
+  if (e0 + PER > c.E) {
+#pragma unroll
+    for (int q = 0; q < PER; ++q)
+      if (e0 + q >= c.E) key[q] = 0u;
   }
   kmax = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(kmax)));
   // Error of a difference of two keys, in units of 2^-24. Softmax, of the largest score: 5 of each score's
@@ -339,14 +363,18 @@ __device__ __forceinline__ int gate_token(const float* __restrict__ logits, cons
   const float tau = (c.router == MOE_ROUTER_SOFTMAX ? 0x1p-18f : 0x1p-20f) * pmax + 0x1p-22f * kmax;
   bool groups_sure = true;
   if (c.topk_groups < c.n_groups) {
-    const unsigned keep = kept_groups<PER>(key, c, tau, logits, bias, m, scr, groups_sure);
-    const int S = c.E / c.n_groups;
-    int g = e0 / S, left = (g + 1) * S - e0;     // experts until the next group
+    const unsigned keep = kept_groups<PER>(key, c, place, tau, logits, bias, m, scr, groups_sure);
+    int g = place.g, left = place.left;
+    if (place.fills) {
+#pragma unroll
+      for (int q = 0; q < PER; ++q)
+        if (!(keep >> (g & 31) & 1u)) key[q] = 0u;
+    } else
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
-      if (!(keep >> g & 1u)) key[q] = 0u;
+      if (!(keep >> (g & 31) & 1u)) key[q] = 0u;
       if (--left == 0) {
-        left = S;
+        left = place.S;
         g = min(g + 1, 31);                      // (past the last expert the key is 0 already)
       }
     }
@@ -428,7 +456,8 @@ struct DispatchSmem {
 };
 
 // Sorted positions of the assignments a0 .. a1, in passes of the block's threads; run[] holds each expert's first.
-__device__ __forceinline__ void rank_chunk(DispatchSmem& sm, const int* idx, int a0, int a1, int E,
+// first: the expert of assignment a0 + threadIdx.x (-1 behind a1), which the caller may have loaded long before.
+__device__ __forceinline__ void rank_chunk(DispatchSmem& sm, const int* idx, int a0, int a1, int E, int first,
                                            int* __restrict__ perm, int* __restrict__ inv) {
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   for (int p0 = a0; p0 < a1; p0 += kGateThreads) {
@@ -436,7 +465,7 @@ __device__ __forceinline__ void rank_chunk(DispatchSmem& sm, const int* idx, int
     for (int i = tid; i < nw * kMaxE; i += kGateThreads) (&sm.wcnt[0][0])[i] = 0;
     __syncthreads();
     const int a = p0 + tid;
-    const int e = a < a1 ? idx[a] : -1;
+    const int e = p0 == a0 ? first : a < a1 ? idx[a] : -1;
     const unsigned same = __match_any_sync(kFull, e);
     const int rank = __popc(same & ((1u << lane) - 1u));
     if (e >= 0 && rank == 0) sm.wcnt[w][e] = __popc(same);
@@ -475,9 +504,10 @@ __global__ void __launch_bounds__(kGateThreads) gate_kernel(const float* __restr
   if (counts && tid < kMaxE) sm.run[tid] = 0;
   __syncthreads();
   const int t0 = blockIdx.x * tokens, t1 = min(T, t0 + tokens);
+  const Place place(c, PER);
   for (int t = t0 + w; t < t1; t += kGateWarps) {
     float g;
-    const int e = gate_token<PER>(logits + (size_t)t * c.E, bias, c, reinterpret_cast<unsigned*>(sm.wcnt[w]), g);
+    const int e = gate_token<PER>(logits + (size_t)t * c.E, bias, c, place, reinterpret_cast<unsigned*>(sm.wcnt[w]), g);
     if (lane < c.k) {
       idx[(size_t)t * c.k + lane] = e;
       gate[(size_t)t * c.k + lane] = g;
@@ -499,7 +529,7 @@ __global__ void __launch_bounds__(kGateThreads) gate_kernel(const float* __restr
     if (tid == c.E - 1) off[c.E] = first + n;
   }
   __syncthreads();
-  rank_chunk(sm, idx, 0, T * c.k, c.E, perm, inv);
+  rank_chunk(sm, idx, 0, T * c.k, c.E, tid < T * c.k ? idx[tid] : -1, perm, inv);
 }
 
 // Second kernel of a dispatch of several chunks: CTA ch adds up every chunk's counts (and those before its own) and
@@ -511,6 +541,8 @@ __global__ void __launch_bounds__(kGateThreads) dispatch_kernel(const int* __res
   griddep_wait();
   griddep_launch();
   const int tid = threadIdx.x, ch = blockIdx.x;
+  const int a0 = ch * tokens * k, a1 = min(T, (ch + 1) * tokens) * k;
+  const int mine = a0 + tid < a1 ? idx[a0 + tid] : -1;
   // four threads an expert, each a quarter of the chunks
   const int e = tid & (kMaxE - 1), part = tid / kMaxE;
   int all = 0, before = 0;
@@ -544,7 +576,7 @@ __global__ void __launch_bounds__(kGateThreads) dispatch_kernel(const int* __res
     }
   }
   __syncthreads();
-  rank_chunk(sm, idx, ch * tokens * k, min(T, (ch + 1) * tokens) * k, E, perm, inv);
+  rank_chunk(sm, idx, a0, a1, E, mine, perm, inv);
 }
 
 // One warp a token. With p the scores, ps those selected, D = sum ps + 1e-20:

@@ -4,8 +4,8 @@
 // through the one reduction (sum of squares), and every output leaves from there. A 128-value scale block is 16
 // neighbouring lanes, so its maximum takes four shuffles. Bound by HBM at many rows, by latency at few.
 //
-// Backward: a CTA walks rows with stride gridDim, keeps its part of dw in registers and makes one
-// reduction a row (mean(u n); rstd comes from the forward pass). The parts are summed in a fixed order by a
+// Backward: as many CTAs as run at once walk the rows with stride gridDim, each with its part of dw in registers, and
+// make one reduction a row (mean(u n); rstd comes from the forward pass). The parts are summed in a fixed order by a
 // second kernel, so dw does not depend on timing.
 #include "fp8_quant.cuh"
 #include "launch.cuh"
@@ -14,7 +14,7 @@
 namespace moe {
 namespace {
 
-constexpr int kNormCtas = 304;   // two CTAs a SM walk the rows of the backward pass
+constexpr int kNormParts = 640;   // CTAs of the backward pass, at most
 
 // Sum over the block; red holds one word a warp and is free for reuse after the next barrier.
 __device__ __forceinline__ float block_sum(float v, float* red) {
@@ -92,83 +92,110 @@ __global__ void __launch_bounds__(VPT == 4 ? 512 : 1024, 1) norm_fwd_kernel(cons
   }
 }
 
-// The next row's dy and h (and dh) are loaded before this row's reduction, so that their latency passes behind it
-// (not at VPT = 2, whose 1024 threads have no registers for it).
-template <typename T, int VPT>
-__global__ void __launch_bounds__(1024, 1) norm_bwd_kernel(const T* dy, const T* dh, const T* __restrict__ h,
-                                                        const T* __restrict__ w, const float* __restrict__ rstd,
-                                                        int rows, int d, T* dx, float* part) {
+// A row is held as it is stored (12 registers of bf16 a thread) and unpacked twice, before and after its reduction, so
+// that there is room for the next row, which is loaded a whole row ahead. (Unpacked values in registers and loads just
+// before the reduction: 31 us for 2,368 x 7,168 instead of @.)
+template <typename T, int VPT, int MAXT>
+__global__ void __launch_bounds__(MAXT, 1) norm_bwd_kernel(const T* dy, const T* dh, const T* __restrict__ h,
+                                                           const T* __restrict__ w, const float* __restrict__ rstd,
+                                                           int rows, int d, T* dx, float* part) {
   __shared__ float red[2][32];
   griddep_wait();
   griddep_launch();
   const int nv = d >> 3;
-  float acc[VPT][8];
+  uint64_t acc[VPT][4];
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
+    for (int j = 0; j < 4; ++j) acc[i][j] = 0;
   const float inv_d = 1.0f / (float)d;
-  Raw8<T> py[VPT], ph[VPT], pe[VPT];
-  float pr = 0.f;
-  const auto fetch = [&](long long t) {
+  struct Row {
+    Raw8<T> y[VPT], h[VPT], e[VPT];
+    float r;
+  };
+  const auto fetch = [&](Row& p, int t) {
     if (t >= rows) return;
-    pr = rstd[t];
+    p.r = rstd[t];
+    const long long at = (long long)t * d;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = i * blockDim.x + threadIdx.x;
       if (c < nv) {
-        py[i].load(dy + t * d + 8 * c);
-        ph[i].load(h + t * d + 8 * c);
-        if (dh && VPT == 1) pe[i].load(dh + t * d + 8 * c);
+        p.y[i].load(dy + at + 8 * c);
+        p.h[i].load(h + at + 8 * c);
+        if (dh) p.e[i].load(dh + at + 8 * c);
       }
     }
   };
-  if (VPT == 1) fetch(blockIdx.x);
-  int flip = 0;
-  for (long long t = blockIdx.x; t < rows; t += gridDim.x, flip ^= 1) {
-    if (VPT > 1) fetch(t);
-    const float r = pr;
-    Raw8<T> e[VPT];
-    float a[VPT][8], n[VPT][8], s = 0.f;
+  const auto take = [&](Row& p, int t, float* words) {
+    const uint64_t r2 = f32x2(p.r, p.r);
+    uint64_t s2 = 0;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = i * blockDim.x + threadIdx.x;
       if (c < nv) {
-        float g[8];
-        py[i].get(a[i]);
-        ph[i].get(n[i]);
-        if (VPT == 1) e[i] = pe[i];
-        load8(w + 8 * c, g);
+        uint64_t a[4], n[4], g[4];
+        Raw8<T> wr;
+        wr.load(w + 8 * c);
+        p.y[i].pairs(a);
+        p.h[i].pairs(n);
+        wr.pairs(g);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          n[i][j] *= r;
-          acc[i][j] += a[i][j] * n[i][j];
-          a[i][j] *= g[j];
-          s += a[i][j] * n[i][j];
+        for (int j = 0; j < 4; ++j) {
+          n[j] = f32x2_mul(n[j], r2);
+          acc[i][j] = f32x2_fma(a[j], n[j], acc[i][j]);
+          s2 = f32x2_fma(f32x2_mul(a[j], g[j]), n[j], s2);
         }
       }
     }
-    if (VPT == 1) fetch(t + gridDim.x);
-    if (!dx) continue;
-    const float mean = block_sum(s, red[flip]) * inv_d;   // two buffers: one barrier a row
+    if (!dx) return;
+    float s, s1;
+    f32x2_get(s2, s, s1);
+    const float mean = block_sum(s + s1, words) * inv_d;
+    const uint64_t m2 = f32x2(-mean * p.r, -mean * p.r);      // n mean = h (rstd mean)
+    const long long at = (long long)t * d;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = i * blockDim.x + threadIdx.x;
       if (c < nv) {
-        float o[8];
-        if (dh && VPT > 1) e[i].load(dh + t * d + 8 * c);
-        if (dh) e[i].get(o);
+        uint64_t a[4], n[4], g[4], o[4] = {0, 0, 0, 0};
+        Raw8<T> wr;
+        wr.load(w + 8 * c);
+        p.y[i].pairs(a);
+        p.h[i].pairs(n);
+        wr.pairs(g);
+        if (dh) p.e[i].pairs(o);
+        float f[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = (dh ? o[j] : 0.f) + r * (a[i][j] - n[i][j] * mean);
-        store8(dx + t * d + 8 * c, o);
+        for (int j = 0; j < 4; ++j)
+          f32x2_get(f32x2_fma(r2, f32x2_fma(n[j], m2, f32x2_mul(a[j], g[j])), o[j]), f[2 * j], f[2 * j + 1]);
+        store8(dx + at + 8 * c, f);
       }
     }
+  };
+  Row a, b;
+  int t = blockIdx.x;
+  const int step = gridDim.x;
+  fetch(a, t);
+  while (t < rows) {      // (two buffers of words: one barrier a row)
+    fetch(b, t + step);
+    take(a, t, red[0]);
+    t += step;
+    if (t >= rows) break;
+    fetch(a, t + step);
+    take(b, t, red[1]);
+    t += step;
   }
   if (part) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = i * blockDim.x + threadIdx.x;
-      if (c < nv) store8(part + (long long)blockIdx.x * d + 8 * c, acc[i]);
+      if (c < nv) {
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f32x2_get(acc[i][j], f[2 * j], f[2 * j + 1]);
+        store8(part + (long long)blockIdx.x * d + 8 * c, f);
+      }
     }
   }
 }
@@ -182,7 +209,7 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const float* __restrict__
   float s = 0.f;
   if (c < d) {
 #pragma unroll
-    for (int i = 0; i < (kNormCtas + 31) / 32; ++i)
+    for (int i = 0; i < (kNormParts + 31) / 32; ++i)
       if (w + 32 * i < parts) s += part[(long long)(w + 32 * i) * d + c];
   }
   red[w][lane] = s;
@@ -198,12 +225,12 @@ cudaError_t fwd(const void* x, long long ld_x, const void* res, long long ld_res
   return launch_pdl(norm_fwd_kernel<T, VPT>, dim3(rows), dim3(threads), 0, s, (const T*)x, ld_x, (const T*)res, ld_res,
                     (const T*)w, d, eps, (T*)h, (T*)y, (uint8_t*)q, scale, rstd);
 }
-template <typename T, int VPT>
+template <typename T, int VPT, int MAXT>
 cudaError_t bwd(const void* dy, const void* dh, const void* h, const void* w, const float* rstd, int rows, int d,
                 void* dx, float* part, int parts, cudaStream_t s) {
   const int threads = ceil_div(ceil_div(d / 8, VPT), 32) * 32;
-  return launch_pdl(norm_bwd_kernel<T, VPT>, dim3(parts), dim3(threads), 0, s, (const T*)dy, (const T*)dh, (const T*)h,
-                    (const T*)w, rstd, rows, d, (T*)dx, part);
+  return launch_pdl(norm_bwd_kernel<T, VPT, MAXT>, dim3(parts), dim3(threads), 0, s, (const T*)dy, (const T*)dh,
+                    (const T*)h, (const T*)w, rstd, rows, d, (T*)dx, part);
 }
 
 // Steps of 8 values a thread. Few rows: as many threads as there are (one step up to d = 8192).
@@ -215,7 +242,12 @@ inline int steps(int d, bool wide) {
 
 }  // namespace
 
-int norm_partials(int T) { return T < kNormCtas ? T : kNormCtas; }
+// CTAs of the backward pass: about 1,024 threads a SM (its rows in flight are registers).
+int norm_partials(int T, int d) {
+  const int threads = ceil_div(ceil_div(d / 8, d > 8192 ? 2 : 1), 32) * 32;
+  const int most = 152 * (threads > 512 ? 1 : threads > 256 ? 2 : 4);
+  return T < most ? T : most;
+}
 
 cudaError_t norm_forward(const moe_ops_s* o, int dtype, const void* x, long long ld_x, const void* res,
                          long long ld_res, const void* w, int T, int d, float eps, void* h, void* y, void* q,
@@ -231,13 +263,14 @@ cudaError_t norm_forward(const moe_ops_s* o, int dtype, const void* x, long long
 cudaError_t norm_backward(const moe_ops_s* o, int dtype, const void* dy, const void* dh, const void* h,
                           const void* w, const float* rstd, int T, int d, void* dx, float* dw, float* part,
                           cudaStream_t s, long long* n) {
-  const int vpt = steps(d, true), parts = norm_partials(T);
-  if (T > 0) {
-    *n += 1;
-    const bool b = dtype == MOE_BF16;
-    const auto call = vpt == 1 ? (b ? bwd<bf16, 1> : bwd<float, 1>) : (b ? bwd<bf16, 2> : bwd<float, 2>);
-    MOE_TRY(call(dy, dh, h, w, rstd, T, d, dx, dw ? part : nullptr, parts, s));
-  }
+  const int parts = norm_partials(T, d);
+  const bool b = dtype == MOE_BF16;
+  const auto call = d > 8192 ? (b ? bwd<bf16, 2, 1024> : bwd<float, 2, 1024>)
+                    : d > 7168 ? (b ? bwd<bf16, 1, 1024> : bwd<float, 1, 1024>)
+                    : d > 4096 ? (b ? bwd<bf16, 1, 896> : bwd<float, 1, 896>)
+                               : (b ? bwd<bf16, 1, 512> : bwd<float, 1, 512>);
+  *n += 1;
+  MOE_TRY(call(dy, dh, h, w, rstd, T, d, dx, dw ? part : nullptr, parts, s));
   if (!dw) return cudaSuccess;
   *n += 1;
   return launch_pdl(norm_dw_kernel, dim3(ceil_div(d, 32)), dim3(1024), 0, s, (const float*)part, parts, d, dw);

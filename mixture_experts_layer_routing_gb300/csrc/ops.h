@@ -26,7 +26,7 @@ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
 cudaError_t norm_forward(const moe_ops_s* o, int dtype, const void* x, long long ld_x, const void* res,
                          long long ld_res, const void* w, int T, int d, float eps, void* h, void* y, void* q,
                          float* scale, float* rstd, cudaStream_t s, long long* n);
-int norm_partials(int T);            // rows of the backward's weight-gradient partials
+int norm_partials(int T, int d);     // rows of the backward's weight-gradient partials
 cudaError_t norm_backward(const moe_ops_s* o, int dtype, const void* dy, const void* dh, const void* h,
                           const void* w, const float* rstd, int T, int d, void* dx, float* dw, float* part,
                           cudaStream_t s, long long* n);

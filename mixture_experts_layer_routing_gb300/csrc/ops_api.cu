@@ -123,7 +123,7 @@ moe_status moe_norm_forward(moe_ops ops, int dtype, const void* x, long long ld_
 
 moe_status moe_norm_workspace_size(int T, int d, size_t* bytes) {
   CHECK(T >= 0 && d >= 1 && bytes, MOE_ERR_INVALID_ARG);
-  *bytes = sizeof(float) * (size_t)norm_partials(T) * d;
+  *bytes = sizeof(float) * (size_t)norm_partials(T, d) * d;
   return MOE_OK;
 }
 
