@@ -509,7 +509,9 @@ __global__ void __launch_bounds__(kWThreads, 1)
       uint64_t acc[WC / 2];    // pairs of neighbouring columns
 #pragma unroll
       for (int i = 0; i < WC / 2; ++i) acc[i] = 0;
-      for (int left = wide_tile<CG, WGRAD>(p, sm.seg, L, rank).nkb; left > 0 && ok; left -= kWChunk, ++ch) {
+      const WTile t0 = wide_tile<CG, WGRAD>(p, sm.seg, L, rank);
+      const bool some = WGRAD || t0.row0 + quad * 32 < t0.row_end;   // this warp's rows are not all behind the segment
+      for (int left = t0.nkb; left > 0 && ok; left -= kWChunk, ++ch) {
         const int n = min(kWChunk, left);
         if (!WGRAD) ok = warp_wait(sfull0 + 8 * (ch & 1), (ch >> 1) & 1, abort_flag, p.status);
 #pragma unroll 1
@@ -520,6 +522,14 @@ __global__ void __launch_bounds__(kWThreads, 1)
           const float* cs = &sm.sb[WGRAD ? slot : 0][part * WC];
           const float s = WGRAD ? sm.sa[slot][r] : sm.sa[slot][r] * sm.sbh[slot][part * WC / 128];
           tc_fence_after();
+          if (!some) {
+            __syncwarp();
+            if (lane == 0) {
+              if (CG == 1) mbar_arrive(back0 + 8 * b);
+              else arrive_remote(back0 + 8 * b);
+            }
+            continue;
+          }
 #pragma unroll
           for (int c = 0; c < WC; c += 16) {
             uint32_t u[16];
@@ -624,7 +634,7 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
 
 // Cluster of S CTAs per unit (token tile, 128 weight rows); rank r takes K blocks r nkb / S .. (r + 1) nkb / S.
 template <int NT, bool GATHER, typename O>
-__global__ void __launch_bounds__(kNThreads)
+__global__ void __launch_bounds__(kNThreads, 2)
     fp8_narrow_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, GemmParams p,
                       int S) {
   constexpr int ST = n_stages<NT>(), SB = n_stage_bytes<NT>(), COLS = kNBufs * NT;
@@ -667,22 +677,6 @@ __global__ void __launch_bounds__(kNThreads)
     kb0 = (int)((long long)rank * p.nkb / S);
     nkb = (int)((long long)(rank + 1) * p.nkb / S) - kb0;
   }
-  // the token tile's scales for this CTA's K blocks (zero past the segment)
-  for (int i = tid; i < NT * nkb; i += kNThreads) {
-    const int j = i / nkb, kb = i - j * nkb;
-    float s = 0.f;
-    if (row0 + j < row_end) {
-      const int ar = GATHER ? p.row_index[row0 + j] : row0 + j;
-      if ((unsigned)ar < (unsigned)p.a_rows) {
-        s = p.sa[(size_t)ar * p.nkb + kb0 + kb];
-      } else {
-        set_error(p.status, MOE_ERR_DEVICE_INDEX);
-      }
-    }
-    sas[kb * NT + j] = s;
-  }
-  __syncthreads();
-
   float acc[NT];
 #pragma unroll
   for (int j = 0; j < NT; ++j) acc[j] = 0.f;
@@ -745,6 +739,21 @@ __global__ void __launch_bounds__(kNThreads)
     // -------------------------------------------------------------------- epilogue: thread = weight row
     const int quad = warp & 3;
     const uint32_t tq = tmem + ((uint32_t)(quad * 32) << 16);
+    // the token tile's scales for this CTA's K blocks (zero past the segment), while the operands are on their way
+    for (int i = tid - 64; i < NT * nkb; i += 128) {
+      const int j = i / nkb, kb = i - j * nkb;
+      float s = 0.f;
+      if (row0 + j < row_end) {
+        const int ar = GATHER ? p.row_index[row0 + j] : row0 + j;
+        if ((unsigned)ar < (unsigned)p.a_rows) {
+          s = p.sa[(size_t)ar * p.nkb + kb0 + kb];
+        } else {
+          set_error(p.status, MOE_ERR_DEVICE_INDEX);
+        }
+      }
+      sas[kb * NT + j] = s;
+    }
+    asm volatile("bar.sync 1, 128;" ::: "memory");
     const float* sb = p.sb + ((size_t)g * nt + n0 / 128) * p.nkb + kb0;
     float nsb = nkb > 0 ? __ldg(sb) : 0.f;
     for (int kb = 0; kb < nkb; ++kb) {
@@ -1023,7 +1032,11 @@ cudaError_t fp8_matmul(const moe_ops_s* o, const void* a, const float* sa, int a
     p.sa = so;
     p.a_rows = a_rows = M;
   }
-  const int cg = ceil_div(M, G) > WM ? 2 : 1;
+  // Pairs take a K block of 128 rows x 256 columns a SM in 500 ns where single CTAs take 560, but cut segments into
+  // tiles of 256 rows: 12,288 rows of 64 uneven segments (192 on average) x 2,816 x 2,048 take 134 us with pairs and 120
+  // without, 8,192 rows of one segment x 4,096 x 7,168 196 and 214. With half a tile lost a segment the two meet near
+  // 500 rows.
+  const int cg = ceil_div(M, G) >= 512 ? 2 : 1;
   CUtensorMap tm[5];
   if (!make_tmap(&tm[0], a, K, a_rows, BK, WM, 1) || !make_tmap(&tm[1], b, K, (uint64_t)G * N, BK, WN / cg, 1))
     return cudaErrorInvalidValue;

@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(VPT == 4 ? 512 : 1024, 1) norm_fwd_kernel(cons
 
 // A row is held as it is stored (12 registers of bf16 a thread) and unpacked twice, before and after its reduction, so
 // that there is room for the next row, which is loaded a whole row ahead. (Unpacked values in registers and loads just
-// before the reduction: 31 us for 2,368 x 7,168 instead of @.)
+// before the reduction, two CTAs a SM in turn: 32.5 us for 2,368 x 7,168 with the sum of the parts, now 28.8.)
 template <typename T, int VPT, int MAXT>
 __global__ void __launch_bounds__(MAXT, 1) norm_bwd_kernel(const T* dy, const T* dh, const T* __restrict__ h,
                                                            const T* __restrict__ w, const float* __restrict__ rstd,

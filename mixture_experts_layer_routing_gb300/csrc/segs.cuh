@@ -18,10 +18,19 @@ struct SegSmem {
 __device__ __forceinline__ void load_segments(SegSmem& s, const int* __restrict__ off, int G, int M, int tile,
                                               int* status) {
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  if (!off) {
+    if (tid == 0) {
+      s.off[0] = s.tile[0] = 0;
+      s.off[1] = M;
+      s.tile[1] = (M + tile - 1) / tile;
+    }
+    __syncthreads();
+    return;
+  }
   int lo = 0, hi = 0;
   if (tid < G) {
-    lo = off ? off[tid] : 0;
-    hi = off ? off[tid + 1] : M;
+    lo = off[tid];
+    hi = off[tid + 1];
   }
   const bool bad = __syncthreads_or(lo < 0 || lo > hi || hi > M);
   if (bad) {
