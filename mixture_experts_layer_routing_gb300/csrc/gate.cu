@@ -25,7 +25,8 @@ namespace moe {
 namespace {
 
 constexpr int kGateThreads = 1024, kGateWarps = kGateThreads / 32;
-constexpr int kGateTokens = 64;      // tokens of a chunk, at least
+// Tokens of a chunk: all of them up to 64 (then one kernel does it all), else at least 32, a token a warp.
+constexpr int kOneChunk = 64, kChunkTokens = 32;
 constexpr unsigned kFull = 0xffffffffu;
 
 // Order-preserving map of floats (no NaN) to unsigned; 0 is below every float's.
@@ -205,6 +206,18 @@ __device__ __forceinline__ void load_lane(const float* __restrict__ row, int E, 
   }
 }
 
+// 2^x and 1/x, approximate (2 units in the last place), without the steps that keep subnormal values.
+__device__ __forceinline__ float fast_exp(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+  return r;
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // Where a lane's experts lie among the groups (integer divisions, once a warp).
 struct Place {
   int S;          // experts of a group
@@ -331,16 +344,16 @@ __device__ __forceinline__ int gate_token(const float* __restrict__ logits, cons
     sum = 0.f;
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
-      p[q] = __expf(l[q] - m);
+      p[q] = fast_exp(l[q] - m);
       sum += p[q];
     }
     sum = warp_sum(sum);
-    pmax = sum == 0.f ? 0.f : __fdividef(1.f, sum);
+    pmax = sum == 0.f ? 0.f : fast_rcp(sum);
 #pragma unroll
     for (int q = 0; q < PER; ++q) p[q] *= pmax;
   } else {
 #pragma unroll
-    for (int q = 0; q < PER; ++q) p[q] = __fdividef(1.f, 1.f + __expf(-l[q]));
+    for (int q = 0; q < PER; ++q) p[q] = fast_rcp(1.f + fast_exp(-l[q]));
   }
   unsigned key[PER];               // 0: no expert, or of a group that is left out
   float kmax = 0.f;
@@ -661,8 +674,9 @@ __global__ void __launch_bounds__(256) gate_bwd_kernel(const float* __restrict__
 }
 
 inline int chunk_tokens(int T, int sms) {
+  if (T <= kOneChunk) return T;
   const int t = ceil_div(T, sms);
-  return t < kGateTokens ? kGateTokens : t;
+  return t < kChunkTokens ? kChunkTokens : t;
 }
 
 template <int PER>
@@ -680,9 +694,9 @@ cudaError_t bwd(const float* logits, const int* idx, const float* dgate, int T, 
 
 }  // namespace
 
-// One count of every expert for each chunk (at most one chunk for each 64 tokens); a single chunk needs none.
+// One count of every expert for each chunk; a single chunk needs none.
 size_t gate_workspace(const moe_gate_config& c, int T) {
-  return T <= kGateTokens ? 0 : sizeof(int) * (size_t)c.E * ceil_div(T, kGateTokens);
+  return T <= kOneChunk ? 0 : sizeof(int) * (size_t)c.E * ceil_div(T, kChunkTokens);
 }
 
 cudaError_t gate_forward(const moe_ops_s* o, const moe_gate_config& c, const float* logits, const float* bias, int T,
