@@ -89,12 +89,20 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const bf16* __restrict_
   if ((threadIdx.x & 7) == 0) scale[i] = block_scale(m);
 }
 
+// Codes of 16 bf16 values (low halves) by division: blocks of zeros, of NaN, of magnitudes at the ends of the range.
+__device__ __forceinline__ void slow_codes16(const uint32_t (&x)[16], float m, uint32_t (&w)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = pack_codes4(code_value(__uint_as_float(x[4 * i] << 16), m), code_value(__uint_as_float(x[4 * i + 1] << 16), m),
+                       code_value(__uint_as_float(x[4 * i + 2] << 16), m), code_value(__uint_as_float(x[4 * i + 3] << 16), m));
+}
+
 // CTA per 128 tokens and a run of 64-column blocks: rows are read 128 bytes wide into shared memory (the next block's
 // while this one is worked on), a warp takes 16 tokens and a lane two neighbouring columns of them, and the codes go
 // back through shared memory so that a column's 128 leave as one 128-byte line. Segments and row indexes are looked up
 // once a CTA.
-constexpr int kColBlocks = 8;        // column blocks of a CTA
-__global__ void __launch_bounds__(256, 3) quant_cols_kernel(const bf16* __restrict__ src, long long ld, int src_rows,
+constexpr int kColBlocks = 4;        // column blocks of a CTA
+__global__ void __launch_bounds__(256, 4) quant_cols_kernel(const bf16* __restrict__ src, long long ld, int src_rows,
                                                          int T, int C, const int* __restrict__ off, int G,
                                                          const int* __restrict__ row_index, uint8_t* __restrict__ q,
                                                          float* __restrict__ scale, long long Tp, int* status) {
@@ -110,24 +118,25 @@ __global__ void __launch_bounds__(256, 3) quant_cols_kernel(const bf16* __restri
   const int g = segment_of(seg, G, t);
   const int row0 = seg.off[g] + (t - seg.tile[g]) * kScaleBlock, row1 = seg.off[g + 1];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const bf16* rows[4];                 // this thread's rows (null: zeros)
+  int rows[4];                         // this thread's rows (-1: zeros)
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = i * 32 + (tid >> 3);
-    rows[i] = nullptr;
+    rows[i] = -1;
     if (row0 + r < row1) {
       int s = row0 + r;
       if (row_index) s = row_index[s];
-      if ((unsigned)s < (unsigned)src_rows) rows[i] = src + s * ld + (tid & 7) * 8;
+      if ((unsigned)s < (unsigned)src_rows) rows[i] = s;
       else set_error(status, MOE_ERR_DEVICE_INDEX);
     }
   }
   const int c_first = blockIdx.x * kColBlocks * 64, c_end = min(C, c_first + kColBlocks * 64);
   uint4 v4[4];
   const auto fetch = [&](int c0) {
+    const int c = c0 + (tid & 7) * 8;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      v4[i] = rows[i] && c0 + (tid & 7) * 8 < c_end ? *reinterpret_cast<const uint4*>(rows[i] + c0) : make_uint4(0u, 0u, 0u, 0u);
+      v4[i] = rows[i] >= 0 && c < c_end ? *reinterpret_cast<const uint4*>(src + rows[i] * ld + c) : make_uint4(0u, 0u, 0u, 0u);
   };
   fetch(c_first);
   for (int c0 = c_first; c0 < c_end; c0 += 64) {
@@ -150,24 +159,22 @@ __global__ void __launch_bounds__(256, 3) quant_cols_kernel(const bf16* __restri
     const float ma = __uint_as_float(m2 << 16), mb = __uint_as_float(m2 & 0xffff0000u);
     const Divisor da(ma), db(mb);
     uint32_t wa[4], wb[4];
-    const bool plain = da.plain && db.plain;
-    const uint64_t rr = f32x2(da.r, db.r), nm = f32x2(-ma, -mb);
+    if (da.plain && db.plain) {
+      const uint64_t rr = f32x2(da.r, db.r), nm = f32x2(-ma, -mb);
 #pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-      float a[4], b[4];
+      for (int i = 0; i < 16; i += 4) {
+        float a[4], b[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        a[j] = __uint_as_float(x[i + j] << 16);
-        b[j] = __uint_as_float(x[i + j] & 0xffff0000u);
-        if (plain) {
-          f32x2_get(code2(f32x2(a[j], b[j]), rr, nm), a[j], b[j]);
-        } else {
-          a[j] = code_value(a[j], ma);
-          b[j] = code_value(b[j], mb);
-        }
+        for (int j = 0; j < 4; ++j)
+          f32x2_get(code2(f32x2(__uint_as_float(x[i + j] << 16), __uint_as_float(x[i + j] & 0xffff0000u)), rr, nm), a[j], b[j]);
+        wa[i / 4] = pack_codes4(a[0], a[1], a[2], a[3]);
+        wb[i / 4] = pack_codes4(b[0], b[1], b[2], b[3]);
       }
-      wa[i / 4] = pack_codes4(a[0], a[1], a[2], a[3]);
-      wb[i / 4] = pack_codes4(b[0], b[1], b[2], b[3]);
+    } else {
+      slow_codes16(x, ma, wa);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] >>= 16;
+      slow_codes16(x, mb, wb);
     }
     *reinterpret_cast<uint4*>(&out[lane][warp * 16]) = make_uint4(wa[0], wa[1], wa[2], wa[3]);
     *reinterpret_cast<uint4*>(&out[32 + lane][warp * 16]) = make_uint4(wb[0], wb[1], wb[2], wb[3]);
