@@ -1,5 +1,5 @@
 // CPython binding of include/moe_ops.h for torch tensors: checks types, shapes, layouts and devices, allocates
-// outputs that are not given, and forwards to the C ABI. (The same checks written in Python cost a call seven to ten
+// outputs that are not given and scratch (on torch's current stream, which is the call's), and forwards to the C ABI. (The same checks written in Python cost a call seven to ten
 // microseconds, several times what the smallest kernels take.) Every function returns the call's status code.
 #include <Python.h>
 
@@ -166,10 +166,10 @@ PyObject* norm_forward(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
-// dy, h, weight, rstd, dh, out, workspace
+// dy, h, weight, rstd, dh, out
 PyObject* norm_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return guarded([&] {
-    Args a(args, n, 10);
+    Args a(args, n, 9);
     const at::Tensor& dy = a.tensor(3, "dy");
     if (dy.dim() != 2) refuse(PyExc_ValueError, "dy", "two dimensions expected");
     const int dt = dtype_of(dy, "dy");
@@ -184,8 +184,8 @@ PyObject* norm_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
     void* dx = a.output(out, k_dx, "dx", type, {T, d});
     void* dw = a.output(out, k_dw, "dw", at::kFloat, {d});
     at::Tensor ws;
-    void* scratch = (void*)address(a, 9, "workspace");
-    if (dw && !scratch) {
+    void* scratch = nullptr;
+    if (dw) {
       size_t bytes = 0;
       const moe_status st = moe_norm_workspace_size(to_int(T, "dy"), to_int(d, "dy"), &bytes);
       if (st != MOE_OK) return st;
@@ -208,10 +208,10 @@ moe_gate_config gate_config(const Args& a, int i, int64_t E, int64_t k) {
   return c;
 }
 
-// logits, k, bias, router, renorm, route_scale, n_groups, topk_groups, dispatch, out, workspace
+// logits, k, bias, router, renorm, route_scale, n_groups, topk_groups, dispatch, out
 PyObject* gate(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return guarded([&] {
-    Args a(args, n, 14);
+    Args a(args, n, 13);
     const at::Tensor& l = a.tensor(3, "logits");
     if (l.dim() != 2) refuse(PyExc_ValueError, "logits", "two dimensions expected");
     const int64_t T = l.size(0), E = l.size(1), k = a.integer(4);
@@ -231,15 +231,12 @@ PyObject* gate(PyObject*, PyObject* const* args, Py_ssize_t n) {
       off = a.output(out, k_off, "off", at::kInt, {E + 1}, true);
       perm = a.output(out, k_perm, "perm", at::kInt, {T * k}, true);
       inv = a.output(out, k_inv, "inv", at::kInt, {T * k}, true);
-      scratch = (void*)address(a, 13, "workspace");
-      if (!scratch) {
-        size_t bytes = 0;
-        const moe_status st = moe_gate_workspace_size(&c, to_int(T, "logits"), &bytes);
-        if (st != MOE_OK) return st;
-        if (bytes) {
-          ws = at::empty({(int64_t)bytes}, a.opts.dtype(at::kByte));
-          scratch = ws.data_ptr();
-        }
+      size_t bytes = 0;
+      const moe_status st = moe_gate_workspace_size(&c, to_int(T, "logits"), &bytes);
+      if (st != MOE_OK) return st;
+      if (bytes) {
+        ws = at::empty({(int64_t)bytes}, a.opts.dtype(at::kByte));
+        scratch = ws.data_ptr();
       }
     }
     return moe_gate_forward(a.ops, &c, (const float*)l.data_ptr(), (const float*)bias, to_int(T, "logits"),
@@ -352,10 +349,10 @@ PyObject* quant_blocks(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
-// a, a_scale, b, b_scale, off, row_index, out, workspace
+// a, a_scale, b, b_scale, off, row_index, out
 PyObject* fp8_matmul(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return guarded([&] {
-    Args a(args, n, 11);
+    Args a(args, n, 10);
     const at::Tensor &x = a.tensor(3, "a"), &b = a.tensor(5, "b");
     const bool many = a.given(7);
     if (x.dim() != 2 || b.dim() != (many ? 3 : 2))
@@ -377,8 +374,8 @@ PyObject* fp8_matmul(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const int dt = dtype_of(out, "out");
     a.dense(out, "out", out.scalar_type(), {M, N});
     at::Tensor ws;
-    void* scratch = (void*)address(a, 10, "workspace");
-    if (a.given(8) && !scratch) {
+    void* scratch = nullptr;
+    if (a.given(8)) {
       size_t bytes = 0;
       const moe_status st = moe_fp8_matmul_workspace_size(M, G, to_int(K, "a"), 1, &bytes);
       if (st != MOE_OK) return st;

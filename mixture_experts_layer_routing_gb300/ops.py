@@ -111,23 +111,17 @@ class MoeOps:
         except Exception:
             pass
 
-    def _stream(self, stream):
+    def _stream(self, stream=None):
         if stream is None:
             return _current_stream(self._index)
         return stream if isinstance(stream, int) else stream.cuda_stream
 
-    def _scratch(self, stream, size, *args):
-        """Scratch of a call on a stream given by its caller, from the C ABI's size function. The allocator may hand it
-        out again once that stream is past the call. (On the current stream the binding allocates it.)"""
-        if stream is None:
-            return None
-        n = ctypes.c_size_t()
-        _check(size(*args, ctypes.byref(n)), size.__name__)
-        if not n.value:
-            return None
-        ws = torch.empty(n.value, dtype=torch.uint8, device=self.device)
-        ws.record_stream(torch.cuda.ExternalStream(stream, self.device) if isinstance(stream, int) else stream)
-        return ws
+    def _on(self, stream, method, *args, **kw):
+        """The method with `stream` (a torch stream or a cudaStream_t) current, so that outputs and scratch that it
+        allocates belong to that stream too."""
+        s = torch.cuda.ExternalStream(stream, self.device) if isinstance(stream, int) else stream
+        with torch.cuda.stream(s):
+            return method(*args, **kw)
 
     def status(self, stream=None) -> int:
         """moe_ops_get_status: waits for the stream, reads and clears the device status word."""
@@ -148,21 +142,24 @@ class MoeOps:
         allocated): "h" the sum, "y" the norm, "q" and "scale" its 8-bit form, "rstd". Default: y, and h with a
         residual.
         """
+        if stream is not None:
+            return self._on(stream, self.rms_norm, x, weight, residual, eps, want, out)
         if out is None:
             out = dict.fromkeys(want or (("h", "y") if residual is not None else ("y",)))
             if "q" in out or "scale" in out:
                 out.update(q=None, scale=None)
-        s = self._b.norm_forward(self.h, self._index, self._stream(stream), x, weight, residual, eps, out)
+        s = self._b.norm_forward(self.h, self._index, self._stream(), x, weight, residual, eps, out)
         if s:
             _check(s, "moe_norm_forward")
         return out
 
     def rms_norm_backward(self, dy, h, weight, rstd, dh=None, out=None, stream=None) -> dict:
         """moe_norm_backward. Returns {"dx", "dw"} (with `out`: those that it holds)."""
+        if stream is not None:
+            return self._on(stream, self.rms_norm_backward, dy, h, weight, rstd, dh, out)
         if out is None:
             out = dict(dx=None, dw=None)
-        ws = self._scratch(stream, self._lib.moe_norm_workspace_size, *dy.shape) if stream is not None else None
-        s = self._b.norm_backward(self.h, self._index, self._stream(stream), dy, h, weight, rstd, dh, out, ws)
+        s = self._b.norm_backward(self.h, self._index, self._stream(), dy, h, weight, rstd, dh, out)
         if s:
             _check(s, "moe_norm_backward")
         return out
@@ -173,17 +170,15 @@ class MoeOps:
         """moe_gate_forward. logits [T, E] fp32, bias [E] fp32. Returns idx, gate and (dispatch) cnt, off, perm, inv.
 
         With `out` the dispatch is made where it holds "perm"."""
+        if stream is not None:
+            return self._on(stream, self.gate, logits, k, bias, router, renorm, route_scale, n_groups, topk_groups, dispatch, out)
         kind = _ROUTERS[router]
         if out is None:
             out = {}
         else:
             dispatch = "perm" in out
-        ws = None
-        if stream is not None and dispatch:
-            cfg = moe_gate_config(logits.shape[1], k, kind, int(bool(renorm)), route_scale, n_groups, topk_groups)
-            ws = self._scratch(stream, self._lib.moe_gate_workspace_size, ctypes.byref(cfg), logits.shape[0])
-        s = self._b.gate(self.h, self._index, self._stream(stream), logits, k, bias, kind, renorm, route_scale,
-                         n_groups, topk_groups, dispatch, out, ws)
+        s = self._b.gate(self.h, self._index, self._stream(), logits, k, bias, kind, renorm, route_scale,
+                         n_groups, topk_groups, dispatch, out)
         if s:
             _check(s, "moe_gate_forward")
         return out
@@ -191,9 +186,11 @@ class MoeOps:
     def gate_backward(self, logits, idx, dgate, router="softmax", renorm=True, route_scale=1.0, out=None,
                       stream=None) -> dict:
         """moe_gate_backward. Returns {"dlogits"} [T, E] fp32."""
+        if stream is not None:
+            return self._on(stream, self.gate_backward, logits, idx, dgate, router, renorm, route_scale, out)
         if out is None:
             out = {}
-        s = self._b.gate_backward(self.h, self._index, self._stream(stream), logits, idx, dgate, _ROUTERS[router],
+        s = self._b.gate_backward(self.h, self._index, self._stream(), logits, idx, dgate, _ROUTERS[router],
                                   renorm, route_scale, out)
         if s:
             _check(s, "moe_gate_backward")
@@ -202,27 +199,33 @@ class MoeOps:
     # ------------------------------------------------------------ quantisers
     def quant_rows(self, src, swiglu=False, out=None, stream=None):
         """moe_quant_rows. src [T, C] bf16 (swiglu: [T, 2C], gate half then up half) -> (q [T, C], scale)."""
+        if stream is not None:
+            return self._on(stream, self.quant_rows, src, swiglu, out)
         if out is None:
             out = {}
-        s = self._b.quant_rows(self.h, self._index, self._stream(stream), src, swiglu, out)
+        s = self._b.quant_rows(self.h, self._index, self._stream(), src, swiglu, out)
         if s:
             _check(s, "moe_quant_rows")
         return out["q"], out["scale"]
 
     def quant_cols(self, src, off=None, row_index=None, out=None, stream=None):
         """moe_quant_cols. src [rows, C] bf16 -> (q [C, Tp], scale [Tp / 128, C]), segments of tokens by off."""
+        if stream is not None:
+            return self._on(stream, self.quant_cols, src, off, row_index, out)
         if out is None:
             out = {}
-        s = self._b.quant_cols(self.h, self._index, self._stream(stream), src, off, row_index, out)
+        s = self._b.quant_cols(self.h, self._index, self._stream(), src, off, row_index, out)
         if s:
             _check(s, "moe_quant_cols")
         return out["q"], out["scale"]
 
     def quant_blocks(self, w, transpose=False, out=None, stream=None) -> dict:
         """moe_quant_blocks. w [N, K] or [G, N, K] bf16 -> {"q", "scale"} and, transpose, {"qt", "scale_t"}."""
+        if stream is not None:
+            return self._on(stream, self.quant_blocks, w, transpose, out)
         if out is None:
             out = {}
-        s = self._b.quant_blocks(self.h, self._index, self._stream(stream), w, transpose, out)
+        s = self._b.quant_blocks(self.h, self._index, self._stream(), w, transpose, out)
         if s:
             _check(s, "moe_quant_blocks")
         return out
@@ -231,15 +234,12 @@ class MoeOps:
     def fp8_matmul(self, a, a_scale, b, b_scale, off=None, row_index=None, out=None, out_dtype=torch.bfloat16,
                    stream=None):
         """moe_fp8_matmul. a [rows, K], b [N, K] or (with off) [G, N, K], e4m3 with scales -> [M, N]."""
+        if stream is not None:
+            return self._on(stream, self.fp8_matmul, a, a_scale, b, b_scale, off, row_index, out, out_dtype)
         if out is None:
             rows = a.shape[0] if row_index is None else row_index.numel()
             out = torch.empty((rows, b.shape[-2]), dtype=out_dtype, device=self.device)
-        ws = None
-        if stream is not None and row_index is not None:
-            ws = self._scratch(stream, self._lib.moe_fp8_matmul_workspace_size, row_index.numel(),
-                               1 if off is None else off.numel() - 1, a.shape[1], 1)
-        s = self._b.fp8_matmul(self.h, self._index, self._stream(stream), a, a_scale, b, b_scale, off, row_index, out,
-                               ws)
+        s = self._b.fp8_matmul(self.h, self._index, self._stream(), a, a_scale, b, b_scale, off, row_index, out)
         if s:
             _check(s, "moe_fp8_matmul")
         return out
@@ -250,10 +250,12 @@ class MoeOps:
 
         tokens: the number of tokens given to quant_cols (default: the most that Tp holds).
         """
+        if stream is not None:
+            return self._on(stream, self.fp8_wgrad, dct, dct_scale, xt, xt_scale, off, tokens, out, out_dtype)
         if out is None:
             shape = (dct.shape[0], xt.shape[0])
             out = torch.empty(shape if off is None else (off.numel() - 1, *shape), dtype=out_dtype, device=self.device)
-        s = self._b.fp8_wgrad(self.h, self._index, self._stream(stream), dct, dct_scale, xt, xt_scale, off, tokens,
+        s = self._b.fp8_wgrad(self.h, self._index, self._stream(), dct, dct_scale, xt, xt_scale, off, tokens,
                               out)
         if s:
             _check(s, "moe_fp8_wgrad")

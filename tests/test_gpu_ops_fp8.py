@@ -211,6 +211,42 @@ def test_many_tiles_of_weight_gradients(ops):
         near(got[g][torch.from_numpy(rows).cuda()], d.T @ v, np.abs(d).T @ np.abs(v), -(-(hi - lo) // 128))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("N", [77, 264, 1000])
+@pytest.mark.parametrize("cnt", [None, [700, 3, 1300, 37]])
+def test_long_segments(ops, dtype, N, cnt):
+    """Pairs of CTAs: 512 rows a segment and more, with ends inside a tile and inside a warp's 32 rows, and widths that
+    its 128-byte stores divide, that they do not, and that cannot be stored 16 bytes at a time."""
+    K, G = 400, len(cnt) if cnt else 1
+    M = sum(cnt) if cnt else 1111
+    a = rnd(M, K, seed=40, spread=True)
+    b = rnd(G, N, K, seed=41)
+    q, s = ops.quant_rows(a.cuda())
+    wq, ws = map(np.stack, zip(*(oo.quantise_blocks(f64(b[g])) for g in range(G))))
+    bq, bs = torch.from_numpy(wq).float().to(torch.float8_e4m3fn).cuda(), torch.from_numpy(ws).float().cuda()
+    off = make_off(cnt) if cnt else None
+    out = torch.full((M + 8, N), 7.0, dtype=dtype, device="cuda")
+    got = ops.fp8_matmul(q, s, bq if cnt else bq[0], bs if cnt else bs[0], off=None if off is None else off.cuda(),
+                         out=out[:M])
+    A, B = oo.values(f64(q), f64(s)), oo.values(wq, ws, (-2, -1))
+    want, size = oo.matmul(A, B if cnt else B[0], None if off is None else off.tolist())
+    near(got, want, size, 4)
+    assert torch.equal(out[M:], torch.full_like(out[M:], 7.0)) and ops.status() == 0
+
+
+def test_outputs_past_32_bits(ops):
+    """70,000 x 32,768 values: the last rows' offsets pass 2^31."""
+    M, N, K = 70000, 32768, 128
+    q, s, w, _, B = operands(ops, 600, N, K, 0, seed=42)
+    index = torch.arange(M, dtype=torch.int32) % 600
+    got = ops.fp8_matmul(q, s, w["q"], w["scale"], row_index=index.cuda())
+    A = oo.values(f64(q), f64(s))
+    for m in (0, 40000, 65535, 65536, 69999):
+        near(got[m:m + 1], A[m % 600][None] @ B.T, np.abs(A[m % 600][None]) @ np.abs(B).T, 1)
+    del got
+    assert ops.status() == 0
+
+
 def test_rows_of_no_segment_stay(ops):
     q, s, w, A, B = operands(ops, 300, 128, 256, 3, seed=8)
     for off in ([0, 10, 12, 40], [0, 100, 230, 260]):

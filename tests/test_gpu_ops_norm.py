@@ -166,6 +166,18 @@ def test_no_rows(ops):
     assert torch.equal(dw, torch.zeros_like(dw))
 
 
+def test_offsets_past_32_bits(ops):
+    T, d = 300000, 8192
+    x = torch.ones(T, d, dtype=torch.bfloat16, device="cuda")
+    x[-3:] = torch.randn(3, d, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).cuda()
+    w = torch.ones(d, dtype=torch.bfloat16, device="cuda")
+    y = ops.rms_norm(x, w, want=("y", "rstd"))
+    check_forward({k: v[-4:] for k, v in y.items()}, x[-4:], None, w, 1e-6, "bf16")
+    g = ops.rms_norm_backward(y["y"], x, w, y["rstd"], out=dict(dx=None))["dx"]
+    dx, _, size, _ = oo.rms_norm_backward(f64(y["y"][-4:]), f64(x[-4:]), f64(w), f64(y["rstd"][-4:]))
+    assert np.all(np.abs(f64(g[-4:]) - dx) <= HALF["bf16"] * np.abs(dx) + 2 * SUMS * size)
+
+
 def test_another_stream_graph_and_repeats(ops):
     x, r, w = make(200, 1024, "bf16", 13)
     want = ops.rms_norm(x, w, r, want=("h", "y", "q", "rstd"))
