@@ -4,15 +4,17 @@
 // MMAs of K = 32 into one of several partial accumulators), read back, and added with its scales to sums that live
 // in registers: c += (sa sb) * partial, in fp32. Two kernels:
 //
-// wide: many rows. CTA tile 128 rows x 256 columns, one CTA a SM, persistent. TMEM holds two partials of 256
-//   columns (all 512), so that the tensor core works on one while eight epilogue warps (128 sums a thread) take
-//   in the other. Per K block the MMAs take 512 cycles and the 32,768 FMAs of the sums 256.
+// wide: many rows. 128 rows x 256 columns a CTA, one CTA a SM, persistent, two CTAs on one tile of 256 rows where
+//   segments are long. TMEM holds two partials of 256 columns (all 512), so that the tensor core works on one while
+//   eight epilogue warps (128 sums a thread) take in the other. Per K block the MMAs take 512 cycles, the 32,768 FMAs
+//   of the sums 256 and the partial's way out of TMEM about as long as the MMAs.
 // narrow: few rows a segment (decoding). The operands change places: 128 weight rows are the MMA's M and 16 to 64
 //   token rows its N, so that the MMA's M is filled by weights and a weight byte is read once. The reduction is
 //   split over the CTAs of a cluster where tiles alone would not fill the GPU; the parts are added through
 //   distributed shared memory in rank order. Bound by the weights' bytes.
 //
-// Operands come by TMA (128-byte swizzle); gathered rows (row_index) by TMA gathers of four rows. Every wait is
+// Operands come by TMA (128-byte swizzle); gathered rows (row_index) by TMA gathers of four rows in the narrow kernel,
+// and put in order by a kernel of their own before the wide one, which reads a row once a column tile. Every wait is
 // bounded: a role that gives up sets the abort flag and the others leave their loops too.
 #include "common.cuh"
 #include "launch.cuh"
@@ -632,7 +634,11 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
   return v;
 }
 
-// Cluster of S CTAs per unit (token tile, 128 weight rows); rank r takes K blocks r nkb / S .. (r + 1) nkb / S.
+// Cluster of S CTAs per unit (token tile, 128 weight rows); rank r takes K blocks r nkb / S .. (r + 1) nkb / S. Two CTAs
+// a SM, with rings of 5 stages (90 KB) for 16 tokens: eight in one CTA a SM were slower (below: 18.9 and 173 us).
+// Measured: 128 rows over 32 experts of 7168 x 4096 in 146-150 us (93-95% of the HBM copy rate); one row x 4096 x 7168
+// in 7.9 us, of which 4.3 are its bytes at that rate and the rest the start, the first copy and the joining of 8 parts
+// (split in 4: 9.8, in 2: 14.8).
 template <int NT, bool GATHER, typename O>
 __global__ void __launch_bounds__(kNThreads, 2)
     fp8_narrow_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, GemmParams p,
@@ -899,7 +905,8 @@ cudaError_t pick_wide(const moe_ops_s* o, int cg, const CUtensorMap* tm, GemmPar
   return fp32 ? launch_wide<2, WGRAD, float>(o, tm, p, units, s) : launch_wide<2, WGRAD, bf16>(o, tm, p, units, s);
 }
 
-// Rows of a (and their scales) in the order of c's rows, one warp a row; an index out of range gives zeros.
+// Rows of a (and their scales) in the order of c's rows, one warp a row; an index out of range gives zeros. Most reads
+// hit L2: 12,288 rows of 2,048 bytes in 8 us, 50 MB moved.
 __global__ void __launch_bounds__(256) gather_rows_kernel(const uint8_t* __restrict__ a, const float* __restrict__ sa,
                                                           const int* __restrict__ row_index, int M, int a_rows, int K,
                                                           int nkb, uint8_t* __restrict__ out, float* __restrict__ so,
@@ -953,8 +960,18 @@ int out_vec(const void* c, long long n, int fp32) {
   const uintptr_t at = (uintptr_t)c;
   return bytes % 32 == 0 && at % 32 == 0 ? 32 : bytes % 16 == 0 && at % 16 == 0 ? 16 : 0;
 }
-// Few rows a segment: the weights' bytes decide, and the narrow kernel fills its MMAs with them.
-bool use_narrow(int M, int G, int K) { return ceil_div(M, G) <= 64 && ceil_div(K, BK) <= kNarrowMaxKb; }
+// Rows a segment up to which the narrow kernel is the faster one. Where the wide kernel's tiles fill the GPU, it too
+// streams the weights, reads them once for up to 128 rows and loses nothing on uneven segments: 64 uneven segments of
+// 2,816 x 2,048 take 80.5 us (narrow) and 81.6 (wide) with 4 rows each on average, 82.6 both with 8, 94.9 and 83.6 with
+// 24; 32 of 7,168 x 4,096 156 and 159, 166 and 164, 191 and 166. Where they do not fill it, the narrow kernel has more
+// tiles and splits the reduction: one segment of 4,096 x 7,168 (16 wide tiles) 17 and 33 with 32 rows, 21 and 35 with
+// 64; 16,384 x 7,168 (64 tiles) 38 and 44, 50 and 44. (Cold, with an event's 2 us.)
+constexpr int kNarrowAlways = 8, kNarrowHalf = 32, kNarrowMost = 64;
+bool use_narrow(int M, int G, int N, int K, int sms) {
+  const long long tiles = (long long)(G < M ? G : M) * ceil_div(N, WN);
+  const int rows = tiles >= sms ? kNarrowAlways : 4 * tiles >= sms ? kNarrowHalf : kNarrowMost;
+  return ceil_div(M, G) <= rows && ceil_div(K, BK) <= kNarrowMaxKb;
+}
 
 }  // namespace
 
@@ -985,7 +1002,8 @@ cudaError_t fp8_init(int* pairs) {
 }
 
 size_t fp8_matmul_workspace(int M, int G, int K, bool gathered) {
-  if (!gathered || use_narrow(M, G, K)) return 0;
+  // (whatever N is)
+  if (!gathered || (ceil_div(M, G) <= kNarrowAlways && ceil_div(K, BK) <= kNarrowMaxKb)) return 0;
   return (size_t)M * K + 16 + sizeof(float) * (size_t)M * ceil_div(K, BK);
 }
 
@@ -1006,7 +1024,9 @@ cudaError_t fp8_matmul(const moe_ops_s* o, const void* a, const float* sa, int a
   p.c = c;
   p.status = o->status;
   CUtensorMap ta, tb;
-  if (use_narrow(M, G, K)) {
+  if (use_narrow(M, G, N, K, o->sms)) {
+    // Tokens a tile, with room for uneven segments: one segment of 4,096 x 7,168 with 32 rows takes 21, 19 and 17 us
+    // with tiles of 16, 32 and 64, 64 segments of 2,816 x 2,048 with 8 rows each 83, 85 and 91.
     const int avg = ceil_div(M, G), NT = avg <= 12 ? 16 : avg <= 24 ? 32 : 64;
     if (!make_tmap(&ta, a, K, a_rows, BK, row_index ? 1 : NT, 1) ||
         !make_tmap(&tb, b, K, (uint64_t)G * N, BK, 128, 1))
@@ -1014,6 +1034,8 @@ cudaError_t fp8_matmul(const moe_ops_s* o, const void* a, const float* sa, int a
     const int nt = ceil_div(N, 128);
     // token tiles: at most one that is not full for each segment that holds a row
     const long long most = (G < M ? G : M), units = (M / NT + most < M ? M / NT + most : M) * (long long)nt;
+    // Split while all parts run at once, two CTAs a SM: one row x 16,384 x 2,048 (128 tiles) takes 15 us whole and 17
+    // split in 2, 16,384 x 7,168 36 and 33, 4,096 x 7,168 (32 tiles) 27, 21, 17 and 17 split in 1, 2, 4 and 8.
     int S = 1;
     while (S < 8 && 2 * S <= p.nkb && units * S * 2 <= 2 * o->sms) S *= 2;
     *n += 1;

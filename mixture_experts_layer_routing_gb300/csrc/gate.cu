@@ -13,6 +13,10 @@
 // The dispatch: tokens are cut into chunks, one CTA each, at most one chunk a SM. The selecting CTA counts its
 // chunk's experts. With one chunk it also writes offsets and permutation; otherwise a second kernel adds up the
 // chunk counts before its own chunk and ranks the chunk's assignments. Integers only, the same in every run.
+//
+// Measured, 8192 tokens of 256 experts in 8 groups: 22 us, 16 of them the selection (63% of the issue slots, some 1,100
+// instructions a token; its 8.4 MB would take 1.3) and the rest the dispatch. With 64-bit keys for all 50 us. Four
+// tokens in 4.6 us.
 #include <cfloat>
 #include <cmath>
 
@@ -25,8 +29,11 @@ namespace moe {
 namespace {
 
 constexpr int kGateThreads = 1024, kGateWarps = kGateThreads / 32;
-// Tokens of a chunk: all of them up to 64 (then one kernel does it all), else at least 32, a token a warp.
-constexpr int kOneChunk = 64, kChunkTokens = 32;
+// Tokens of a chunk: all of them up to 16 (then one kernel does it all), else 8 in up to 64 chunks and 32, a token a
+// warp, before there are more. A warp with a second token, or many of them on one SM, cost more than a second launch
+// and its reading of all chunks' counts: 64 tokens of 256 experts take 13.7 us in one chunk, 9.3 in chunks of 32 and
+// 6.4 of 8, 512 tokens 17.0 in chunks of 32 and 14.0 of 8, but 2,048 tokens 17.4 and 18.2, of 64 experts 9.4 and 11.0.
+constexpr int kOneChunk = 16, kChunkLeast = 8, kChunkTokens = 32, kFewChunks = 64;
 constexpr unsigned kFull = 0xffffffffu;
 
 // Order-preserving map of floats (no NaN) to unsigned; 0 is below every float's.
@@ -673,10 +680,14 @@ __global__ void __launch_bounds__(256) gate_bwd_kernel(const float* __restrict__
     if (e0 + q < c.E) dlogits[(size_t)t * c.E + e0 + q] = row[q];
 }
 
+inline int least_tokens(int T) {
+  const int t = ceil_div(T, kFewChunks);
+  return t < kChunkLeast ? kChunkLeast : t < kChunkTokens ? t : kChunkTokens;
+}
 inline int chunk_tokens(int T, int sms) {
   if (T <= kOneChunk) return T;
-  const int t = ceil_div(T, sms);
-  return t < kChunkTokens ? kChunkTokens : t;
+  const int least = least_tokens(T), t = ceil_div(T, sms);
+  return t < least ? least : t;
 }
 
 template <int PER>
@@ -696,7 +707,7 @@ cudaError_t bwd(const float* logits, const int* idx, const float* dgate, int T, 
 
 // One count of every expert for each chunk; a single chunk needs none.
 size_t gate_workspace(const moe_gate_config& c, int T) {
-  return T <= kOneChunk ? 0 : sizeof(int) * (size_t)c.E * ceil_div(T, kChunkTokens);
+  return T <= kOneChunk ? 0 : sizeof(int) * (size_t)c.E * ceil_div(T, least_tokens(T));
 }
 
 cudaError_t gate_forward(const moe_ops_s* o, const moe_gate_config& c, const float* logits, const float* bias, int T,

@@ -1,6 +1,6 @@
 // Quantisers of include/moe_ops.h: e4m3 codes with one fp32 scale for 128 values, along rows, along the token axis
 // (transposed, for the weights' gradient) and in 128 x 128 blocks (weights, optionally transposed as well).
-// All read each value once; bound by HBM.
+// All read each value once; along rows HBM bounds them, along the token axis the instructions.
 #include "fp8_quant.cuh"
 #include "launch.cuh"
 #include "segs.cuh"
@@ -35,6 +35,7 @@ __global__ void __launch_bounds__(256) quant_swiglu_kernel(const bf16* __restric
 
 // Rows of bf16 values, eight lanes a block of 128 (16 values each, so that what a block needs once, its maximum, its
 // reciprocal and its scale, is shared by more of them: with 8 values a lane the kernel was bound by its instructions).
+// 12,288 x 2816 in 17.4 us, 104 MB at 6.0 TB/s.
 __global__ void __launch_bounds__(256) quant_rows_kernel(const bf16* __restrict__ src, long long ld, unsigned items,
                                                          int nb, int C, uint8_t* __restrict__ q,
                                                          float* __restrict__ scale) {
@@ -100,7 +101,8 @@ __device__ __forceinline__ void slow_codes16(const uint32_t (&x)[16], float m, u
 // CTA per 128 tokens and a run of 64-column blocks: rows are read 128 bytes wide into shared memory (the next block's
 // while this one is worked on), a warp takes 16 tokens and a lane two neighbouring columns of them, and the codes go
 // back through shared memory so that a column's 128 leave as one 128-byte line. Segments and row indexes are looked up
-// once a CTA.
+// once a CTA. 12,288 x 2816 of 64 segments in 29 us, 12,288 gathered rows x 2048 in 20 us: bound by instructions and the
+// three barriers a block (58% of the issue slots), not by HBM (32%).
 constexpr int kColBlocks = 4;        // column blocks of a CTA
 __global__ void __launch_bounds__(256, 4) quant_cols_kernel(const bf16* __restrict__ src, long long ld, int src_rows,
                                                          int T, int C, const int* __restrict__ off, int G,
@@ -195,7 +197,7 @@ __global__ void __launch_bounds__(256, 4) quant_cols_kernel(const bf16* __restri
   }
 }
 
-// CTA per 128 x 128 block of one matrix.
+// CTA per 128 x 128 block of one matrix, for weights, which are quantised once.
 __global__ void __launch_bounds__(256) quant_blocks_kernel(const bf16* __restrict__ w, int N, int K,
                                                            uint8_t* __restrict__ q, float* __restrict__ scale,
                                                            uint8_t* __restrict__ qt, float* __restrict__ scale_t) {

@@ -178,6 +178,38 @@ def test_many_experts(ops, per):
     assert ops.status() == 0
 
 
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("G,most,N,K", [(40, 33, 1100, 272), (160, 24, 72, 400), (20, 130, 2056, 144)])
+def test_few_rows_of_many_tiles(ops, G, most, N, K, gather):
+    """Short segments whose weights alone fill the GPU with tiles of the wide kernel."""
+    cnt = np.random.default_rng(G).integers(0, most, G).tolist()
+    M = sum(cnt)
+    rows = 50 if gather else M
+    b = rnd(G, N, K, seed=51)
+    q, s = ops.quant_rows(rnd(rows, K, seed=50, spread=True).cuda())
+    wq, ws = map(np.stack, zip(*(oo.quantise_blocks(f64(b[g])) for g in range(G))))   # (widths that 8 does not divide)
+    w = dict(q=torch.from_numpy(wq).float().to(torch.float8_e4m3fn).cuda(), scale=torch.from_numpy(ws).float().cuda())
+    A, B = oo.values(f64(q), f64(s)), oo.values(wq, ws, (-2, -1))
+    off = make_off(cnt)
+    index = torch.randint(0, rows, (M,), generator=torch.Generator().manual_seed(6), dtype=torch.int32)
+    got = ops.fp8_matmul(q, s, w["q"], w["scale"], off=off.cuda(), row_index=index.cuda() if gather else None)
+    want, size = oo.matmul(A, B, off.tolist(), index.long().numpy() if gather else None)
+    near(got, want, size, -(-K // 128))
+    assert ops.status() == 0
+
+
+@pytest.mark.parametrize("M", [8, 32, 33, 64])
+@pytest.mark.parametrize("gather", [False, True])
+def test_few_rows_of_one_wide_matrix(ops, M, gather):
+    rows = 50 if gather else M
+    q, s, w, A, B = operands(ops, rows, 10016, 272, 0, seed=51)
+    index = torch.randint(0, rows, (M,), generator=torch.Generator().manual_seed(7), dtype=torch.int32)
+    got = ops.fp8_matmul(q, s, w["q"], w["scale"], row_index=index.cuda() if gather else None)
+    want, size = oo.matmul(A[index.long().numpy()] if gather else A, B)
+    near(got, want, size, 3)
+    assert ops.status() == 0
+
+
 @pytest.mark.parametrize("M,N,K,cnt", [(100, 40000, 2048, None), (700, 16384, 2176, None),
                                        (1500, 8192, 1536, [200, 0, 700, 130, 470])])
 def test_many_tiles_a_cta(ops, M, N, K, cnt):

@@ -70,6 +70,13 @@ def test_many_chunks(ops):
         assert np.array_equal(out[n].cpu().numpy(), want), n
 
 
+@pytest.mark.parametrize("T", [16, 17, 24, 40, 63, 64, 65, 511, 513, 1030, 2049])
+@pytest.mark.parametrize("E,k", [(64, 6), (256, 8)])
+def test_chunks_of_several_sizes(ops, T, E, k):
+    g = torch.Generator().manual_seed(T + E)
+    check(ops, 1.5 * torch.randn(T, E, generator=g), None, k)
+
+
 @pytest.mark.parametrize("router", ["softmax", "sigmoid"])
 def test_equal_and_nearly_equal_keys(ops, router):
     """Ties go to the lower index; keys closer than 32 bits can tell are decided as in 64."""
