@@ -368,7 +368,7 @@ __device__ __forceinline__ int gate_token(const float* __restrict__ logits, cons
   for (int q = 0; q < PER; ++q) {
     const float k = p[q] + b[q];
     const bool on = l[q] > -INFINITY && k == k;      // neither masked nor NaN
-    kmax = fmaxf(kmax, on ? fabsf(k) : 0.f);
+    kmax = fmaxf(kmax, on && fabsf(k) <= FLT_MAX ? fabsf(k) : 0.f);   // (infinite ones are exact)
     key[q] = order_of(on ? fmaxf(k, -FLT_MAX) : -FLT_MAX);
   }
   if (e0 + PER > c.E) {
@@ -412,7 +412,8 @@ __device__ __forceinline__ int gate_token(const float* __restrict__ logits, cons
   const bool near = lane < c.k && next && !(of_order(mine) - of_order(next) > tau);
   const bool sure = !__any_sync(kFull, near);
   const unsigned kth = __shfl_sync(kFull, mine, c.k - 1);   // 0: fewer than k different keys
-  // Candidates: the selection, or where it is not sure every expert whose key may reach it.
+  // Candidates: the selection, or where it is not sure every expert whose key may reach it. (tau is finite, so an
+  // infinite kth stays what it is.)
   const unsigned least = sure || !kth ? kth : order_of(of_order(kth) - tau);
   int n = 0;
 #pragma unroll
@@ -428,7 +429,7 @@ __device__ __forceinline__ int gate_token(const float* __restrict__ logits, cons
   }
   __syncwarp();
   int e;
-  if (!groups_sure || n > 32) {
+  if (!groups_sure || n > 32 || n < c.k) {   // (never fewer than k; a lane below takes only an index that was written)
     e = select_exact<PER>(logits, bias, m, c);
   } else {
     e = lane < n ? (int)scr[lane] : 0;

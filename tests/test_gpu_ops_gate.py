@@ -215,3 +215,32 @@ def test_python_refusals(ops):
         ops.gate(l, 4, n_groups=7)
     with pytest.raises(ValueError):
         ops.gate_backward(l, torch.zeros(4, 2, dtype=torch.int32).cuda(), torch.zeros(4, 3).cuda())
+
+
+BIASES = {
+    "one +inf": lambda b: b.index_fill_(0, torch.tensor([37]), float("inf")),
+    "three +inf": lambda b: b.index_fill_(0, torch.tensor([2, 37, 38]), float("inf")),
+    "all +inf": lambda b: b.fill_(float("inf")),
+    "one -inf": lambda b: b.index_fill_(0, torch.tensor([5]), -float("inf")),
+    "few left of -inf": lambda b: b[:-3].fill_(-float("inf")),
+    "all -inf": lambda b: b.fill_(-float("inf")),
+    "+inf and -inf": lambda b: (b[::2].fill_(-float("inf")), b[9:10].fill_(float("inf"))),
+    "masks of -1e9": lambda b: b[1::3].fill_(-1e9),
+    "few left of -1e9": lambda b: b[4:].fill_(-1e9),
+    "one of 1e9": lambda b: b[11:12].fill_(1e9),
+    "lowest value": lambda b: b[::5].fill_(torch.finfo(torch.float32).min),
+    "largest value": lambda b: b[7:9].fill_(torch.finfo(torch.float32).max),
+}
+
+
+@pytest.mark.parametrize("name", BIASES)
+@pytest.mark.parametrize("router", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,kept", [(40, 1, 1), (64, 8, 3), (256, 1, 1), (256, 8, 4), (60, 5, 2)])
+@pytest.mark.parametrize("k", [1, 2, 8])
+def test_infinite_and_masking_biases(ops, name, router, E, groups, kept, k):
+    """A bias of +inf puts an expert first, one of -inf (or the masks' usual numbers) behind the others."""
+    g = torch.Generator().manual_seed(E + k)
+    logits, bias = 1.5 * torch.randn(37, E, generator=g), 0.05 * torch.randn(E, generator=g)
+    BIASES[name](bias)
+    out = check(ops, logits, bias, k, router, n_groups=groups, topk_groups=kept)
+    assert 0 <= out["idx"].min().item() and out["idx"].max().item() < E
