@@ -434,7 +434,7 @@ __device__ __forceinline__ int gate_token(const float* __restrict__ logits, cons
   } else {
     e = lane < n ? (int)scr[lane] : 0;
     int rank = 0;
-    if (sure && n == c.k) {
+    if (sure && kth && n == c.k) {   // k different keys (equal ones, also where just k experts are left, go by index)
       const unsigned k1 = lane < n ? scr[32 + lane] : 0u;
       for (int i = 0; i < n; ++i) rank += scr[32 + i] > k1;
     } else {

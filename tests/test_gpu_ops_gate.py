@@ -244,3 +244,17 @@ def test_infinite_and_masking_biases(ops, name, router, E, groups, kept, k):
     BIASES[name](bias)
     out = check(ops, logits, bias, k, router, n_groups=groups, topk_groups=kept)
     assert 0 <= out["idx"].min().item() and out["idx"].max().item() < E
+
+
+@pytest.mark.parametrize("router", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,groups,kept", [(2, 2, 1, 1), (4, 4, 1, 1), (8, 8, 1, 1), (8, 4, 2, 1), (32, 8, 8, 2),
+                                             (256, 8, 32, 1)])
+def test_as_many_experts_as_are_selected(ops, router, E, k, groups, kept):
+    """Every expert (of the groups kept) is selected, in the order of its key; equal keys, masked ones among them, by
+    index."""
+    g = torch.Generator().manual_seed(E)
+    logits = torch.randint(-2, 3, (200, E), generator=g).float()
+    logits[100:150][torch.rand(50, E, generator=g) < 0.4] = -float("inf")
+    logits[0, :4] = torch.tensor([0.0, 1.0, 1.0, 0.0])[:E]
+    out = check(ops, logits, None, k, router, n_groups=groups, topk_groups=kept)
+    assert all(len(set(row)) == k for row in out["idx"].tolist())
