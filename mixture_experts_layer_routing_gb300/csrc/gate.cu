@@ -3,20 +3,22 @@
 //
 // One warp a token; lane i holds the PER consecutive experts i*PER .. (E <= 32 PER). Keys are computed in 32 bits
 // with fast exponentials and kept as unsigned integers in the floats' order, so a round of the top-k is one redux
-// over the lanes and a masked maximum over a lane's own keys. A bound of their error (tau) decides whether the
-// outcome could differ from that of 64-bit keys: every gap that the selection rests on (between neighbours of the
-// sorted selection, to the first expert left out, between the worst group kept and the best left out) has to exceed
-// it. Where one does not, the experts that may belong to the selection get 64-bit keys, one a lane (double precision
-// runs at about 1/64 of the fp32 rate here, so not every expert's). The gates are computed from the selected logits
-// alone, in full 32-bit precision.
+// over the lanes and a masked maximum over a lane's own keys. A bound of each key's error (KeyBound) decides whether
+// the outcome could differ from that of 64-bit keys: the intervals of neighbours of the sorted selection, of its last
+// and the first expert left out, and of the worst group kept and the best left out must not meet. Where two do, the
+// experts that may belong to the selection get 64-bit keys, one a lane (double precision runs at about 1/64 of the fp32
+// rate here, so not every expert's). The gates are computed from the selected logits with expf; a softmax's
+// denominator is the sum of the fast exponentials, up to 20 units of 2^-24 off, which renormalised gates cancel.
 //
 // The dispatch: tokens are cut into chunks, one CTA each, at most one chunk a SM. The selecting CTA counts its
 // chunk's experts. With one chunk it also writes offsets and permutation; otherwise a second kernel adds up the
 // chunk counts before its own chunk and ranks the chunk's assignments. Integers only, the same in every run.
 //
 // Measured, 8192 tokens of 256 experts in 8 groups: 22 us, 16 of them the selection (63% of the issue slots, some 1,100
-// instructions a token; its 8.4 MB would take 1.3) and the rest the dispatch. With 64-bit keys for all 50 us. Four
-// tokens in 4.6 us.
+// instructions a token; its 8.4 MB would take 1.3) and the rest the dispatch. With 64-bit keys for all 183 us. The
+// same with an expert or 32 masked by the bias, logits around -10, or peaked softmax rows: 18-22 us. Sigmoid logits
+// around 10 without a bias need 64 bits in most rows, their scores being within some 2^-24 of 1 and each other: 74 us.
+// Four tokens in 4.6 us.
 #include <cfloat>
 #include <cmath>
 
@@ -244,18 +246,41 @@ struct Place {
   }
 };
 
-// The groups that stay, a bit each. Where their choice rests on a gap that is not above the error of a score (a sum of
-// two keys), by 64-bit keys of the experts that can be one of their group's two best; sure turns false if these are
-// more than a warp holds. scr: 32 words.
+// How far a key may be from the one computed in 64 bits, with u = 2^-24. A score is off by its exponential (2^-22, and
+// a rounded argument: 2.3 |x| u) and three roundings or fewer behind it, that is by 10 u + 2 u log2(largest / score) of
+// itself, half of which is to spare; a sigmoid's largest score is 1, and the denominator that all scores of a softmax
+// share does not move their order. Without a bias the key is the score: the bound is the key's own, so that small
+// scores beside a large one are told apart. With one, scores of any size can stand behind a key: base is the bound of
+// the row's largest score (32 u of it with the softmax's denominator), and an addition and its comparison cost u |key|
+// each. A key plus its bound grows with the key, so only neighbours need to be compared, whatever lies below them
+// (a mask of -1e9, say). Infinite keys come from an infinite bias, and the lowest value stands for experts that are
+// masked: they have no error.
+struct KeyBound {
+  bool biased;
+  float base, top;     // top: log2 of the largest score
+  __device__ __forceinline__ static float score(float p, float top) {
+    const float doublings = fmaxf(top - __log2f(fmaxf(p, FLT_MIN)), 0.f);
+    return p * (0x1.4p-21f + 0x1p-23f * doublings) + 0x1p-125f;     // (scores below 2^-126 are taken for 0)
+  }
+  __device__ __forceinline__ float operator()(float k) const {
+    if (!(fabsf(k) < FLT_MAX)) return 0.f;
+    return biased ? base + 0x1p-23f * fabsf(k) : score(k, top);
+  }
+};
+
+// The groups that stay, a bit each. Where their choice rests on scores (sums of two keys) whose bounds meet, by 64-bit
+// keys of the experts that can be one of their group's two best; sure turns false if these are more than a warp holds.
+// scr: 32 words.
 template <int PER>
 __device__ __forceinline__ unsigned kept_groups(const unsigned (&key)[PER], const moe_gate_config& c,
-                                                const Place& at_, float tau, const float* __restrict__ logits,
-                                                const float* __restrict__ bias, float m, unsigned* scr, bool& sure) {
+                                                const Place& at_, const KeyBound& bound,
+                                                const float* __restrict__ logits, const float* __restrict__ bias,
+                                                float m, unsigned* scr, bool& sure) {
   const int lane = threadIdx.x & 31, e0 = lane * PER, S = at_.S, L = at_.step;
   // Groups that fill a power of two of lanes: all at once, every lane with its own group's. Others: group by group,
   // lane g with group g's.
   const bool fills = at_.fills;
-  float score = -INFINITY, second = -INFINITY;
+  float first = -FLT_MAX, second = -FLT_MAX;
   if (fills) {
     unsigned a = 0u, b = 0u;
 #pragma unroll
@@ -269,8 +294,8 @@ __device__ __forceinline__ unsigned kept_groups(const unsigned (&key)[PER], cons
       a = max(a, oa);
     }
     if (e0 < c.E) {
+      first = of_order(a);
       second = of_order(S > 1 ? b : a);
-      score = S > 1 ? of_order(a) + second : second;
     }
   } else {
     for (int g = 0; g < c.n_groups; ++g) {
@@ -283,18 +308,23 @@ __device__ __forceinline__ unsigned kept_groups(const unsigned (&key)[PER], cons
         }
       }
       const unsigned best = __reduce_max_sync(kFull, a);
-      float s = of_order(best), s2 = s;
+      unsigned other = best;
       if (S > 1) {
         const int owner = __ffs(__ballot_sync(kFull, a == best)) - 1;
-        s2 = of_order(__reduce_max_sync(kFull, lane == owner ? b : a));
-        s += s2;
+        other = __reduce_max_sync(kFull, lane == owner ? b : a);
       }
       if (lane == g) {
-        score = s;
-        second = s2;
+        first = of_order(best);
+        second = of_order(other);
       }
     }
   }
+  // (sums past the finite range are pulled back to its end, and the bounds there reach over it)
+  const float score = S > 1 && first <= FLT_MAX ? fminf(fmaxf(first + second, -FLT_MAX), FLT_MAX) : first;
+  const float off2 = bound(second);
+  const float off = S > 1 && first <= FLT_MAX ? bound(first) + off2 + 0x1p-22f * fabsf(score) : bound(first);
+  // a masked expert's 64-bit key is far below the lowest value
+  const float low = second == -FLT_MAX ? -INFINITY : score - off, high = score + off;
   const int step = at_.step, g = at_.mine;
   int rank = 0;
   for (int i = 0; i < c.n_groups; ++i) {
@@ -302,8 +332,8 @@ __device__ __forceinline__ unsigned kept_groups(const unsigned (&key)[PER], cons
     rank += other > score || (other == score && i < g);
   }
   const bool in = g < c.n_groups, kept = in && rank < c.topk_groups;
-  const float worst = -lanes_max(kept ? -score : -INFINITY), best = lanes_max(in && !kept ? score : -INFINITY);
-  if (worst - best > 3 * tau) {
+  const float worst = -lanes_max(kept ? -low : -INFINITY), best = lanes_max(in && !kept ? high : -INFINITY);
+  if (worst > best) {
     // bit g of a ballot of the lanes that speak for the groups
     const unsigned mask = __ballot_sync(kFull, kept && lane == g * step);
     if (step == 1) return mask;
@@ -315,7 +345,7 @@ __device__ __forceinline__ unsigned kept_groups(const unsigned (&key)[PER], cons
 #pragma unroll
   for (int q = 0; q < PER; ++q) {
     const int mine = min((e0 + q) / S, c.n_groups - 1);
-    const float limit = __shfl_sync(kFull, second, mine * step) - tau;
+    const float limit = __shfl_sync(kFull, second - 3 * off2, mine * step);
     const bool cand = key[q] && !(of_order(key[q]) < limit);
     const unsigned mask = __ballot_sync(kFull, cand);
     const int at = n + __popc(mask & ((1u << lane) - 1u));
@@ -363,12 +393,10 @@ __device__ __forceinline__ int gate_token(const float* __restrict__ logits, cons
     for (int q = 0; q < PER; ++q) p[q] = fast_rcp(1.f + fast_exp(-l[q]));
   }
   unsigned key[PER];               // 0: no expert, or of a group that is left out
-  float kmax = 0.f;
 #pragma unroll
   for (int q = 0; q < PER; ++q) {
     const float k = p[q] + b[q];
     const bool on = l[q] > -INFINITY && k == k;      // neither masked nor NaN
-    kmax = fmaxf(kmax, on && fabsf(k) <= FLT_MAX ? fabsf(k) : 0.f);   // (infinite ones are exact)
     key[q] = order_of(on ? fmaxf(k, -FLT_MAX) : -FLT_MAX);
   }
   if (e0 + PER > c.E) {
@@ -376,14 +404,19 @@ __device__ __forceinline__ int gate_token(const float* __restrict__ logits, cons
     for (int q = 0; q < PER; ++q)
       if (e0 + q >= c.E) key[q] = 0u;
   }
-  kmax = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(kmax)));
-  // Error of a difference of two keys, in units of 2^-24. Softmax, of the largest score: 5 of each score's
-  // exponential (with its argument's rounding), 12 of the sum and 3 of the quotient, which both share. Sigmoid:
-  // p (1 - p) (4 + |l|) of the exponential and 4 p of the quotient, under 7 a score. Half of |key| each addition.
-  const float tau = (c.router == MOE_ROUTER_SOFTMAX ? 0x1p-18f : 0x1p-20f) * pmax + 0x1p-22f * kmax;
+  KeyBound bound = {bias != nullptr, 0.f, 0.f};
+  if (c.router == MOE_ROUTER_SOFTMAX) {
+    bound.base = 0x1p-19f * pmax;
+    bound.top = __log2f(pmax);
+  } else if (bias) {
+    float large = 0.f;
+#pragma unroll
+    for (int q = 0; q < PER; ++q) large = fmaxf(large, p[q]);
+    bound.base = KeyBound::score(__uint_as_float(__reduce_max_sync(kFull, __float_as_uint(large))), 0.f);
+  }
   bool groups_sure = true;
   if (c.topk_groups < c.n_groups) {
-    const unsigned keep = kept_groups<PER>(key, c, place, tau, logits, bias, m, scr, groups_sure);
+    const unsigned keep = kept_groups<PER>(key, c, place, bound, logits, bias, m, scr, groups_sure);
     int g = place.g, left = place.left;
     if (place.fills) {
 #pragma unroll
@@ -408,13 +441,16 @@ __device__ __forceinline__ int gate_token(const float* __restrict__ logits, cons
     last = __reduce_max_sync(kFull, top);
     if (lane == j) mine = last;
   }
+  const float value = of_order(mine), off = bound(value);
   const unsigned next = __shfl_down_sync(kFull, mine, 1);
-  const bool near = lane < c.k && next && !(of_order(mine) - of_order(next) > tau);
+  const float below = __shfl_down_sync(kFull, value + off, 1);
+  const bool near = lane < c.k && next && !(value - off > below);
   const bool sure = !__any_sync(kFull, near);
   const unsigned kth = __shfl_sync(kFull, mine, c.k - 1);   // 0: fewer than k different keys
-  // Candidates: the selection, or where it is not sure every expert whose key may reach it. (tau is finite, so an
-  // infinite kth stays what it is.)
-  const unsigned least = sure || !kth ? kth : order_of(of_order(kth) - tau);
+  // Candidates: the selection, or where it is not sure every expert whose key may reach it (both bounds, and as much
+  // again for what their own arithmetic rounds). An infinite kth has no bound and stays what it is.
+  const float reach = __shfl_sync(kFull, value - 3 * off, c.k - 1);
+  const unsigned least = sure || !kth ? kth : order_of(reach);
   int n = 0;
 #pragma unroll
   for (int q = 0; q < PER; ++q) {

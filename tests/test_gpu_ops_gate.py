@@ -258,3 +258,30 @@ def test_as_many_experts_as_are_selected(ops, router, E, k, groups, kept):
     logits[0, :4] = torch.tensor([0.0, 1.0, 1.0, 0.0])[:E]
     out = check(ops, logits, None, k, router, n_groups=groups, topk_groups=kept)
     assert all(len(set(row)) == k for row in out["idx"].tolist())
+
+
+def test_masks_and_peaked_scores_cost_what_others_do(ops):
+    """Selections that 32 bits decide stay with them when one bias is far from the others or one score far above: less
+    than twice the ordinary time (21 us; in 64 bits 183)."""
+    g = torch.Generator().manual_seed(10)
+    l, b = torch.randn(8192, 256, generator=g).cuda(), (0.05 * torch.randn(256, generator=g)).cuda()
+    def masked(v):
+        return b.index_fill(0, torch.tensor([3, 90], device="cuda"), v)
+    def us(logits, **kw):
+        out = ops.gate(logits, 8, **kw)
+        best = []
+        for _ in range(7):
+            t = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+            t[0].record()
+            for _ in range(20):
+                ops.gate(logits, 8, out=out, **kw)
+            t[1].record()
+            torch.cuda.synchronize()
+            best.append(t[0].elapsed_time(t[1]) * 50)
+        return min(best)
+    kw = dict(router="sigmoid", n_groups=8, topk_groups=4)
+    usual = us(l, bias=b, **kw)
+    for v in (-float("inf"), -1e9, float("inf")):
+        assert us(l, bias=masked(v), **kw) < 2 * usual, v
+    assert us(1.5 * l - 10, bias=0.01 * b, **kw) < 2 * usual
+    assert us(8 * l, router="softmax") < 2 * us(l, router="softmax")
