@@ -17,7 +17,7 @@
 // Measured, 8192 tokens of 256 experts in 8 groups: 22 us, 16 of them the selection (63% of the issue slots, some 1,100
 // instructions a token; its 8.4 MB would take 1.3) and the rest the dispatch. With 64-bit keys for all 183 us. The
 // same with an expert or 32 masked by the bias, logits around -10, or peaked softmax rows: 18-22 us. Sigmoid logits
-// around 10 without a bias need 64 bits in most rows, their scores being within some 2^-24 of 1 and each other: 74 us.
+// around 10 without a bias need 64 bits in most rows, their scores being within some 2^-24 of 1 and each other: 58 us.
 // Four tokens in 4.6 us.
 #include <cfloat>
 #include <cmath>
@@ -246,10 +246,11 @@ struct Place {
   }
 };
 
-// How far a key may be from the one computed in 64 bits, with u = 2^-24. A score is off by its exponential (2^-22, and
-// a rounded argument: 2.3 |x| u) and three roundings or fewer behind it, that is by 10 u + 2 u log2(largest / score) of
-// itself, half of which is to spare; a sigmoid's largest score is 1, and the denominator that all scores of a softmax
-// share does not move their order. Without a bias the key is the score: the bound is the key's own, so that small
+// How far a key may be from the one computed in 64 bits, with u = 2^-24. A softmax's score is off by its exponential
+// (4 u, and 2.23 u |x| for the rounded argument x) and a product, a sigmoid's by (1 - p) (4 u + 1.25 u |x|), an addition
+// and a reciprocal (3 u): with 2 u for the bound's own use both are under 8 u + 2 u log2(largest / score) of
+// themselves. (A sigmoid's largest score is 1; the denominator that all scores of a softmax share does not move their
+// order.) Without a bias the key is the score: the bound is the key's own, so that small
 // scores beside a large one are told apart. With one, scores of any size can stand behind a key: base is the bound of
 // the row's largest score (32 u of it with the softmax's denominator), and an addition and its comparison cost u |key|
 // each. A key plus its bound grows with the key, so only neighbours need to be compared, whatever lies below them
@@ -260,7 +261,7 @@ struct KeyBound {
   float base, top;     // top: log2 of the largest score
   __device__ __forceinline__ static float score(float p, float top) {
     const float doublings = fmaxf(top - __log2f(fmaxf(p, FLT_MIN)), 0.f);
-    return p * (0x1.4p-21f + 0x1p-23f * doublings) + 0x1p-125f;     // (scores below 2^-126 are taken for 0)
+    return p * (0x1p-21f + 0x1p-23f * doublings) + 0x1p-125f;     // (scores below 2^-126 are taken for 0)
   }
   __device__ __forceinline__ float operator()(float k) const {
     if (!(fabsf(k) < FLT_MAX)) return 0.f;
@@ -345,7 +346,7 @@ __device__ __forceinline__ unsigned kept_groups(const unsigned (&key)[PER], cons
 #pragma unroll
   for (int q = 0; q < PER; ++q) {
     const int mine = min((e0 + q) / S, c.n_groups - 1);
-    const float limit = __shfl_sync(kFull, second - 3 * off2, mine * step);
+    const float limit = __shfl_sync(kFull, second - 2 * off2, mine * step);
     const bool cand = key[q] && !(of_order(key[q]) < limit);
     const unsigned mask = __ballot_sync(kFull, cand);
     const int at = n + __popc(mask & ((1u << lane) - 1u));
@@ -447,9 +448,9 @@ __device__ __forceinline__ int gate_token(const float* __restrict__ logits, cons
   const bool near = lane < c.k && next && !(value - off > below);
   const bool sure = !__any_sync(kFull, near);
   const unsigned kth = __shfl_sync(kFull, mine, c.k - 1);   // 0: fewer than k different keys
-  // Candidates: the selection, or where it is not sure every expert whose key may reach it (both bounds, and as much
-  // again for what their own arithmetic rounds). An infinite kth has no bound and stays what it is.
-  const float reach = __shfl_sync(kFull, value - 3 * off, c.k - 1);
+  // Candidates: the selection, or where it is not sure every expert whose key may reach it (its own bound is at most
+  // that of the larger kth, up to what the bounds have to spare). An infinite kth has no bound and stays what it is.
+  const float reach = __shfl_sync(kFull, value - 2 * off, c.k - 1);
   const unsigned least = sure || !kth ? kth : order_of(reach);
   int n = 0;
 #pragma unroll
