@@ -285,3 +285,45 @@ def test_masks_and_peaked_scores_cost_what_others_do(ops):
         assert us(l, bias=masked(v), **kw) < 2 * usual, v
     assert us(1.5 * l - 10, bias=0.01 * b, **kw) < 2 * usual
     assert us(8 * l, router="softmax") < 2 * us(l, router="softmax")
+
+
+@pytest.mark.parametrize("E,k,scale", [(24, 1, 1.0), (24, 2, 1.0), (200, 8, 2.5), (64, 6, 1.0)])
+def test_backward_of_selected_scores_far_below_the_largest(ops, E, k, scale):
+    """Renormalised softmax gates whose scores' sum is near or below the 1e-20 that is added to it: the other logits
+    have a gradient there.
+
+    A score e^x of the row's largest, x = -30 .. -130, is off by |x| 2^-24 of itself through its rounded argument, and
+    enters a gradient four times (its own, the sum, twice the mean); below 2^-126 it may be lost whole, over 1e-20."""
+    g = torch.Generator().manual_seed(E + k)
+    T = 101
+    l, dg = torch.randn(T, E, generator=g), torch.randn(T, k, generator=g)
+    idx = torch.stack([torch.randperm(E, generator=g)[:k] for _ in range(T)])
+    down = torch.linspace(30, 130, T)[:, None]
+    l.scatter_add_(1, idx, -down.expand(T, k) + torch.rand(T, k, generator=g))
+    got = ops.gate_backward(l.cuda(), idx.int().cuda(), dg.cuda(), router="softmax", route_scale=scale)["dlogits"]
+    want, size = oo.gate_backward(l.double().numpy(), idx.numpy(), dg.double().numpy(), "softmax", True, scale)
+    lost = 2.0 ** -126 * 1e20 * 2 * k * scale * np.abs(dg.numpy()).max(1, keepdims=True)
+    err = np.abs(got.double().cpu().numpy() - want)
+    assert np.all(err <= (NEAR + 4 * 2.0 ** -24 * (down.numpy() + 8)) * size + lost), (err / (size + lost)).max()
+    # the stated example: gates 0.253 and 0.093, and a gradient of -0.105 at the largest logit
+    d = ops.gate_backward(torch.tensor([[0.0, -47, -48, -49]]).cuda(), torch.tensor([[1, 2]], dtype=torch.int32).cuda(),
+                          torch.tensor([[1.0, -1]]).cuda(), router="softmax")["dlogits"][0].tolist()
+    assert np.allclose(d, [-0.105, 0.213, -0.108, 0], atol=1e-3)
+
+
+def test_forward_and_backward_agree_near_the_added_constant(ops):
+    """The gradient against differences of the forward pass's formula, D between 1e-24 and 1e-16."""
+    l = torch.tensor([[0.0, -37, -38, 1], [0, -46, -45.5, -1], [0, -55, -54, 0.5]])
+    dg = torch.tensor([[1.0, -1], [0.5, 2], [-1, 1]])
+    idx = torch.tensor([[1, 2]] * 3)
+    d = ops.gate_backward(l.cuda(), idx.int().cuda(), dg.cuda(), router="softmax")["dlogits"].double().cpu().numpy()
+    def loss(z):
+        p = oo.scores(z, "softmax")[np.arange(3)[:, None], idx.numpy()]
+        return (p / (p.sum(1, keepdims=True) + 1e-20) * dg.double().numpy()).sum()
+    z = l.double().numpy()
+    for t in range(3):
+        for e in range(4):
+            a, b = z.copy(), z.copy()
+            a[t, e] += 1e-5
+            b[t, e] -= 1e-5
+            assert abs((loss(a) - loss(b)) / 2e-5 - d[t, e]) <= 1e-4
