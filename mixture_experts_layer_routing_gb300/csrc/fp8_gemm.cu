@@ -905,16 +905,18 @@ cudaError_t pick_wide(const moe_ops_s* o, int cg, const CUtensorMap* tm, GemmPar
   return fp32 ? launch_wide<2, WGRAD, float>(o, tm, p, units, s) : launch_wide<2, WGRAD, bf16>(o, tm, p, units, s);
 }
 
-// Rows of a (and their scales) in the order of c's rows, one warp a row; an index out of range gives zeros. Most reads
-// hit L2: 12,288 rows of 2,048 bytes in 8 us, 50 MB moved.
+// Rows of a (and their scales) in the order of c's rows, one warp a row; an index out of range gives zeros. Rows of no
+// segment are left alone, and so is what row_index holds there. Most reads hit L2: 12,288 rows of 2,048 bytes in 8 us,
+// 50 MB moved.
 __global__ void __launch_bounds__(256) gather_rows_kernel(const uint8_t* __restrict__ a, const float* __restrict__ sa,
-                                                          const int* __restrict__ row_index, int M, int a_rows, int K,
+                                                          const int* __restrict__ row_index,
+                                                          const int* __restrict__ off, int G, int M, int a_rows, int K,
                                                           int nkb, uint8_t* __restrict__ out, float* __restrict__ so,
                                                           int* status) {
   griddep_wait();
   griddep_launch();
   const int lane = threadIdx.x & 31, m = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (m >= M) return;
+  if (m >= M || (off && (m < off[0] || m >= off[G]))) return;
   const int r = row_index[m];
   const bool in = (unsigned)r < (unsigned)a_rows;
   if (!in) set_error(status, MOE_ERR_DEVICE_INDEX);
@@ -1048,8 +1050,8 @@ cudaError_t fp8_matmul(const moe_ops_s* o, const void* a, const float* sa, int a
     // and one of four 128-byte rows takes about 80 cycles: 2,600 cycles a stage of 128 rows, whose MMAs take 512.)
     float* so = (float*)((char*)ws + ((size_t)M * K + 15) / 16 * 16);
     *n += 1;
-    MOE_TRY(launch_pdl(gather_rows_kernel, dim3(ceil_div(M, 8)), dim3(256), 0, s, (const uint8_t*)a, sa, row_index, M,
-                       a_rows, K, p.nkb, (uint8_t*)ws, so, o->status));
+    MOE_TRY(launch_pdl(gather_rows_kernel, dim3(ceil_div(M, 8)), dim3(256), 0, s, (const uint8_t*)a, sa, row_index, off, G,
+                       M, a_rows, K, p.nkb, (uint8_t*)ws, so, o->status));
     a = ws;
     p.sa = so;
     p.a_rows = a_rows = M;

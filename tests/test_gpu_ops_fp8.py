@@ -412,3 +412,30 @@ def test_python_refusals(ops):
         ops.quant_rows(torch.randn(4, 64).cuda())
     with pytest.raises(RuntimeError):
         ops.quant_rows(rnd(4, 60).cuda())
+
+
+@pytest.mark.parametrize("M,G,N", [(24, 3, 128), (300, 2, 128), (1500, 2, 264), (200, 40, 1100)])
+def test_indexes_of_rows_of_no_segment_are_not_read(ops, M, G, N):
+    """An index list of fixed length, -1 where it holds no row: before the first segment and behind the last, whichever
+    kernel takes the product."""
+    K, rows = 256, 50
+    b = rnd(G, N, K, seed=61)
+    q, s = ops.quant_rows(rnd(rows, K, seed=60, spread=True).cuda())
+    wq, ws = map(np.stack, zip(*(oo.quantise_blocks(f64(b[g])) for g in range(G))))
+    bq, bs = torch.from_numpy(wq).float().to(torch.float8_e4m3fn).cuda(), torch.from_numpy(ws).float().cuda()
+    A, B = oo.values(f64(q), f64(s)), oo.values(wq, ws, (-2, -1))
+    lo, hi = 3, M - 5
+    off = torch.linspace(lo, hi, G + 1).int()
+    index = torch.full((M,), -1, dtype=torch.int32)
+    index[lo:hi] = torch.randint(0, rows, (hi - lo,), generator=torch.Generator().manual_seed(8), dtype=torch.int32)
+    out = torch.full((M, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    ops.fp8_matmul(q, s, bq, bs, off=off.cuda(), row_index=index.cuda(), out=out)
+    assert ops.status() == 0
+    for g, (a, z) in enumerate(zip(off[:-1].tolist(), off[1:].tolist())):
+        r = A[index[a:z].long().numpy()]
+        near(out[a:z], r @ B[g].T, np.abs(r) @ np.abs(B[g]).T, 2)
+    for part in (out[:lo], out[hi:]):
+        assert torch.equal(part, torch.full_like(part, 7.0))
+    x = rnd(rows, 136, seed=62).cuda()
+    q1, s1 = ops.quant_cols(x, off=off.cuda(), row_index=index.cuda())
+    assert ops.status() == 0
