@@ -14,7 +14,8 @@
  * status word. A wait that ran out (MOE_ERR_TIMEOUT) or an index out of range
  * that a kernel read on the device (MOE_ERR_DEVICE_INDEX; the access is left
  * out) is recorded there: read it with moe_ops_get_status. A handle may be used
- * from several streams. The device it was created on must be current.
+ * from several streams and host threads. The device it was created on must be
+ * current.
  *
  * 8-bit operands. A block of 128 values v (the last one of a row may be
  * shorter) with the largest magnitude m is held as
@@ -38,7 +39,8 @@ typedef struct moe_ops_s* moe_ops;
 
 moe_status moe_ops_create(moe_ops* out);
 moe_status moe_ops_destroy(moe_ops ops);
-/* Wait for `stream`, then read and clear the status word. */
+/* Wait for `stream`, then read and clear the status word (in one step: an error that work on another stream records
+ * meanwhile is returned by this call or by the next). */
 moe_status moe_ops_get_status(moe_ops ops, void* stream, int* device_status);
 /* Kernels launched since moe_ops_create (host counter). */
 moe_status moe_ops_launch_count(moe_ops ops, long long* launches);

@@ -37,6 +37,9 @@ moe_status check_handle(moe_ops o) {
     return e_ == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;                        \
   } while (0)
 
+// Reads and clears in one step: what a kernel on another stream records meanwhile is read here or stays.
+__global__ void take_status_kernel(int* status, int* out) { *out = atomicExch(status, 0); }
+
 moe_status check_gate(const moe_gate_config* c, int T) {
   CHECK(c && c->E >= 1 && c->k >= 1 && T >= 0, MOE_ERR_INVALID_ARG);
   CHECK(c->router == MOE_ROUTER_SOFTMAX || c->router == MOE_ROUTER_SIGMOID, MOE_ERR_INVALID_ARG);
@@ -84,9 +87,20 @@ moe_status moe_ops_get_status(moe_ops ops, void* stream, int* device_status) {
   CHECK(device_status, MOE_ERR_INVALID_ARG);
   cudaStream_t s = (cudaStream_t)stream;
   int v = 0;
-  if (cudaMemcpyAsync(&v, ops->status, sizeof(int), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-      cudaMemsetAsync(ops->status, 0, sizeof(int), s) != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess)
+  int* word = nullptr;   // the call's own: another one may be taking the status on another stream
+  cudaError_t e = cudaMallocAsync(&word, sizeof(int), s);
+  if (e == cudaSuccess) {
+    take_status_kernel<<<1, 1, 0, s>>>(ops->status, word);
+    e = cudaGetLastError();
+    if (e == cudaSuccess) e = cudaMemcpyAsync(&v, word, sizeof(int), cudaMemcpyDeviceToHost, s);
+    const cudaError_t freed = cudaFreeAsync(word, s);
+    if (e == cudaSuccess) e = freed;
+  }
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
     return MOE_ERR_CUDA;
+  }
   *device_status = v;
   return MOE_OK;
 }
