@@ -42,7 +42,7 @@ moe_status moe_ops_destroy(moe_ops ops);
 /* Wait for `stream`, then read and clear the status word (in one step: an error that work on another stream records
  * meanwhile is returned by this call or by the next). */
 moe_status moe_ops_get_status(moe_ops ops, void* stream, int* device_status);
-/* Kernels launched since moe_ops_create (host counter). */
+/* Kernels that the operators launched since moe_ops_create (host counter). */
 moe_status moe_ops_launch_count(moe_ops ops, long long* launches);
 
 /* ---- RMS norm. dtype (MOE_BF16 or MOE_FP32) is the type of x, residual, weight,

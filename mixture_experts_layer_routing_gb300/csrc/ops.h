@@ -4,6 +4,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/moe_ops.h"
 
 struct moe_ops_s {
@@ -11,7 +13,7 @@ struct moe_ops_s {
   int sms;
   int pairs;              // two-CTA clusters of the wide products that run at once
   int* status;            // device word: the first device-side error
-  long long launches;
+  std::atomic<long long> launches;   // (host threads share a handle)
 };
 
 namespace moe {

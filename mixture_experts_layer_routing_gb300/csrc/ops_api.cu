@@ -107,7 +107,7 @@ moe_status moe_ops_get_status(moe_ops ops, void* stream, int* device_status) {
 
 moe_status moe_ops_launch_count(moe_ops ops, long long* launches) {
   CHECK(ops && launches, MOE_ERR_INVALID_ARG);
-  *launches = ops->launches;
+  *launches = ops->launches.load();
   return MOE_OK;
 }
 

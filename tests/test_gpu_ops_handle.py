@@ -1,4 +1,6 @@
 """The operators' handle from several streams and host threads (GPU)."""
+import ctypes
+import threading
 
 import pytest
 import torch
@@ -33,3 +35,25 @@ def test_no_error_is_lost_between_reading_and_clearing(ops):
         assert set(seen) <= {0, moe.MOE_ERR_DEVICE_INDEX}
         lost += not any(seen)
     assert lost == 0
+
+
+def test_launches_of_several_host_threads_are_all_counted(ops):
+    x, w = torch.randn(4, 64, device="cuda"), torch.ones(64, device="cuda")
+    threads, calls = 4, 20000
+    y = [torch.empty_like(x) for _ in range(threads)]
+    streams = [torch.cuda.Stream() for _ in range(threads)]
+    torch.cuda.synchronize()
+    f, before = ops._lib.moe_norm_forward, ops.launch_count()
+    bad = []
+    def work(i):
+        arg = (ops.h, 0, x.data_ptr(), 64, None, 0, w.data_ptr(), 4, 64, 1e-6, None, y[i].data_ptr(), None, None, None,
+               ctypes.c_void_p(streams[i].cuda_stream))
+        bad.extend(s for s in (f(*arg) for _ in range(calls)) if s)       # (a ctypes call lets other threads run)
+    ts = [threading.Thread(target=work, args=(i,)) for i in range(threads)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    torch.cuda.synchronize()
+    assert not bad
+    assert ops.launch_count() - before == threads * calls
