@@ -99,11 +99,11 @@ struct Args {
   }
 };
 
-// Row stride of a matrix whose rows are dense.
+// Row stride of a matrix whose rows are dense. (A single row has none: it may be a part of an array of any width.)
 long long row_stride(const at::Tensor& t, const char* what) {
   if (t.dim() != 2) refuse(PyExc_ValueError, what, "two dimensions expected");
   if (t.size(1) > 1 && t.stride(1) != 1) refuse(PyExc_ValueError, what, "the values of a row have to be neighbours");
-  return t.size(0) > 1 ? t.stride(0) : std::max(t.size(1), t.stride(0));
+  return t.size(0) > 1 ? t.stride(0) : t.size(1);
 }
 int dtype_of(const at::Tensor& t, const char* what) {
   if (t.scalar_type() == at::kBFloat16) return MOE_BF16;

@@ -216,3 +216,24 @@ def test_python_refusals(ops):
         ops.rms_norm(x, w, want=("z",))
     with pytest.raises(RuntimeError):
         ops.rms_norm(x[:, :60], w[:60].contiguous())           # d not a multiple of 8
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_one_row_of_a_wider_array(ops, dtype):
+    """A single row has no stride: the width of the array that it is a part of does not matter, nor that of its sum's."""
+    x, r, w = make(3, 512, dtype, 15)
+    wide = torch.zeros(3, 1021, dtype=x.dtype, device="cuda")
+    wide[:1, :512], wide[2:, :] = r[:1], 1.0
+    want = ops.rms_norm(x[:1], w, r[:1], want=("h", "y"))
+    got = ops.rms_norm(x[:1], w, wide[:1, :512], want=("h", "y"))
+    row = wide[:1, :512]
+    inplace = ops.rms_norm(row, w, x[:1], out=dict(h=row, y=None))
+    for n in want:
+        assert torch.equal(got[n], want[n]) and torch.equal(inplace[n], want[n]), n
+    if dtype == "bf16":
+        q, s = ops.quant_rows(wide[:1, :512])
+        wq, ws = ops.quant_rows(wide[:1, :512].clone())
+        assert torch.equal(q.float(), wq.float()) and torch.equal(s, ws)
+        q, s = ops.quant_cols(wide[:1, :512])
+        wq, ws = ops.quant_cols(wide[:1, :512].clone())
+        assert torch.equal(q.float(), wq.float()) and torch.equal(s, ws)
