@@ -237,3 +237,29 @@ def test_one_row_of_a_wider_array(ops, dtype):
         q, s = ops.quant_cols(wide[:1, :512])
         wq, ws = ops.quant_cols(wide[:1, :512].clone())
         assert torch.equal(q.float(), wq.float()) and torch.equal(s, ws)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T,d", [(1900, 512), (1501, 2048), (1217, 4096), (457, 4104), (1000, 7168), (461, 8192),
+                                 (500, 16384)])
+def test_backward_of_several_rows_a_cta(ops, T, d, dtype):
+    """Every instance with two rows a CTA and more, the last ones uneven, dh and dw (and dx in dh's place).
+
+    dw: a CTA adds its rows one after the other, then the parts (one a CTA) go through 32 chains and a tree of five; a
+    product's own rounding is one more, rstd's and h's one. With P parts that are under T / P + 1 + P / 32 + 1 + 5 + 2
+    roundings, P between 152 and 608."""
+    h, dh, w = make(T, d, dtype, T + d)
+    dy = torch.randn(T, d, generator=torch.Generator().manual_seed(10)).to(DT[dtype]).cuda()
+    rstd = ops.rms_norm(h, w, want=("rstd",))["rstd"]
+    out = ops.rms_norm_backward(dy, h, w, rstd, dh=dh)
+    dx, dw, size, wsize = oo.rms_norm_backward(f64(dy), f64(h), f64(w), f64(rstd), f64(dh))
+    assert np.all(np.abs(f64(out["dx"]) - dx) <= HALF[dtype] * np.abs(dx) + 2 * SUMS * size)
+    chain = max(T / p + 1 + p / 32 + 1 + 5 + 2 for p in (152, 304, 456, 608))
+    assert np.all(np.abs(f64(out["dw"]) - dw) <= chain * 2.0 ** -24 * wsize)
+    place = dh.clone()
+    got = ops.rms_norm_backward(dy, h, w, rstd, dh=place, out=dict(dx=place, dw=None))
+    assert torch.equal(place, out["dx"]) and torch.equal(got["dw"], out["dw"])
+    got = ops.rms_norm_backward(dy, h, w, rstd)
+    dx, _, size, _ = oo.rms_norm_backward(f64(dy), f64(h), f64(w), f64(rstd))
+    assert np.all(np.abs(f64(got["dx"]) - dx) <= HALF[dtype] * np.abs(dx) + 2 * SUMS * size)
+    assert torch.equal(got["dw"], out["dw"]) and ops.status() == 0
