@@ -270,8 +270,10 @@ def default_ops(device=None) -> MoeOps:
     if device is None and _default:
         index = _current_device()
     else:
-        index = None if device is None else torch.device(device).index
-        index = torch.cuda.current_device() if index is None else index
+        d = torch.device("cuda" if device is None else device)
+        if d.type != "cuda":
+            raise ValueError(f"a CUDA device is needed, got {d}")
+        index = torch.cuda.current_device() if d.index is None else d.index
     ops = _default.get(index)
     if ops is None:
         ops = _default[index] = MoeOps(torch.device("cuda", index))

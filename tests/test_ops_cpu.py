@@ -151,6 +151,12 @@ def test_quantisers_refuse(lib, name, args, code):
     assert getattr(lib, name)(*args) == code
 
 
+@pytest.mark.parametrize("make", [mops.default_ops, mops.MoeOps])
+def test_handles_of_other_devices_are_refused(make):
+    with pytest.raises(ValueError):
+        make("cpu")
+
+
 def test_padded_rows_of_the_token_axis(lib):
     n = ctypes.c_int()
     for T, G, want in [(0, 1, 0), (1, 1, 128), (128, 1, 128), (129, 1, 256), (129, 4, 256 + 4 * 128)]:
