@@ -87,8 +87,9 @@ typedef struct {
  * keys are selected, largest first. Equal groups and keys go to the lower index.
  * Selections are those of keys computed in 64 bits: keys of 32 bits decide where
  * their error cannot change the outcome, keys of 64 bits elsewhere. An expert
- * whose logit is -inf, or whose key is NaN, comes after all others (its gate is
- * 0 for -inf); a row with no expert left selects the lowest indexes with gates 0.
+ * whose logit is -inf, or whose key is NaN or -inf, comes after all others (its
+ * gate is 0 for a logit of -inf); one with a bias of +inf comes first, and so does
+ * its group. A row with no expert left selects the lowest indexes with gates 0.
  * Outputs: idx [T, k] int32, gate [T, k] fp32 (required), and the dispatch of
  * moe_route, all four or none: cnt [E], off [E+1], perm [T*k], inv [T*k].
  * workspace (moe_gate_workspace_size bytes, 16-byte aligned; NULL without a
@@ -98,7 +99,8 @@ moe_status moe_gate_forward(moe_ops ops, const moe_gate_config* cfg, const float
                             int32_t* idx, float* gate, int32_t* cnt, int32_t* off, int32_t* perm, int32_t* inv,
                             void* workspace, void* stream);
 /* dgate [T, k] = dL/dgate of the selection idx -> dlogits [T, E] fp32, written whole
- * (zeros where nothing flows). The bias and the selection get no gradient. Only
+ * (zeros where nothing flows; renormalised softmax gates reach the other logits
+ * where the selected scores' sum is near the 1e-20 added to it). The bias and the selection get no gradient. Only
  * cfg's E, k, router, renorm and route_scale are read. */
 moe_status moe_gate_backward(moe_ops ops, const moe_gate_config* cfg, const float* logits, const int32_t* idx,
                              const float* dgate, int T, float* dlogits, void* stream);

@@ -6,7 +6,7 @@
 // with residual, h and codes in 79 us (98% of the copy rate; 121 with rows unpacked to fp32 in registers, which left
 // fewer CTAs a SM), one row in 2.7 us.
 //
-// Backward: as many CTAs as run at once walk the rows with stride gridDim, each with its part of dw in registers, and
+// Backward: one to four CTAs a SM walk the rows with stride gridDim, each with its part of dw in registers, and
 // make one reduction a row (mean(u n); rstd comes from the forward pass). The parts are summed in a fixed order by a
 // second kernel, so dw does not depend on timing.
 #include "fp8_quant.cuh"
@@ -244,7 +244,10 @@ inline int steps(int d, bool wide) {
 
 }  // namespace
 
-// CTAs of the backward pass: about 1,024 threads a SM (its rows in flight are registers).
+// CTAs of the backward pass: about 1,024 threads a SM (its rows in flight are registers), of 152 SMs, as the size of the
+// workspace is asked for without a handle. Above d = 4096 all of them run at once, one a SM. Below, a thread's 72
+// registers (fp32: 88) let 28 (20) warps run: of d = 2048's 608 CTAs 456 (304) at once, of d = 4096's 304 152. Measured,
+// 2,368 rows of 2,048, 4,096 and 7,168: 12, 18 and 29 us (bf16; their bytes take 6, 11 and 20), 16, 34 and 61 (fp32).
 int norm_partials(int T, int d) {
   const int threads = ceil_div(ceil_div(d / 8, d > 8192 ? 2 : 1), 32) * 32;
   const int most = 152 * (threads > 512 ? 1 : threads > 256 ? 2 : 4);
@@ -268,9 +271,11 @@ cudaError_t norm_backward(const moe_ops_s* o, int dtype, const void* dy, const v
                           cudaStream_t s, long long* n) {
   const int parts = norm_partials(T, d);
   const bool b = dtype == MOE_BF16;
+  // Threads an instance is compiled for. Fewer leave a thread more registers: fp32 spills 16 bytes in 72 registers at
+  // 896 threads and 124 in 64 at 1,024 (2,368 x 7,168 in 61.0 and 70.4 us), bf16 takes 62 at either (29.3 and 29.4).
+  // Past d = 8192 both types spill (232 and 640 bytes: 2,368 x 16,384 in 87 and 235 us, 46 and 92 of them bytes).
   const auto call = d > 8192 ? (b ? bwd<bf16, 2, 1024> : bwd<float, 2, 1024>)
-                    : d > 7168 ? (b ? bwd<bf16, 1, 1024> : bwd<float, 1, 1024>)
-                    : d > 4096 ? (b ? bwd<bf16, 1, 896> : bwd<float, 1, 896>)
+                    : d > 4096 ? (b ? bwd<bf16, 1, 1024> : d > 7168 ? bwd<float, 1, 1024> : bwd<float, 1, 896>)
                                : (b ? bwd<bf16, 1, 512> : bwd<float, 1, 512>);
   *n += 1;
   MOE_TRY(call(dy, dh, h, w, rstd, T, d, dx, dw ? part : nullptr, parts, s));
