@@ -128,7 +128,7 @@ moe_status moe_quant_blocks(moe_ops ops, const void* w, int G, int N, int K, voi
 /* c[m, n] = sum over K of a[r(m), k] b[g(m), n, k], r(m) = row_index[m] or m:
  *   a [a_rows, K], a_scale [a_rows, ceil(K/128)]; b [G, N, K], b_scale [G, ceil(N/128), ceil(K/128)]; c [M, N].
  * off (nullable, device, G+1 ascending within 0 .. M): rows off[g] .. off[g+1] meet b[g], rows of no segment
- * are not written, nor is row_index read there; NULL: G = 1. G is 1..256. A row_index out of range reads zeros and
+ * are not written, whatever row_index holds there; NULL: G = 1. G is 1..256. A row_index out of range reads zeros and
  * records MOE_ERR_DEVICE_INDEX.
  * Forward: a = quantised rows, b = weights. Gradient of the rows: a = quantised dc, b = transposed weights. */
 moe_status moe_fp8_matmul(moe_ops ops, const void* a, const float* a_scale, int a_rows, const int32_t* row_index,

@@ -906,7 +906,7 @@ cudaError_t pick_wide(const moe_ops_s* o, int cg, const CUtensorMap* tm, GemmPar
 }
 
 // Rows of a (and their scales) in the order of c's rows, one warp a row; an index out of range gives zeros. Rows of no
-// segment are left alone, and so is what row_index holds there. Most reads hit L2: 12,288 rows of 2,048 bytes in 8 us,
+// segment are left alone, whatever row_index holds there. Most reads hit L2: 12,288 rows of 2,048 bytes in 8 us,
 // 50 MB moved.
 __global__ void __launch_bounds__(256) gather_rows_kernel(const uint8_t* __restrict__ a, const float* __restrict__ sa,
                                                           const int* __restrict__ row_index,
@@ -916,8 +916,9 @@ __global__ void __launch_bounds__(256) gather_rows_kernel(const uint8_t* __restr
   griddep_wait();
   griddep_launch();
   const int lane = threadIdx.x & 31, m = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (m >= M || (off && (m < off[0] || m >= off[G]))) return;
-  const int r = row_index[m];
+  if (m >= M) return;
+  const int r = row_index[m], lo = off ? off[0] : 0, hi = off ? off[G] : M;   // (loaded together)
+  if (m < lo || m >= hi) return;
   const bool in = (unsigned)r < (unsigned)a_rows;
   if (!in) set_error(status, MOE_ERR_DEVICE_INDEX);
   const uint4* src = reinterpret_cast<const uint4*>(a + (size_t)(in ? r : 0) * K);
