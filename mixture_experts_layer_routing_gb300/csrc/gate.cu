@@ -18,7 +18,7 @@
 // instructions a token; its 8.4 MB would take 1.3) and the rest the dispatch. With 64-bit keys for all 183 us. The
 // same with an expert or 32 masked by the bias, logits around -10, or peaked softmax rows: 18-22 us. Sigmoid logits
 // around 10 without a bias need 64 bits in most rows, their scores being within some 2^-24 of 1 and each other: 58 us.
-// Four tokens in 4.6 us.
+// Four tokens in 4.7 us (the bounds are 0.2 of it).
 #include <cfloat>
 #include <cmath>
 
@@ -250,24 +250,19 @@ struct Place {
 // (4 u, and 2.23 u |x| for the rounded argument x) and a product, a sigmoid's by (1 - p) (4 u + 1.25 u |x|), an addition
 // and a reciprocal (3 u): with 2 u for the bound's own use both are under 8 u + 2 u log2(largest / score) of
 // themselves. (A sigmoid's largest score is 1; the denominator that all scores of a softmax share does not move their
-// order.) Without a bias the key is the score: the bound is the key's own, so that small
-// scores beside a large one are told apart. With one, scores of any size can stand behind a key: base is the bound of
-// the row's largest score (32 u of it with the softmax's denominator), and an addition and its comparison cost u |key|
-// each. A key plus its bound grows with the key, so only neighbours need to be compared, whatever lies below them
-// (a mask of -1e9, say). Infinite keys come from an infinite bias, and the lowest value stands for experts that are
-// masked: they have no error.
+// order.) Without a bias the key is the score: the bound is the key's own, so that small scores beside a large one are
+// told apart. With one, scores of any size can stand behind a key: base is the bound of the row's largest score (32 u of
+// it with the softmax's denominator), and an addition and its comparison cost u |key| each. A key plus its bound grows
+// with the key, so only neighbours need to be compared, whatever lies below them (a mask of -1e9, say). Infinite keys
+// come from an infinite bias, and the lowest value stands for experts that are masked: they have no error.
 struct KeyBound {
-  bool biased;
-  float base, top;     // top: log2 of the largest score
-  __device__ __forceinline__ static float score(float p, float top) {
-    const float doublings = fmaxf(top - __log2f(fmaxf(p, FLT_MIN)), 0.f);
-    return p * (0x1p-21f + 0x1p-23f * doublings) + 0x1p-125f;     // (scores below 2^-126 are taken for 0)
-  }
+  float base, rel, per_doubling, top;     // top: log2 of the largest score
   __device__ __forceinline__ float operator()(float k) const {
-    if (!(fabsf(k) < FLT_MAX)) return 0.f;
-    return biased ? base + 0x1p-23f * fabsf(k) : score(k, top);
+    const float a = fabsf(k), doublings = fmaxf(top - __log2f(fmaxf(a, FLT_MIN)), 0.f);
+    return a < FLT_MAX ? fmaf(a, fmaf(per_doubling, doublings, rel), base) : 0.f;
   }
 };
+constexpr float kScoreBase = 0x1p-125f, kScoreRel = 0x1p-21f, kScoreDoubling = 0x1p-23f;   // (below 2^-126: taken for 0)
 
 // The groups that stay, a bit each. Where their choice rests on scores (sums of two keys) whose bounds meet, by 64-bit
 // keys of the experts that can be one of their group's two best; sure turns false if these are more than a warp holds.
@@ -405,15 +400,18 @@ __device__ __forceinline__ int gate_token(const float* __restrict__ logits, cons
     for (int q = 0; q < PER; ++q)
       if (e0 + q >= c.E) key[q] = 0u;
   }
-  KeyBound bound = {bias != nullptr, 0.f, 0.f};
-  if (c.router == MOE_ROUTER_SOFTMAX) {
-    bound.base = 0x1p-19f * pmax;
-    bound.top = __log2f(pmax);
-  } else if (bias) {
-    float large = 0.f;
+  KeyBound bound = {kScoreBase, kScoreRel, kScoreDoubling, c.router == MOE_ROUTER_SOFTMAX ? __log2f(pmax) : 0.f};
+  if (bias) {
+    float large = pmax;
+    if (c.router == MOE_ROUTER_SIGMOID) {
+      large = 0.f;
 #pragma unroll
-    for (int q = 0; q < PER; ++q) large = fmaxf(large, p[q]);
-    bound.base = KeyBound::score(__uint_as_float(__reduce_max_sync(kFull, __float_as_uint(large))), 0.f);
+      for (int q = 0; q < PER; ++q) large = fmaxf(large, p[q]);
+      large = bound(__uint_as_float(__reduce_max_sync(kFull, __float_as_uint(large))));
+    } else {
+      large *= 0x1p-19f;
+    }
+    bound = {large, 0x1p-23f, 0.f, 0.f};
   }
   bool groups_sure = true;
   if (c.topk_groups < c.n_groups) {
@@ -450,8 +448,8 @@ __device__ __forceinline__ int gate_token(const float* __restrict__ logits, cons
   const unsigned kth = __shfl_sync(kFull, mine, c.k - 1);   // 0: fewer than k different keys
   // Candidates: the selection, or where it is not sure every expert whose key may reach it (its own bound is at most
   // that of the larger kth, up to what the bounds have to spare). An infinite kth has no bound and stays what it is.
-  const float reach = __shfl_sync(kFull, value - 2 * off, c.k - 1);
-  const unsigned least = sure || !kth ? kth : order_of(reach);
+  unsigned least = kth;
+  if (!sure && kth) least = order_of(__shfl_sync(kFull, value - 2 * off, c.k - 1));
   int n = 0;
 #pragma unroll
   for (int q = 0; q < PER; ++q) {
