@@ -169,14 +169,14 @@ class MoeOps:
              dispatch=True, out=None, stream=None) -> dict:
         """moe_gate_forward. logits [T, E] fp32, bias [E] fp32. Returns idx, gate and (dispatch) cnt, off, perm, inv.
 
-        With `out` the dispatch is made where it holds "perm"."""
+        With `out` the dispatch is made where it holds any of its four outputs (the others are added)."""
         if stream is not None:
             return self._on(stream, self.gate, logits, k, bias, router, renorm, route_scale, n_groups, topk_groups, dispatch, out)
         kind = _ROUTERS[router]
         if out is None:
             out = {}
         else:
-            dispatch = "perm" in out
+            dispatch = "perm" in out or "inv" in out or "off" in out or "cnt" in out
         s = self._b.gate(self.h, self._index, self._stream(), logits, k, bias, kind, renorm, route_scale,
                          n_groups, topk_groups, dispatch, out)
         if s:

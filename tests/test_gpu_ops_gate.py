@@ -327,3 +327,16 @@ def test_forward_and_backward_agree_near_the_added_constant(ops):
             a[t, e] += 1e-5
             b[t, e] -= 1e-5
             assert abs((loss(a) - loss(b)) / 2e-5 - d[t, e]) <= 1e-4
+
+
+@pytest.mark.parametrize("names", [("cnt",), ("cnt", "off"), ("inv",), ("perm",)])
+def test_any_output_of_the_dispatch_is_written(ops, names):
+    l = torch.randn(50, 16, generator=torch.Generator().manual_seed(11)).cuda()
+    want = ops.gate(l, 3)
+    out = {n: torch.full_like(want[n], -7) for n in names}
+    got = ops.gate(l, 3, out=dict(out))
+    for n in names:
+        assert got[n] is out[n]
+    for n in want:
+        assert torch.equal(got[n], want[n]), n
+    assert set(ops.gate(l, 3, out=dict(idx=None, gate=None))) == {"idx", "gate"}
