@@ -5,6 +5,8 @@
  *   moe_gate_*    routing from router logits: bias, groups, top-k, dispatch
  *   moe_quant_*   e4m3 codes with one fp32 scale for each 128 values
  *   moe_fp8_*     products of such operands, dense and by experts' rows
+ *   moe_quant_w4, moe_w4_*   4-bit weights with a scale for a group of values: products of
+ *                 few rows, and the experts' layer of a few tokens
  *
  * Conventions are moe.h's: device pointers owned by the caller, row-major
  * layouts, every call only enqueues on `stream` and never synchronises, bad
@@ -142,6 +144,56 @@ moe_status moe_fp8_matmul_workspace_size(int M, int G, int K, int gathered, size
  * without tokens. T and off as they were given to moe_quant_cols; N and K multiples of 8, scales 16-byte aligned. */
 moe_status moe_fp8_wgrad(moe_ops ops, const void* dct, const float* dct_scale, const void* xt, const float* xt_scale,
                          int T, const int32_t* off, int G, int N, int K, void* c, int out_dtype, void* stream);
+
+/* ---- 4-bit weights. A group of `group` (32, 64 or 128; the last one of a row may be shorter) consecutive values along
+ * K shares a scale and, where zero is given, a zero point:
+ *   w = (code - zero) * scale      codes 0..15, zero 0..15 (8 without zero points)
+ * codes [G, N, K/8] words of eight values, value 2i in bits 4i .. 4i+3 and value 2i+1 in bits 16+4i .. 16+4i+3;
+ * scale [G, ceil(K/group), N] bf16; zero [G, ceil(K/group), N] bytes, or NULL. N is a multiple of 8, K of 32; codes and
+ * scale 16-byte aligned, zero 8-byte. */
+typedef struct {
+  const uint32_t* codes;
+  const void* scale;
+  const uint8_t* zero;
+  int group;
+} moe_w4;
+
+/* w [G, N, K] bf16, dense, to codes, scale and (nullable) zero. With m the largest magnitude of a group:
+ *   scale = bf16(m / 7)              code = clamp(rint(w / scale) + 8)
+ * with zero, lo and hi being the smallest and the largest of a group's values and 0:
+ *   scale = bf16((hi - lo) / 15)     zero = clamp(rint(-lo / scale))     code = clamp(rint(w / scale) + zero)
+ * clamped to 0..15, quotients in fp32. A group of zeros has scale 0 and reads zeros; one that holds a NaN or an
+ * infinity reads NaN. */
+moe_status moe_quant_w4(moe_ops ops, const void* w, int G, int N, int K, int group, uint32_t* codes, void* scale,
+                        uint8_t* zero, void* stream);
+/* c[m, n] = sum over K of x[r(m), k] w[g(m), n, k], r(m) = row_index[m] or m: x [x_rows, K] bf16, rows ld_x elements
+ * apart (a multiple of 8, 16-byte aligned); c [M, N] of out_dtype (MOE_BF16 or MOE_FP32); off, G, row_index and rows of
+ * no segment as in moe_fp8_matmul. The values of x and w - zero meet on the tensor cores unrounded, sums are fp32, one
+ * rounding at the end. Made for few rows: a segment's weights are read once for every 8 (M up to 8) or 16 of its rows,
+ * so past some 64 rows the 8-bit products are the faster ones. */
+moe_status moe_w4_matmul(moe_ops ops, const void* x, long long ld_x, int x_rows, const int32_t* row_index, int M,
+                         const moe_w4* w, const int32_t* off, int G, int N, int K, void* c, int out_dtype, void* stream);
+
+typedef struct {
+  int E;              /* routed experts, 1..256 */
+  int n_shared;       /* experts E .. E+n_shared-1 that every token takes with a gate of 1, 0..8 */
+  int k;              /* routed experts of a token, 1..8 */
+  int d;              /* a multiple of 32 */
+  int f;              /* a multiple of 32 */
+} moe_w4_config;
+/* The experts' layer of T = 0..64 tokens, behind the routing, in two kernels:
+ *   y_t = sum_j gate[t, j] FFN_idx[t, j](x_t) + sum of the shared experts' FFN(x_t)
+ *   FFN_e(x) = (silu(x Wg[e]^T) * (x Wu[e]^T)) Wd[e]^T
+ * x [T, d] bf16, rows ld_x elements apart (a multiple of 8, 16-byte aligned); idx [T, k], gate [T, k] fp32 as
+ * moe_gate_forward gives them (an expert may be named twice by a token: its gates add up); w13 of [E+n_shared, 2f, d]
+ * (gate half, up half), wd of [E+n_shared, d, f], with one group size and both with zero points or neither; y [T, d]
+ * of out_dtype. An index outside 0..E-1 is left out and records MOE_ERR_DEVICE_INDEX. h is kept to 16 bits of
+ * mantissa, the other sums in fp32; one rounding at the end. Only experts in use are read. workspace:
+ * moe_w4_experts_workspace_size bytes, 16-byte aligned; calls that may run at once need one each. */
+moe_status moe_w4_experts_workspace_size(const moe_w4_config* cfg, int T, size_t* bytes);
+moe_status moe_w4_experts(moe_ops ops, const moe_w4_config* cfg, const void* x, long long ld_x, int T,
+                          const int32_t* idx, const float* gate, const moe_w4* w13, const moe_w4* wd, void* y,
+                          int out_dtype, void* workspace, void* stream);
 
 #ifdef __cplusplus
 }

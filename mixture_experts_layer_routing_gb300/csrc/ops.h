@@ -56,4 +56,14 @@ cudaError_t fp8_matmul(const moe_ops_s* o, const void* a, const float* sa, int a
 cudaError_t fp8_wgrad(const moe_ops_s* o, const void* dct, const float* sdct, const void* xt, const float* sxt, int T,
                       const int* off, int G, int N, int K, void* c, int out_fp32, cudaStream_t s, long long* n);
 
+cudaError_t quant_w4(const moe_ops_s* o, const void* w, int G, int N, int K, int group, uint32_t* codes, void* scale,
+                     uint8_t* zero, cudaStream_t s, long long* n);
+cudaError_t w4_matmul(const moe_ops_s* o, const void* x, long long ld, int x_rows, const int* row_index, int M,
+                      const moe_w4& w, const int* off, int G, int N, int K, void* c, int out_fp32, cudaStream_t s,
+                      long long* n);
+size_t w4_experts_workspace(const moe_w4_config& c, int T);
+cudaError_t w4_experts(const moe_ops_s* o, const moe_w4_config& c, const void* x, long long ld, int T, const int* idx,
+                       const float* gate, const moe_w4& w13, const moe_w4& wd, void* y, int out_fp32, void* ws,
+                       cudaStream_t s, long long* n);
+
 }  // namespace moe

@@ -50,6 +50,22 @@ moe_status check_gate(const moe_gate_config* c, int T) {
   return MOE_OK;
 }
 
+// 4-bit weights [G, N, K].
+moe_status check_w4(const moe_w4* w, int N, int K) {
+  CHECK(w && w->codes && w->scale, MOE_ERR_INVALID_ARG);
+  CHECK(w->group == 32 || w->group == 64 || w->group == 128, MOE_ERR_UNSUPPORTED);
+  CHECK(N % 8 == 0 && K % 32 == 0 && N < (1 << 28) && K < (1 << 28), MOE_ERR_UNSUPPORTED);
+  CHECK(aligned(w->codes, 16) && aligned(w->scale, 16) && aligned(w->zero, 8), MOE_ERR_UNSUPPORTED);
+  return MOE_OK;
+}
+
+moe_status check_w4_experts(const moe_w4_config* c, int T) {
+  CHECK(c && c->E >= 1 && c->k >= 1 && c->n_shared >= 0 && c->d >= 1 && c->f >= 1 && T >= 0, MOE_ERR_INVALID_ARG);
+  CHECK(c->E <= 256 && c->k <= 8 && c->n_shared <= 8 && T <= 64, MOE_ERR_UNSUPPORTED);
+  CHECK(c->d % 32 == 0 && c->f % 32 == 0 && c->d < (1 << 24) && c->f < (1 << 24), MOE_ERR_UNSUPPORTED);
+  return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -293,6 +309,64 @@ moe_status moe_fp8_wgrad(moe_ops ops, const void* dct, const float* dct_scale, c
   }
   DONE(fp8_wgrad(ops, dct, dct_scale, xt, xt_scale, T, off, G, N, K, c, out_dtype == MOE_FP32, (cudaStream_t)stream,
                  &n_));
+}
+
+moe_status moe_quant_w4(moe_ops ops, const void* w, int G, int N, int K, int group, uint32_t* codes, void* scale,
+                        uint8_t* zero, void* stream) {
+  CHECK(ops && w && codes && scale && G >= 1 && N >= 1 && K >= 1, MOE_ERR_INVALID_ARG);
+  const moe_w4 out = {codes, scale, zero, group};
+  const moe_status st = check_w4(&out, N, K);
+  if (st != MOE_OK) return st;
+  CHECK(aligned(w, 16) && (long long)G * N < (1ll << 31) / ceil_div(K, group), MOE_ERR_UNSUPPORTED);
+  HANDLE(ops);
+  DONE(quant_w4(ops, w, G, N, K, group, codes, scale, zero, (cudaStream_t)stream, &n_));
+}
+
+moe_status moe_w4_matmul(moe_ops ops, const void* x, long long ld_x, int x_rows, const int32_t* row_index, int M,
+                         const moe_w4* w, const int32_t* off, int G, int N, int K, void* c, int out_dtype,
+                         void* stream) {
+  CHECK(ops && M >= 0 && x_rows >= 0 && N >= 1 && K >= 1 && G >= 1, MOE_ERR_INVALID_ARG);
+  CHECK(off || G == 1, MOE_ERR_INVALID_ARG);
+  CHECK(row_index || x_rows >= M, MOE_ERR_INVALID_ARG);
+  CHECK(out_dtype == MOE_BF16 || out_dtype == MOE_FP32, MOE_ERR_INVALID_ARG);
+  const moe_status st = check_w4(w, N, K);
+  if (st != MOE_OK) return st;
+  CHECK(G <= kMaxSegs && M < (1 << 30), MOE_ERR_UNSUPPORTED);
+  CHECK((ceil_div(M, 8) + (long long)G) * ceil_div(N, 16) < (1ll << 30), MOE_ERR_UNSUPPORTED);   // units
+  if (M == 0) return MOE_OK;
+  CHECK(x && c && x_rows >= 1 && ld_x >= K, MOE_ERR_INVALID_ARG);
+  CHECK(ld_x % 8 == 0 && aligned(x, 16) && aligned(c, 4), MOE_ERR_UNSUPPORTED);
+  CHECK((long long)x_rows <= 0xffffffffll / (ld_x / 8), MOE_ERR_UNSUPPORTED);   // row starts in units of 16 bytes
+  HANDLE(ops);
+  DONE(w4_matmul(ops, x, ld_x, x_rows, row_index, M, *w, off, G, N, K, c, out_dtype == MOE_FP32, (cudaStream_t)stream,
+                 &n_));
+}
+
+moe_status moe_w4_experts_workspace_size(const moe_w4_config* cfg, int T, size_t* bytes) {
+  const moe_status st = check_w4_experts(cfg, T);
+  if (st != MOE_OK) return st;
+  CHECK(bytes, MOE_ERR_INVALID_ARG);
+  *bytes = w4_experts_workspace(*cfg, T);
+  return MOE_OK;
+}
+
+moe_status moe_w4_experts(moe_ops ops, const moe_w4_config* cfg, const void* x, long long ld_x, int T,
+                          const int32_t* idx, const float* gate, const moe_w4* w13, const moe_w4* wd, void* y,
+                          int out_dtype, void* workspace, void* stream) {
+  CHECK(ops, MOE_ERR_INVALID_ARG);
+  moe_status st = check_w4_experts(cfg, T);
+  if (st == MOE_OK) st = check_w4(w13, 2 * cfg->f, cfg->d);
+  if (st == MOE_OK) st = check_w4(wd, cfg->d, cfg->f);
+  if (st != MOE_OK) return st;
+  CHECK(out_dtype == MOE_BF16 || out_dtype == MOE_FP32, MOE_ERR_INVALID_ARG);
+  CHECK(w13->group == wd->group && (w13->zero != nullptr) == (wd->zero != nullptr), MOE_ERR_UNSUPPORTED);
+  if (T == 0) return MOE_OK;
+  CHECK(x && idx && gate && y && ld_x >= cfg->d, MOE_ERR_INVALID_ARG);
+  CHECK(ld_x % 8 == 0 && ld_x < (1ll << 28) && aligned(x, 16) && aligned(y, 4), MOE_ERR_UNSUPPORTED);
+  CHECK(workspace && aligned(workspace, 16), MOE_ERR_WORKSPACE);
+  HANDLE(ops);
+  DONE(w4_experts(ops, *cfg, x, ld_x, T, idx, gate, *w13, *wd, y, out_dtype == MOE_FP32, workspace,
+                  (cudaStream_t)stream, &n_));
 }
 
 }  // extern "C"

@@ -117,7 +117,7 @@ int to_int(int64_t v, const char* what) {
 const void* address(const Args& a, int i, const char* what) { return a.given(i) ? a.tensor(i, what).data_ptr() : nullptr; }
 
 PyObject *k_h, *k_y, *k_q, *k_scale, *k_rstd, *k_dx, *k_dw, *k_idx, *k_gate, *k_cnt, *k_off, *k_perm, *k_inv,
-    *k_dlogits, *k_qt, *k_scale_t;
+    *k_dlogits, *k_qt, *k_scale_t, *k_codes, *k_zero, *k_group;
 
 template <class F>
 PyObject* guarded(F&& f) {
@@ -417,10 +417,120 @@ PyObject* fp8_wgrad(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
+// Entry `key` of a dict of 4-bit weights (null if missing or None).
+PyObject* entry(PyObject* w, PyObject* key) {
+  PyObject* o = PyDict_GetItemWithError(w, key);
+  if (!o && PyErr_Occurred()) throw Refused();
+  return o == Py_None ? nullptr : o;
+}
+
+// 4-bit weights as quant_w4 returns them: [N, K], or (many) [G, N, K].
+moe_w4 weights4(const Args& a, int i, const char* what, bool many, int64_t* G, int64_t* N, int64_t* K) {
+  if (!PyDict_Check(a.a[i])) refuse(PyExc_TypeError, what, "a dict of codes, scale and group expected");
+  PyObject *codes = entry(a.a[i], k_codes), *scale = entry(a.a[i], k_scale), *zero = entry(a.a[i], k_zero),
+           *group = entry(a.a[i], k_group);
+  if (!codes || !scale || !group) refuse(PyExc_ValueError, what, "codes, scale and group expected");
+  const at::Tensor &c = a.tensor(codes, "codes"), &s = a.tensor(scale, "scale");
+  if (c.dim() != (many ? 3 : 2)) refuse(PyExc_ValueError, what, many ? "three dimensions expected" : "two dimensions expected");
+  moe_w4 w = {};
+  const int64_t g = PyLong_AsLongLong(group);
+  if (g == -1 && PyErr_Occurred()) throw Refused();
+  if (g != 32 && g != 64 && g != 128) refuse(PyExc_ValueError, what, "groups of 32, 64 or 128 expected");
+  w.group = (int)g;
+  *G = many ? c.size(0) : 1;
+  *N = c.size(-2);
+  *K = c.size(-1) * 8;
+  const int64_t KG = (*K + g - 1) / g;
+  const auto check = [&](const at::Tensor& t, const char* name, at::ScalarType type, int64_t r, int64_t q) {
+    if (many) a.dense(t, name, type, {*G, r, q});
+    else a.dense(t, name, type, {r, q});
+    return t.data_ptr();
+  };
+  w.codes = (const uint32_t*)check(c, "codes", at::kInt, *N, c.size(-1));
+  w.scale = check(s, "scale", at::kBFloat16, KG, *N);
+  if (zero) w.zero = (const uint8_t*)check(a.tensor(zero, "zero"), "zero", at::kByte, KG, *N);
+  return w;
+}
+
+// w, group, zero, out
+PyObject* quant_w4(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&] {
+    Args a(args, n, 7);
+    const at::Tensor& w = a.tensor(3, "w");
+    if (w.dim() != 2 && w.dim() != 3) refuse(PyExc_ValueError, "w", "two or three dimensions expected");
+    a.dense(w, "w", at::kBFloat16, w.sizes());
+    const bool many = w.dim() == 3;
+    const int64_t G = many ? w.size(0) : 1, N = w.size(-2), K = w.size(-1), g = a.integer(4);
+    if (g != 32 && g != 64 && g != 128) refuse(PyExc_ValueError, "group", "32, 64 or 128 expected");
+    if (K % 32) refuse(PyExc_ValueError, "w", "a multiple of 32 columns expected");
+    PyObject* out = a.dict(6);
+    const auto get = [&](PyObject* key, const char* what, at::ScalarType type, int64_t r, int64_t c) {
+      return many ? a.output(out, key, what, type, {G, r, c}, true) : a.output(out, key, what, type, {r, c}, true);
+    };
+    const int64_t KG = (K + g - 1) / g;
+    void* codes = get(k_codes, "codes", at::kInt, N, K / 8);
+    void* scale = get(k_scale, "scale", at::kBFloat16, KG, N);
+    void* zero = PyObject_IsTrue(a.a[5]) ? get(k_zero, "zero", at::kByte, KG, N) : nullptr;
+    return moe_quant_w4(a.ops, w.data_ptr(), to_int(G, "w"), to_int(N, "w"), to_int(K, "w"), (int)g, (uint32_t*)codes,
+                        scale, (uint8_t*)zero, a.stream);
+  });
+}
+
+// x, w, off, row_index, out
+PyObject* w4_matmul(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&] {
+    Args a(args, n, 8);
+    long long ld;
+    const at::Tensor& x = bf16_rows(a, 3, "x", &ld);
+    const bool many = a.given(5);
+    int64_t G, N, K;
+    const moe_w4 w = weights4(a, 4, "w", many, &G, &N, &K);
+    const int64_t rows = x.size(0);
+    if (x.size(1) != K) refuse_shape("x", x, {rows, K});
+    if (many && segments(a, 5) != G) refuse(PyExc_ValueError, "off", "one more value than matrices expected");
+    const int M = to_int(indexed(a, 6, rows), "row_index");
+    const at::Tensor& out = a.tensor(7, "out");
+    const int dt = dtype_of(out, "out");
+    a.dense(out, "out", out.scalar_type(), {M, N});
+    return moe_w4_matmul(a.ops, x.data_ptr(), ld, to_int(rows, "x"), (const int32_t*)address(a, 6, "row_index"), M, &w,
+                         (const int32_t*)address(a, 5, "off"), to_int(G, "w"), to_int(N, "w"), to_int(K, "w"),
+                         out.data_ptr(), dt, a.stream);
+  });
+}
+
+// x, idx, gate, w13, wd, n_shared, out
+PyObject* w4_experts(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&] {
+    Args a(args, n, 10);
+    long long ld;
+    const at::Tensor &x = bf16_rows(a, 3, "x", &ld), &idx = a.tensor(4, "idx");
+    if (idx.dim() != 2) refuse(PyExc_ValueError, "idx", "two dimensions expected");
+    const int64_t T = x.size(0), k = idx.size(1), shared = a.integer(8);
+    int64_t G, N, d, Gd, Nd, f;
+    const moe_w4 w13 = weights4(a, 6, "w13", true, &G, &N, &d), wd = weights4(a, 7, "wd", true, &Gd, &Nd, &f);
+    if (x.size(1) != d) refuse_shape("x", x, {T, d});
+    if (Gd != G || Nd != d || N != 2 * f) refuse(PyExc_ValueError, "w13, wd", "matrices [E, 2f, d] and [E, d, f] expected");
+    if (shared < 0 || shared >= G) refuse(PyExc_ValueError, "n_shared", "fewer than the experts expected");
+    a.dense(idx, "idx", at::kInt, {T, k});
+    const void* gate = a.dense(5, "gate", at::kFloat, {T, k}).data_ptr();
+    const at::Tensor& out = a.tensor(9, "out");
+    const int dt = dtype_of(out, "out");
+    a.dense(out, "out", out.scalar_type(), {T, d});
+    const moe_w4_config c = {to_int(G - shared, "w13"), (int)shared, to_int(k, "idx"), to_int(d, "w13"), to_int(f, "wd")};
+    size_t bytes = 0;
+    const moe_status st = moe_w4_experts_workspace_size(&c, to_int(T, "x"), &bytes);
+    if (st != MOE_OK) return st;
+    at::Tensor ws = at::empty({(int64_t)bytes}, a.opts.dtype(at::kByte));
+    return moe_w4_experts(a.ops, &c, x.data_ptr(), ld, (int)T, (const int32_t*)idx.data_ptr(), (const float*)gate, &w13,
+                          &wd, out.data_ptr(), dt, ws.data_ptr(), a.stream);
+  });
+}
+
 #define METHOD(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD(norm_forward), METHOD(norm_backward), METHOD(gate),         METHOD(gate_backward),
                          METHOD(quant_rows),   METHOD(quant_cols),    METHOD(quant_blocks), METHOD(fp8_matmul),
-                         METHOD(fp8_wgrad),    {nullptr, nullptr, 0, nullptr}};
+                         METHOD(fp8_wgrad),    METHOD(quant_w4),      METHOD(w4_matmul),    METHOD(w4_experts),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_ops_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
@@ -429,7 +539,8 @@ PyMODINIT_FUNC PyInit__ops_binding() {
   const struct { PyObject** key; const char* name; } keys[] = {
       {&k_h, "h"}, {&k_y, "y"}, {&k_q, "q"}, {&k_scale, "scale"}, {&k_rstd, "rstd"}, {&k_dx, "dx"}, {&k_dw, "dw"},
       {&k_idx, "idx"}, {&k_gate, "gate"}, {&k_cnt, "cnt"}, {&k_off, "off"}, {&k_perm, "perm"}, {&k_inv, "inv"},
-      {&k_dlogits, "dlogits"}, {&k_qt, "qt"}, {&k_scale_t, "scale_t"}};
+      {&k_dlogits, "dlogits"}, {&k_qt, "qt"}, {&k_scale_t, "scale_t"}, {&k_codes, "codes"},
+      {&k_zero, "zero"}, {&k_group, "group"}};
   for (const auto& k : keys)
     if (!(*k.key = PyUnicode_InternFromString(k.name))) return nullptr;
   return PyModule_Create(&module_def);

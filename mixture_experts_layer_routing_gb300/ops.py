@@ -18,7 +18,8 @@ from . import MOE_ROUTER_SIGMOID, MOE_ROUTER_SOFTMAX, _check, load_library
 OPS_EXPORTED = ("moe_ops_create", "moe_ops_destroy", "moe_ops_get_status", "moe_ops_launch_count",
                 "moe_norm_forward", "moe_norm_workspace_size", "moe_norm_backward", "moe_gate_workspace_size",
                 "moe_gate_forward", "moe_gate_backward", "moe_quant_rows", "moe_quant_cols_rows", "moe_quant_cols",
-                "moe_quant_blocks", "moe_fp8_matmul", "moe_fp8_matmul_workspace_size", "moe_fp8_wgrad")
+                "moe_quant_blocks", "moe_fp8_matmul", "moe_fp8_matmul_workspace_size", "moe_fp8_wgrad", "moe_quant_w4",
+                "moe_w4_matmul", "moe_w4_experts_workspace_size", "moe_w4_experts")
 
 BLOCK = 128                     # values that share a scale
 _ROUTERS = {"softmax": MOE_ROUTER_SOFTMAX, "sigmoid": MOE_ROUTER_SIGMOID}
@@ -29,6 +30,16 @@ _current_device = getattr(torch._C, "_cuda_getDevice", None)
 class moe_gate_config(ctypes.Structure):
     _fields_ = [("E", ctypes.c_int), ("k", ctypes.c_int), ("router", ctypes.c_int), ("renorm", ctypes.c_int),
                 ("route_scale", ctypes.c_float), ("n_groups", ctypes.c_int), ("topk_groups", ctypes.c_int)]
+
+
+class moe_w4(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("zero", ctypes.c_void_p),
+                ("group", ctypes.c_int)]
+
+
+class moe_w4_config(ctypes.Structure):
+    _fields_ = [("E", ctypes.c_int), ("n_shared", ctypes.c_int), ("k", ctypes.c_int), ("d", ctypes.c_int),
+                ("f", ctypes.c_int)]
 
 
 _bound = None
@@ -59,6 +70,11 @@ def _lib():
     lib.moe_fp8_matmul.argtypes = [vp, vp, vp, i32, vp, i32, vp, vp, vp, i32, i32, i32, vp, i32, vp, vp]
     lib.moe_fp8_matmul_workspace_size.argtypes = [i32, i32, i32, i32, P(sz)]
     lib.moe_fp8_wgrad.argtypes = [vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, vp, i32, vp]
+    w4, w4cfg = P(moe_w4), P(moe_w4_config)
+    lib.moe_quant_w4.argtypes = [vp, vp, i32, i32, i32, i32, vp, vp, vp, vp]
+    lib.moe_w4_matmul.argtypes = [vp, vp, i64, i32, vp, i32, w4, vp, i32, i32, i32, vp, i32, vp]
+    lib.moe_w4_experts_workspace_size.argtypes = [w4cfg, i32, P(sz)]
+    lib.moe_w4_experts.argtypes = [vp, w4cfg, vp, i64, i32, vp, vp, w4, w4, vp, i32, vp, vp]
     for name in OPS_EXPORTED:
         getattr(lib, name).restype = i32
     _bound = lib
@@ -259,6 +275,47 @@ class MoeOps:
                               out)
         if s:
             _check(s, "moe_fp8_wgrad")
+        return out
+
+    # --------------------------------------------------------- 4-bit weights
+    def quant_w4(self, w, group=128, zero=False, out=None, stream=None) -> dict:
+        """moe_quant_w4. w [N, K] or [G, N, K] bf16 -> {"codes", "scale", "group"} and, with zero points, {"zero"}.
+
+        The dict is what w4_matmul and w4_experts take as weights.
+        """
+        if stream is not None:
+            return self._on(stream, self.quant_w4, w, group, zero, out)
+        if out is None:
+            out = {}
+        s = self._b.quant_w4(self.h, self._index, self._stream(), w, group, zero, out)
+        if s:
+            _check(s, "moe_quant_w4")
+        out["group"] = group
+        return out
+
+    def w4_matmul(self, x, w, off=None, row_index=None, out=None, out_dtype=torch.bfloat16, stream=None):
+        """moe_w4_matmul. x [rows, K] bf16 (rows may be strided), w as quant_w4 gives it for [N, K] or (with off)
+        [G, N, K] -> [M, N]."""
+        if stream is not None:
+            return self._on(stream, self.w4_matmul, x, w, off, row_index, out, out_dtype)
+        if out is None:
+            rows = x.shape[0] if row_index is None else row_index.numel()
+            out = torch.empty((rows, w["codes"].shape[-2]), dtype=out_dtype, device=self.device)
+        s = self._b.w4_matmul(self.h, self._index, self._stream(), x, w, off, row_index, out)
+        if s:
+            _check(s, "moe_w4_matmul")
+        return out
+
+    def w4_experts(self, x, idx, gate, w13, wd, n_shared=0, out=None, out_dtype=torch.bfloat16, stream=None):
+        """moe_w4_experts. x [T, d] bf16, idx and gate [T, k] as gate() gives them, w13 and wd as quant_w4 gives them
+        for [E + n_shared, 2f, d] (gate half, up half) and [E + n_shared, d, f] -> y [T, d]."""
+        if stream is not None:
+            return self._on(stream, self.w4_experts, x, idx, gate, w13, wd, n_shared, out, out_dtype)
+        if out is None:
+            out = torch.empty(x.shape, dtype=out_dtype, device=self.device)
+        s = self._b.w4_experts(self.h, self._index, self._stream(), x, idx, gate, w13, wd, n_shared, out)
+        if s:
+            _check(s, "moe_w4_experts")
         return out
 
 

@@ -149,3 +149,74 @@ def matmul(a, b, off=None, row_index=None):
     c = [a[off[g]:off[g + 1]] @ b[g].T for g in range(len(off) - 1)]
     s = [np.abs(a[off[g]:off[g + 1]]) @ np.abs(b[g]).T for g in range(len(off) - 1)]
     return np.concatenate(c), np.concatenate(s)
+
+
+# ---- 4-bit weights: code order of a word's eight values, (code - zero) * scale
+
+W4_SHIFT = np.array([0, 16, 4, 20, 8, 24, 12, 28])
+
+
+def bf16(v):
+    """fp32 values rounded to bf16, to nearest, ties to even (finite values)."""
+    u = np.asarray(v, np.float32).view(np.uint32).astype(np.uint64)
+    u = (u + 0x7fff + ((u >> 16) & 1)) >> 16 << 16
+    return u.astype(np.uint32).view(np.float32).astype(np.float64)
+
+
+def w4_pack(codes):
+    c = np.asarray(codes, np.uint64).reshape(*codes.shape[:-1], -1, 8)
+    return (c << W4_SHIFT.astype(np.uint64)).sum(-1).astype(np.uint32).view(np.int32)
+
+
+def w4_unpack(words):
+    w = np.asarray(words).view(np.uint32)
+    return ((w[..., None] >> W4_SHIFT.astype(np.uint32)) & 15).reshape(*w.shape[:-1], -1).astype(np.float64)
+
+
+def w4_values(words, scale, zero, group):
+    """Values [N, K] of one matrix: words [N, K/8], scale and zero [KG, N] (zero None: 8)."""
+    c = w4_unpack(words)
+    at = np.arange(c.shape[1]) // group
+    return (c - (8.0 if zero is None else zero.T[:, at])) * scale.T[:, at]
+
+
+def quant_w4(w, group, with_zero):
+    """codes [N, K], scale and zero [KG, N] of w [N, K]: quotients in fp32, the scale rounded to bf16 first."""
+    w = np.asarray(w, np.float32)
+    N, K = w.shape
+    KG = -(-K // group)
+    codes, scale, zero = np.empty((N, K)), np.empty((KG, N)), np.empty((KG, N))
+    with np.errstate(divide="ignore", invalid="ignore", over="ignore"):
+        for i in range(KG):
+            v = w[:, i * group:(i + 1) * group]
+            lo, hi = np.minimum(v.min(1), 0), np.maximum(v.max(1), 0)
+            s = bf16((hi - lo) / np.float32(15) if with_zero else np.abs(v).max(1) / np.float32(7)).astype(np.float32)
+            live = (s > 0) & np.isfinite(s)
+            z = np.clip(np.rint(-lo / s), 0, 15) if with_zero else np.full(N, 8.0, np.float32)
+            z = np.where(live, z, 0.0 if with_zero else 8.0)
+            codes[:, i * group:(i + 1) * group] = np.where(live[:, None], np.clip(np.rint(v / s[:, None]) + z[:, None], 0, 15),
+                                                           z[:, None])
+            scale[i], zero[i] = s, z
+    return codes, scale, zero
+
+
+def w4_experts(x, idx, gate, w13, wd, n_shared, add):
+    """(y, bound) of the experts' layer: w13 and wd lists of [2f, d] and [d, f] values. `add` is what an fp32 sum over
+    d or f may be off, relative to the sum of its terms' magnitudes; bound is what y may be off before it is rounded:
+    the products' sums, SwiGLU with the fast exponential and division (2^-18), and h kept to 2^-16."""
+    T = x.shape[0]
+    E = len(w13) - n_shared
+    y, bound = np.zeros((T, wd[0].shape[0])), np.zeros((T, wd[0].shape[0]))
+    with np.errstate(invalid="ignore", over="ignore"):
+        for t in range(T):
+            use = [(e, g) for e, g in zip(idx[t], gate[t]) if 0 <= e < E] + [(E + s, 1.0) for s in range(n_shared)]
+            for e, g in use:
+                f = wd[e].shape[1]
+                gu, size = w13[e] @ x[t], np.abs(w13[e]) @ np.abs(x[t])
+                a, u, sa, su = gu[:f], gu[f:], size[:f], size[f:]
+                s = a / (1 + np.exp(-a))
+                h = g * s * u
+                off = np.abs(g) * add * (1.1 * np.abs(u) * sa + np.abs(s) * su) + (2.0 ** -18 + 2.0 ** -16) * np.abs(h)
+                y[t] += wd[e] @ h
+                bound[t] += np.abs(wd[e]) @ (off + add * np.abs(h))
+    return y, bound

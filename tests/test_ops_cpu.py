@@ -213,3 +213,88 @@ def test_gate_gradient_against_differences(router, renorm):
     f = lambda z: (oo.gate(z, b, **kw)[1] * dg).sum()  # noqa: E731  (the selection does not move)
     got, _ = oo.gate_backward(l, idx, dg, router, renorm, 2.5)
     assert np.allclose(got, _numeric(f, l), atol=1e-7)
+
+
+# --------------------------------------------------------- 4-bit weights
+
+def w4(**over):
+    return ctypes.byref(mops.moe_w4(**{**dict(codes=P, scale=P, zero=None, group=64), **over}))
+
+
+W4MM = dict(ops=P, x=P, ld=256, x_rows=8, row_index=None, M=8, w=None, off=None, G=1, N=128, K=256, c=P, out=1, stream=None)
+
+
+@pytest.mark.parametrize("over,wover,code", [
+    (dict(ops=None), {}, ARG), (dict(M=-1), {}, ARG), (dict(N=0), {}, ARG), (dict(K=0), {}, ARG), (dict(G=0), {}, ARG),
+    (dict(G=2), {}, ARG), (dict(x_rows=7), {}, ARG), (dict(out=2), {}, ARG), (dict(ld=248), {}, ARG),
+    (dict(x=None), {}, ARG), (dict(c=None), {}, ARG), (dict(row_index=P, x_rows=0), {}, ARG),
+    ({}, dict(codes=None), ARG), ({}, dict(scale=None), ARG),
+    ({}, dict(group=16), UNSUP), ({}, dict(group=0), UNSUP), ({}, dict(codes=P + 8), UNSUP), ({}, dict(scale=P + 8), UNSUP),
+    ({}, dict(zero=P + 4), UNSUP), (dict(N=132), {}, UNSUP), (dict(K=240), {}, UNSUP), (dict(G=257, off=P), {}, UNSUP),
+    (dict(x=P + 8), {}, UNSUP), (dict(ld=260), {}, UNSUP), (dict(c=P + 2), {}, UNSUP),
+    (dict(M=1 << 29, x_rows=1 << 29), {}, UNSUP), (dict(x_rows=1 << 30, ld=1024), {}, UNSUP),
+])
+def test_w4_matmul_refuses(lib, over, wover, code):
+    assert call(lib, "moe_w4_matmul", {**W4MM, "w": w4(**wover)}, over) == code
+
+
+def test_w4_matmul_of_no_rows_does_nothing(lib):
+    assert call(lib, "moe_w4_matmul", {**W4MM, "w": w4()}, dict(M=0, x=None, c=None, x_rows=0)) == OK
+    assert call(lib, "moe_w4_matmul", W4MM, {}) == ARG
+
+
+W4L = dict(ops=P, cfg=None, x=P, ld=256, T=4, idx=P, gate=P, w13=None, wd=None, y=P, out=1, workspace=P, stream=None)
+
+
+@pytest.mark.parametrize("cover,over,wover,code", [
+    ({}, dict(ops=None), {}, ARG), (dict(E=0), {}, {}, ARG), (dict(k=0), {}, {}, ARG), (dict(n_shared=-1), {}, {}, ARG),
+    (dict(d=0), {}, {}, ARG), (dict(f=0), {}, {}, ARG), ({}, dict(T=-1), {}, ARG), (dict(E=257), {}, {}, UNSUP),
+    (dict(k=9), {}, {}, UNSUP), (dict(n_shared=9), {}, {}, UNSUP), ({}, dict(T=65), {}, UNSUP),
+    (dict(d=240), {}, {}, UNSUP), (dict(f=80), {}, {}, UNSUP), ({}, dict(out=2), {}, ARG), ({}, dict(x=None), {}, ARG),
+    ({}, dict(idx=None), {}, ARG), ({}, dict(gate=None), {}, ARG), ({}, dict(y=None), {}, ARG), ({}, dict(ld=128), {}, ARG),
+    ({}, dict(ld=260), {}, UNSUP), ({}, dict(x=P + 8), {}, UNSUP), ({}, dict(y=P + 2), {}, UNSUP),
+    ({}, dict(workspace=None), {}, WS), ({}, dict(workspace=P + 8), {}, WS), ({}, {}, dict(group=32), UNSUP),
+    ({}, {}, dict(zero=P), UNSUP), ({}, {}, dict(codes=None), ARG),
+])
+def test_w4_experts_refuse(lib, cover, over, wover, code):
+    c = mops.moe_w4_config(**{**dict(E=8, n_shared=1, k=2, d=256, f=128), **cover})
+    assert call(lib, "moe_w4_experts", {**W4L, "cfg": ctypes.byref(c), "w13": w4(), "wd": w4(**wover)}, over) == code
+
+
+def test_w4_experts_without_tokens_and_its_workspace(lib):
+    c, n = mops.moe_w4_config(8, 1, 2, 256, 128), ctypes.c_size_t()
+    assert call(lib, "moe_w4_experts", {**W4L, "cfg": ctypes.byref(c), "w13": w4(), "wd": w4()},
+                dict(T=0, x=None, idx=None, gate=None, y=None, workspace=None)) == OK
+    assert lib.moe_w4_experts_workspace_size(ctypes.byref(c), 4, ctypes.byref(n)) == OK
+    assert n.value == 4 * 3 * 2 * 128 * 2        # pairs, two bf16 of each value of h
+    assert lib.moe_w4_experts_workspace_size(ctypes.byref(c), 4, None) == ARG
+    assert lib.moe_w4_experts_workspace_size(None, 4, ctypes.byref(n)) == ARG
+
+
+@pytest.mark.parametrize("args,code", [
+    ((P, None, 1, 64, 64, 32, P, P, None, None), ARG), ((P, P, 1, 64, 64, 32, None, P, None, None), ARG),
+    ((P, P, 1, 64, 64, 32, P, None, None, None), ARG), ((P, P, 0, 64, 64, 32, P, P, None, None), ARG),
+    ((P, P, 1, 64, 64, 48, P, P, None, None), UNSUP), ((P, P, 1, 60, 64, 32, P, P, None, None), UNSUP),
+    ((P, P, 1, 64, 48, 32, P, P, None, None), UNSUP), ((P, P + 8, 1, 64, 64, 32, P, P, None, None), UNSUP),
+    ((P, P, 1, 64, 64, 32, P, P, P + 4, None), UNSUP), ((P, P, 1 << 20, 1 << 10, 128, 32, P, P, None, None), UNSUP),
+])
+def test_quant_w4_refuses(lib, args, code):
+    assert lib.moe_quant_w4(*args) == code
+
+
+def test_w4_words_and_values():
+    """The order of the codes in a word, and the quantiser's bounds: half a step of the scale where nothing is clamped."""
+    codes = np.arange(8)[None]
+    assert oo.w4_pack(codes).view(np.uint32)[0, 0] == 0x75316420
+    rng = np.random.default_rng(3)
+    c = rng.integers(0, 16, (5, 64))
+    assert np.array_equal(oo.w4_unpack(oo.w4_pack(c)), c)
+    w = torch.from_numpy(rng.normal(size=(16, 160))).to(torch.bfloat16).float().numpy()
+    for group in (32, 64, 128):
+        for zero in (False, True):
+            codes, scale, z = oo.quant_w4(w, group, zero)
+            back = oo.w4_values(oo.w4_pack(codes), scale, z if zero else None, group)
+            step = scale.T[:, np.arange(160) // group]
+            # the scale's own rounding (2^-9 of up to 15 steps) and the zero point's (half a step) add to half a step
+            assert np.all(np.abs(back - w) <= step * (0.5 + 15 * 2.0 ** -8 + (0.5 if zero else 0.0)))
+    assert np.array_equal(oo.bf16(w), w.astype(np.float64))
