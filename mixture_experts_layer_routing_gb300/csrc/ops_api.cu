@@ -335,7 +335,7 @@ moe_status moe_w4_matmul(moe_ops ops, const void* x, long long ld_x, int x_rows,
   CHECK((ceil_div(M, 8) + (long long)G) * ceil_div(N, 16) < (1ll << 30), MOE_ERR_UNSUPPORTED);   // units
   if (M == 0) return MOE_OK;
   CHECK(x && c && x_rows >= 1 && ld_x >= K, MOE_ERR_INVALID_ARG);
-  CHECK(ld_x % 8 == 0 && aligned(x, 16) && aligned(c, 4), MOE_ERR_UNSUPPORTED);
+  CHECK(ld_x % 8 == 0 && aligned(x, 16) && aligned(c, 16), MOE_ERR_UNSUPPORTED);
   CHECK((long long)x_rows <= 0xffffffffll / (ld_x / 8), MOE_ERR_UNSUPPORTED);   // row starts in units of 16 bytes
   HANDLE(ops);
   DONE(w4_matmul(ops, x, ld_x, x_rows, row_index, M, *w, off, G, N, K, c, out_dtype == MOE_FP32, (cudaStream_t)stream,
@@ -362,7 +362,7 @@ moe_status moe_w4_experts(moe_ops ops, const moe_w4_config* cfg, const void* x, 
   CHECK(w13->group == wd->group && (w13->zero != nullptr) == (wd->zero != nullptr), MOE_ERR_UNSUPPORTED);
   if (T == 0) return MOE_OK;
   CHECK(x && idx && gate && y && ld_x >= cfg->d, MOE_ERR_INVALID_ARG);
-  CHECK(ld_x % 8 == 0 && ld_x < (1ll << 28) && aligned(x, 16) && aligned(y, 4), MOE_ERR_UNSUPPORTED);
+  CHECK(ld_x % 8 == 0 && ld_x < (1ll << 28) && aligned(x, 16) && aligned(y, 16), MOE_ERR_UNSUPPORTED);
   CHECK(workspace && aligned(workspace, 16), MOE_ERR_WORKSPACE);
   HANDLE(ops);
   DONE(w4_experts(ops, *cfg, x, ld_x, T, idx, gate, *w13, *wd, y, out_dtype == MOE_FP32, workspace,

@@ -7,51 +7,64 @@ namespace moe {
 namespace {
 
 constexpr int kMaxSlots = 264;               // experts, shared ones included
-constexpr int kMaxPairs = 64 * 16;           // (token, expert) pairs
-constexpr int kThreads = kW4Warps * 32;
+constexpr int kSlotsEach = 3;                // of a thread that counts: CTAs have at least 4 warps
 
-// The experts in use and their tokens, made by every CTA of both kernels from idx alone. Pairs are sorted by expert,
-// then token; an expert that a token names twice is one pair with both gates. A tile is up to `rows` pairs of a slot.
-struct LayerLists {
-  unsigned mask[kMaxSlots][2];               // tokens of a slot
-  int pair[kMaxSlots + 1], tile[kMaxSlots + 1];
-  uint16_t slot_of[kMaxPairs];
-  uint8_t token[kMaxPairs];
+// The experts in use and their tokens, made by every CTA of both kernels from idx alone. Pairs (token, expert) are
+// sorted by expert, then token; an expert that a token names twice is one pair with both gates. A tile is up to `rows`
+// pairs of a slot. TMAX is 16 or 64 (shared memory is what two CTAs on an SM run short of).
+template <int TMAX> struct LayerLists {
+  static constexpr int kPairs = TMAX * 16, kWords = (TMAX + 31) / 32;
+  unsigned mask[kMaxSlots][kWords];          // tokens of a slot
+  uint16_t pair[kMaxSlots + 1], tile[kMaxSlots + 1];
+  uint16_t slot_of_tile[kPairs];
+  uint8_t token[kPairs];
   int tmp[kW4Warps];
+};
+template <int TMAX> struct LayerGates {
+  int idx[TMAX * 8];
+  float gate[TMAX * 8];
 };
 
 struct W4LayerParams {
-  const uint8_t* x;
-  unsigned ld16;
+  const bf16* x;
+  unsigned ld16;          // row of x in units of 16 bytes
   int T, k, E, slots, d, f;
   const int* idx;
   const float* gate;
   W4 w13, wd;
   W4Shape s13, sd;
-  uint8_t* h;             // [pairs][2][f] bf16: rounded, and what the rounding left
+  bf16* h;                // [pairs][2][f] bf16: rounded, and what the rounding left
   void* y;
   int out_fp32;
   int* status;
 };
 
-__device__ __forceinline__ void build_lists(LayerLists& L, const W4LayerParams& P, int rows) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const unsigned all[2] = {P.T >= 32 ? ~0u : (1u << P.T) - 1u, P.T >= 64 ? ~0u : P.T > 32 ? (1u << (P.T - 32)) - 1u : 0u};
-  for (int i = tid; i < P.slots; i += kThreads) {
-    L.mask[i][0] = i < P.E ? 0u : all[0];
-    L.mask[i][1] = i < P.E ? 0u : all[1];
+template <int TMAX>
+__device__ __forceinline__ void build_lists(LayerLists<TMAX>& L, LayerGates<TMAX>* gates, const W4LayerParams& P, int rows) {
+  constexpr int kWords = LayerLists<TMAX>::kWords;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, kThreads = blockDim.x;
+  for (int i = tid; i < P.slots * kWords; i += kThreads) {
+    const int n = P.T - 32 * (i % kWords);   // tokens from this word on
+    L.mask[i / kWords][i % kWords] = i / kWords < P.E || n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u;
   }
   __syncthreads();
   for (int i = tid; i < P.T * P.k; i += kThreads) {
     const int e = P.idx[i], t = i / P.k;
+    if (gates) {
+      gates->idx[i] = e;
+      gates->gate[i] = P.gate[i];
+    }
     if ((unsigned)e < (unsigned)P.E) atomicOr(&L.mask[e][t >> 5], 1u << (t & 31));
     else set_error(P.status, MOE_ERR_DEVICE_INDEX);
   }
   __syncthreads();
-  int n[2], v = 0;                           // two slots a thread; tiles in the high half
+  int n[kSlotsEach], v = 0;                  // tiles in the high half
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int i = 2 * tid + j, r = i < P.slots ? __popc(L.mask[i][0]) + __popc(L.mask[i][1]) : 0;
+  for (int j = 0; j < kSlotsEach; ++j) {
+    const int i = kSlotsEach * tid + j;
+    int r = 0;
+    if (i < P.slots)
+      for (int h = 0; h < kWords; ++h) r += __popc(L.mask[i][h]);
     n[j] = ((r + rows - 1) / rows << 16) + r;
     v += n[j];
   }
@@ -63,264 +76,296 @@ __device__ __forceinline__ void build_lists(LayerLists& L, const W4LayerParams& 
   if (lane == 31) L.tmp[warp] = v;
   __syncthreads();
   for (int i = 0; i < warp; ++i) v += L.tmp[i];
-  int before = v - n[0] - n[1];
+  int before = v;
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int i = 2 * tid + j;
+  for (int j = 0; j < kSlotsEach; ++j) before -= n[j];
+#pragma unroll
+  for (int j = 0; j < kSlotsEach; ++j) {
+    const int i = kSlotsEach * tid + j;
     if (i <= P.slots) {
-      L.pair[i] = before & 0xffff;
-      L.tile[i] = before >> 16;
+      L.pair[i] = (uint16_t)before;
+      L.tile[i] = (uint16_t)(before >> 16);
     }
     if (i < P.slots) {
       int p = before & 0xffff;
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        for (unsigned m = L.mask[i][h]; m; m &= m - 1) {
-          L.token[p] = (uint8_t)(h * 32 + __ffs(m) - 1);
-          L.slot_of[p++] = (uint16_t)i;
-        }
+      for (int h = 0; h < kWords; ++h)
+        for (unsigned m = L.mask[i][h]; m; m &= m - 1) L.token[p++] = (uint8_t)(h * 32 + __ffs(m) - 1);
+      for (int k = before >> 16; k < (before + n[j]) >> 16; ++k) L.slot_of_tile[k] = (uint16_t)i;
     }
     before += n[j];
   }
   __syncthreads();
 }
 // Slot of a tile, its first pair and how many.
-__device__ __forceinline__ int find_tile(const LayerLists& L, const W4LayerParams& P, int tile, int rows, int& pair0, int& R) {
-  int lo = 0, hi = P.slots;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (L.tile[mid] <= tile) lo = mid; else hi = mid;
-  }
-  pair0 = L.pair[lo] + (tile - L.tile[lo]) * rows;
-  R = min(rows, L.pair[lo + 1] - pair0);
-  return lo;
+template <int TMAX>
+__device__ __forceinline__ int find_tile(const LayerLists<TMAX>& L, int tile, int rows, int& pair0, int& R) {
+  const int e = L.slot_of_tile[tile];
+  pair0 = L.pair[e] + (tile - L.tile[e]) * rows;
+  R = min(rows, L.pair[e + 1] - pair0);
+  return e;
 }
 
-constexpr int kUpStages = 3, kDownStages = 3;
-
-template <int NT, int GROUP, bool ZERO> struct W4UpSmem {
-  W4Stage<2, NT, GROUP, ZERO> stage[kW4Warps][kUpStages];
-  float part[2][kW4Warps][NT * 8][36];       // [pair][16 gate rows, 16 up rows]
-  LayerLists lists;
-  float gate[kMaxPairs];
-};
-
-// Gate and up rows of 16 values of h, up to 8 NT pairs of an expert, for each unit; warps split K = d.
-template <int NT, int GROUP, bool ZERO>
-__global__ void __launch_bounds__(kThreads, 1) w4_up_kernel(W4LayerParams P) {
-  using Core = W4Core<2, NT, GROUP, ZERO>;
-  constexpr int kRows = Core::kRows;
-  extern __shared__ __align__(128) uint8_t smem_raw[];
-  auto& sm = *reinterpret_cast<W4UpSmem<NT, GROUP, ZERO>*>(smem_raw);
-  LayerLists& L = sm.lists;
+// Gate and up rows of MT x 8 values of h, up to XR pairs of an expert, for each unit (a tile of 16 weight rows is 8 gate
+// rows and the 8 up rows of the same values). A unit's chunks are dealt to the warps in turn; the last warp adds up the
+// others' sums, in a fixed order, and applies SwiGLU and the gate.
+template <int MT, int XR, int TMAX, int GROUP, bool ZERO>
+__global__ void __launch_bounds__(kW4Warps * 32, 1) w4_up_kernel(W4LayerParams P) {
+  using Core = W4Core<MT, XR, GROUP, ZERO>;
+  constexpr int kCols = MT * 8, kPitch = Core::kPitch, kSums = XR * kPitch;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ LayerLists<TMAX> L;
+  __shared__ LayerGates<TMAX> gates;
+  __shared__ W4Handover<kSumBuffers> hand;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = (blockDim.x >> 5) - 1;
+  if (tid == 0) hand.init(warps);
   griddep_wait();
   griddep_launch();
-  build_lists(L, P, kRows);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int p = tid; p < L.pair[P.slots]; p += kThreads) {
-    const int t = L.token[p], e = L.slot_of[p];
-    float g = e < P.E ? 0.f : 1.f;
-    if (e < P.E)
-      for (int j = 0; j < P.k; ++j)
-        if (P.idx[t * P.k + j] == e) g += P.gate[t * P.k + j];
-    sm.gate[p] = g;
-  }
-  const int blocks = P.f / 16, units = L.tile[P.slots] * blocks;
-  const int C = (P.d + kChunk - 1) / kChunk, c0 = C * warp / kW4Warps, c1 = C * (warp + 1) / kW4Warps;
-  Core core;
-  core.px = P.x;
-  int lu = blockIdx.x, lc = c0;
-  const auto issue = [&](int slot) {
-    if (lu < units && c0 < c1) {
-      if (lc == c0) {
-        int pair0, R;
-        const int tile = lu / blocks, m = lu - tile * blocks, e = find_tile(L, P, tile, kRows, pair0, R);
-        const int row0[2] = {m * 16, P.f + m * 16}, end[2] = {P.f, 2 * P.f};
-        core.set_weights(w4_matrix(P.w13, P.s13, e), P.s13, row0, end, lane);
-        core.xn = (R + 1) / 2;
-#pragma unroll
-        for (int i = 0; i < NT * 4; ++i) {
-          const int r = (lane >> 4) + 2 * i;
-          core.xoff[i] = r < R ? (unsigned)L.token[pair0 + r] * P.ld16 : ~0u;
+  build_lists(L, &gates, P, XR);
+  float* sums = reinterpret_cast<float*>(smem + warps * Core::kBytes);     // [kSumBuffers][warp][XR][kPitch]
+  const int blocks = P.f / kCols, tiles = L.tile[P.slots], C = (P.d + kChunk - 1) / kChunk;
+  const int units = tiles * blocks, u0 = (int)((long long)units * blockIdx.x / gridDim.x);      // this CTA's, in a row
+  const int u1 = (int)((long long)units * (blockIdx.x + 1) / gridDim.x);
+  int tile = u0 / blocks, m = u0 - tile * blocks, pair0 = 0, R = 0;
+  if (warp == warps) {
+    for (int u = u0; u < u1; ++u) {
+      const int e = find_tile(L, tile, XR, pair0, R);
+      hand.wait_full(u - u0, P.status);
+      const float* from = sums + (u - u0) % kSumBuffers * warps * kSums;
+      for (int i = lane; i < R * kCols; i += 32) {
+        const int r = i / kCols, j = i % kCols, at = r * kPitch + (j / 8) * 16 + j % 8, t = L.token[pair0 + r];
+        float g = 0.f, up = 0.f, gate = e < P.E ? 0.f : 1.f;
+        if (e < P.E)
+          for (int q = 0; q < P.k; ++q)
+            if (gates.idx[t * P.k + q] == e) gate += gates.gate[t * P.k + q];
+#pragma unroll 4
+        for (int w = 0; w < warps; ++w) {
+          g += from[w * kSums + at];
+          up += from[w * kSums + at + 8];
         }
+        const float h = silu_f(g) * up * gate;
+        // h as a sum of two bf16 (16 bits of mantissa), so that the layer rounds once, at its output
+        const bf16 hi = __float2bfloat16_rn(h);
+        const float rest = h - __bfloat162float(hi);
+        const bf16 lo = __float2bfloat16_rn(fabsf(rest) <= 3.3895314e38f ? rest : 0.f);
+        bf16* dst = P.h + (long long)(pair0 + r) * 2 * P.f + m * kCols + j;
+        dst[0] = hi;
+        dst[P.f] = lo;
       }
-      core.copy_weights(sm.stage[warp][slot], P.s13, lc, lane);
-      core.copy_x(sm.stage[warp][slot], P.s13, lc, lane);
-      if (++lc == c1) {
-        lc = c0;
-        lu += gridDim.x;
+      hand.taken(u - u0, lane);
+      if (++m == blocks) m = 0, ++tile;
+    }
+    return;
+  }
+  Core core;
+  core.init(smem + warp * Core::kBytes, warps, lane);
+  W4Cursor w(u0, tile, m, warp, C, blocks), x = w;      // the next chunks of the weights and of x to read
+  int aimed = -1, xt = -1, xR = 0;
+  const auto issue = [&](unsigned to) {
+    if (w.u < u1) {
+      if (w.tile != aimed) {
+        aimed = w.tile;
+        int row0[MT], up0[MT];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) row0[i] = w.m * kCols + i * 8, up0[i] = P.f + row0[i];
+        core.aim(w4_matrix(P.w13, P.s13, L.slot_of_tile[aimed]), P.s13, row0, up0, 2 * P.f, w.c, lane);
       }
+      core.copy(P.s13, to, lane);
+      for (int n = w.next(warps, C, blocks); n > 0; --n) core.step(P.s13, kCols, C);
     }
     cp_commit();
   };
+  const auto read_x = [&]() {
+    if (x.u >= u1) return;
+    if (x.tile != xt) {
+      xt = x.tile;
+      int p0;
+      find_tile(L, xt, XR, p0, xR);
 #pragma unroll
-  for (int i = 0; i < kUpStages - 1; ++i) issue(i);
-  __syncthreads();        // the gates
-  int slot = 0, buf = 0;
-  for (int u = blockIdx.x; u < units; u += gridDim.x, buf ^= 1) {
-    int pair0, R;
-    const int tile = u / blocks, m = u - tile * blocks;
-    find_tile(L, P, tile, kRows, pair0, R);
-    float acc[2][NT][4] = {};
-    for (int c = c0; c < c1; ++c) {
-      cp_wait<kUpStages - 2>();
+      for (int r = 0; r < XR; ++r) core.xoff[r] = r < xR ? L.token[p0 + r] * P.ld16 : 0u;
+    }
+    core.read_x(P.x, x.c, P.d, xR, ~0u, lane);
+    x.next(warps, C, blocks);
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) issue(i * Core::kStage);
+  read_x();
+  int c = warp;
+  for (int u = u0; u < u1; ++u) {
+    find_tile(L, tile, XR, pair0, R);
+    float acc[MT][4] = {};
+    for (; c < C; c += warps) {
+      cp_wait<kStages - 2>();
       __syncwarp();
-      issue(slot == 0 ? kUpStages - 1 : slot - 1);
-      Core::multiply(sm.stage[warp][slot], acc, (R + 7) / 8, lane);
-      slot = slot + 1 == kUpStages ? 0 : slot + 1;
+      issue(core.free_slot());
+      core.store_x(R);
+      read_x();
+      __syncwarp();
+      core.multiply(acc, P.d - c * kChunk, lane);
+      core.next();
     }
-    const int quad = lane >> 2, t = lane & 3;
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-        float(*p)[36] = &sm.part[buf][warp][n * 8 + 2 * t];
-        p[0][mt * 16 + quad] = acc[mt][n][0];
-        p[1][mt * 16 + quad] = acc[mt][n][1];
-        p[0][mt * 16 + quad + 8] = acc[mt][n][2];
-        p[1][mt * 16 + quad + 8] = acc[mt][n][3];
-      }
-    __syncthreads();      // (the buffer before the last one has been read by all when they are here)
-    for (int i = tid; i < R * 16; i += kThreads) {
-      const int r = i >> 4, j = i & 15;
-      float g = 0.f, up = 0.f;
-#pragma unroll
-      for (int w = 0; w < kW4Warps; ++w) {
-        g += sm.part[buf][w][r][j];
-        up += sm.part[buf][w][r][16 + j];
-      }
-      const float h = silu_f(g) * up * sm.gate[pair0 + r];
-      // h as a sum of two bf16 (16 bits of mantissa), so that the layer rounds once, at its output
-      const bf16 hi = __float2bfloat16_rn(h);
-      const float left = h - __bfloat162float(hi);
-      const bf16 lo = __float2bfloat16_rn(fabsf(left) <= 3.3895314e38f ? left : 0.f);
-      bf16* dst = reinterpret_cast<bf16*>(P.h) + (long long)(pair0 + r) * 2 * P.f + m * 16 + j;
-      dst[0] = hi;
-      dst[P.f] = lo;
-    }
+    c -= C;
+    hand.wait_empty(u - u0, P.status);
+    core.put(acc, sums + ((u - u0) % kSumBuffers * warps + warp) * kSums, R, lane);
+    hand.put(u - u0, lane);
+    if (++m == blocks) m = 0, ++tile;
   }
 }
 
-template <int NT, int GROUP, bool ZERO> struct W4DownSmem {
-  W4Stage<1, NT, GROUP, ZERO> stage[kW4Warps][kDownStages];
-  LayerLists lists;
-  // float sum[kW4Warps][T][20] follows: [token][16 rows]
-};
+constexpr int down_buffers(int tmax) { return tmax > 16 ? 1 : 2; }      // (of all tokens' sums, a warp)
 
-// 16 values of y for all tokens a unit. The chunks of all experts in use are dealt to the warps; columns 2r and 2r + 1
-// of a product are the two parts of pair r's h, and a warp adds an expert's product to its own sums of the tokens.
-template <int NT, int GROUP, bool ZERO>
-__global__ void __launch_bounds__(kThreads, 1) w4_down_kernel(W4LayerParams P) {
-  using Core = W4Core<1, NT, GROUP, ZERO>;
-  constexpr int kPairs = Core::kRows / 2;
-  extern __shared__ __align__(128) uint8_t smem_raw[];
-  auto& sm = *reinterpret_cast<W4DownSmem<NT, GROUP, ZERO>*>(smem_raw);
-  LayerLists& L = sm.lists;
-  float(*sum)[20] = reinterpret_cast<float(*)[20]>(smem_raw + sizeof(W4DownSmem<NT, GROUP, ZERO>));
-  // idx was written before the kernel in front of this one began; only h is that kernel's
-  build_lists(L, P, kPairs);
-  griddep_wait();
-  griddep_launch();
+// MT x 16 values of y for all tokens a unit. The chunks of all experts in use are dealt to the warps in runs; rows 2r and
+// 2r + 1 of a tile are the two parts of pair r's h, and a warp adds an expert's product to its own sums of the tokens,
+// which the last warp adds up.
+template <int MT, int XR, int TMAX, int GROUP, bool ZERO>
+__global__ void __launch_bounds__(kW4Warps * 32, 1) w4_down_kernel(W4LayerParams P) {
+  using Core = W4Core<MT, XR, GROUP, ZERO>;
+  constexpr int kPairs = XR / 2, kCols = MT * 16, kPitch = Core::kPitch, kBufs = down_buffers(TMAX);
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ LayerLists<TMAX> L;
+  __shared__ W4Handover<kBufs> hand;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, quad = lane >> 2, t = lane & 3;
-  const int units = (P.d + 15) / 16, C = (P.f + kChunk - 1) / kChunk, items = L.tile[P.slots] * C;
-  const int q0 = (int)((long long)items * warp / kW4Warps), q1 = (int)((long long)items * (warp + 1) / kW4Warps);
-  float(*mine)[20] = sum + warp * P.T;
-  Core core;
-  core.px = P.h;
-  int lu = blockIdx.x, lq = q0, lc = 0, ltile = 0;
-  const auto issue = [&](int slot) {
-    if (lu < units && q0 < q1) {
-      if (lq == q0 || lc == C) {
-        if (lq == q0) ltile = q0 / C, lc = q0 - ltile * C;
-        else ++ltile, lc = 0;
-        int pair0, R;
-        const int e = find_tile(L, P, ltile, kPairs, pair0, R);
-        const int row0[1] = {lu * 16}, end[1] = {P.d};
-        core.set_weights(w4_matrix(P.wd, P.sd, e), P.sd, row0, end, lane);
-        core.xn = R;
-#pragma unroll
-        for (int i = 0; i < NT * 4; ++i) {
-          const int r = (lane >> 4) + 2 * i;
-          core.xoff[i] = r < 2 * R ? (unsigned)(2 * pair0 + r) * (unsigned)(P.f / 8) : ~0u;
+  const int warps = (blockDim.x >> 5) - 1;
+  if (tid == 0) hand.init(warps);
+  // idx was written before the kernel in front of this one began; only h is that kernel's
+  build_lists(L, (LayerGates<TMAX>*)nullptr, P, kPairs);
+  float(*sums)[kPitch] = reinterpret_cast<float(*)[kPitch]>(smem + warps * Core::kBytes);   // [kBufs][warp][token][kCols]
+  const int units = (P.d + kCols - 1) / kCols, C = (P.f + kChunk - 1) / kChunk, items = L.tile[P.slots] * C;
+  if (warp == warps) {
+    griddep_wait();
+    griddep_launch();
+    for (int u = blockIdx.x, i = 0; u < units; u += gridDim.x, ++i) {
+      hand.wait_full(i, P.status);
+      const float(*from)[kPitch] = sums + (i % kBufs) * warps * P.T;
+      for (int q = lane; q < P.T * (kCols / 4); q += 32) {
+        const int r = q / (kCols / 4), j = q % (kCols / 4) * 4, col = u * kCols + j;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int w = 0; w < warps; ++w) {
+          const float4 a = *reinterpret_cast<const float4*>(&from[w * P.T + r][j]);
+          v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
+        }
+        if (col < P.d) {       // (d is a multiple of 32)
+          const long long to = (long long)r * P.d + col;
+          if (P.out_fp32) *reinterpret_cast<float4*>(reinterpret_cast<float*>(P.y) + to) = v;
+          else *reinterpret_cast<uint2*>(reinterpret_cast<bf16*>(P.y) + to) = make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
         }
       }
-      core.copy_weights(sm.stage[warp][slot], P.sd, lc, lane);
-      core.copy_x(sm.stage[warp][slot], P.sd, lc, lane);
-      ++lc;
-      if (++lq == q1) {
-        lq = q0;
-        lu += gridDim.x;
+      hand.taken(i, lane);
+    }
+    return;
+  }
+  const int q0 = items * warp / warps, n = items * (warp + 1) / warps - q0;
+  const int tile0 = q0 / C, c0 = q0 - tile0 * C;
+  Core core;
+  core.init(smem + warp * Core::kBytes, 1, lane);
+  int lu = n ? blockIdx.x : units, left = 0, lc = 0, ltile = 0;
+  const auto issue = [&](unsigned to) {
+    if (lu < units) {
+      if (left == 0 || lc == C) {
+        if (left == 0) ltile = tile0, lc = c0, left = n;
+        else ++ltile, lc = 0;
+        int row0[MT], up0[MT];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) row0[i] = lu * kCols + i * 16, up0[i] = row0[i] + 8;
+        core.aim(w4_matrix(P.wd, P.sd, L.slot_of_tile[ltile]), P.sd, row0, up0, P.d, lc, lane);
       }
+      core.copy(P.sd, to, lane);
+      ++lc;
+      if (--left == 0) lu += gridDim.x;
     }
     cp_commit();
   };
+  int xu = n ? blockIdx.x : units, xleft = 0, xc = 0, xtile = 0, xR = 0;
+  const auto read_h = [&]() {
+    if (xu >= units) return;
+    if (xleft == 0 || xc == C) {
+      if (xleft == 0) xtile = tile0, xc = c0, xleft = n;
+      else ++xtile, xc = 0;
+      int p0;
+      find_tile(L, xtile, kPairs, p0, xR);
 #pragma unroll
-  for (int i = 0; i < kDownStages - 1; ++i) issue(i);
-  int slot = 0;
-  for (int u = blockIdx.x; u < units; u += gridDim.x) {
-    for (int i = lane; i < P.T * 20; i += 32) mine[0][i] = 0.f;
-    float acc[1][NT][4] = {};
-    int tile = q0 / C, c = q0 - tile * C, pair0 = 0, R = 0;
-    if (q0 < q1) find_tile(L, P, tile, kPairs, pair0, R);
-    for (int q = q0; q < q1; ++q) {
-      cp_wait<kDownStages - 2>();
+      for (int r = 0; r < XR; ++r) core.xoff[r] = r < 2 * xR ? (unsigned)(2 * p0 + r) * (unsigned)(P.f / 8) : 0u;
+    }
+    core.read_x(P.h, xc, P.f, 2 * xR, ~0u, lane);
+    ++xc;
+    if (--xleft == 0) xu += gridDim.x;
+  };
+  // the first weights do not wait for h
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) issue(i * Core::kStage);
+  griddep_wait();
+  griddep_launch();
+  read_h();
+  for (int u = blockIdx.x, i = 0; u < units; u += gridDim.x, ++i) {
+    float(*mine)[kPitch] = sums + ((i % kBufs) * warps + warp) * P.T;
+    hand.wait_empty(i, P.status);
+    for (int j = lane; j < P.T * kPitch; j += 32) mine[0][j] = 0.f;
+    float acc[MT][4] = {};
+    int tile = tile0, c = c0, pair0 = 0, R = 0;
+    if (n) find_tile(L, tile, kPairs, pair0, R);
+    for (int q = 1; q <= n; ++q) {
+      cp_wait<kStages - 2>();
       __syncwarp();
-      issue(slot == 0 ? kDownStages - 1 : slot - 1);
-      Core::multiply(sm.stage[warp][slot], acc, (R + 3) / 4, lane);
-      slot = slot + 1 == kDownStages ? 0 : slot + 1;
-      if (++c == C || q + 1 == q1) {
-        __syncwarp();
+      issue(core.free_slot());
+      core.store_x(2 * R);
+      read_h();
+      __syncwarp();
+      core.multiply(acc, P.f - c * kChunk, lane);
+      core.next();
+      if (++c == C || q == n) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const int r = n * 4 + t;
-          if (r < R) {
-            float* dst = mine[L.token[pair0 + r]];
-            dst[quad] += acc[0][n][0] + acc[0][n][1];
-            dst[quad + 8] += acc[0][n][2] + acc[0][n][3];
+        for (int mt = 0; mt < MT; ++mt) {
+          if (t < R) {
+            float* dst = mine[L.token[pair0 + t]] + mt * 16 + quad;
+            dst[0] += acc[mt][0] + acc[mt][1];
+            dst[8] += acc[mt][2] + acc[mt][3];
           }
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[0][n][j] = 0.f;
+          for (int k = 0; k < 4; ++k) acc[mt][k] = 0.f;
         }
-        if (q + 1 < q1) {
+        __syncwarp();
+        if (q < n) {
           c = 0;
-          find_tile(L, P, ++tile, kPairs, pair0, R);
+          find_tile(L, ++tile, kPairs, pair0, R);
         }
       }
     }
-    __syncthreads();
-    for (int i = tid; i < P.T * 16; i += kThreads) {
-      const int r = i >> 4, j = i & 15, col = u * 16 + j;
-      float v = 0.f;
-#pragma unroll
-      for (int w = 0; w < kW4Warps; ++w) v += sum[w * P.T + r][j];
-      if (col < P.d) {
-        const long long at = (long long)r * P.d + col;
-        if (P.out_fp32) reinterpret_cast<float*>(P.y)[at] = v;
-        else reinterpret_cast<bf16*>(P.y)[at] = __float2bfloat16_rn(v);
-      }
-    }
-    __syncthreads();
+    hand.put(i, lane);
   }
 }
 
-template <int NT, int GROUP, bool ZERO>
-cudaError_t launch_layer(const moe_ops_s* o, const W4LayerParams& P, cudaStream_t s) {
-  auto* up = w4_up_kernel<NT, GROUP, ZERO>;
-  auto* down = w4_down_kernel<NT, GROUP, ZERO>;
-  const size_t su = sizeof(W4UpSmem<NT, GROUP, ZERO>);
-  const size_t sd = sizeof(W4DownSmem<NT, GROUP, ZERO>) + sizeof(float) * kW4Warps * P.T * 20;
-  MOE_TRY(cudaFuncSetAttribute(up, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)su));
-  MOE_TRY(cudaFuncSetAttribute(down, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sd));
-  const int pairs = P.T * (P.k + P.slots - P.E);
-  const long long units = (long long)pairs * (P.f / 16);
-  MOE_TRY(launch_pdl(up, dim3((unsigned)min(units, (long long)o->sms * 2)), dim3(kThreads), su, s, P));
-  return launch_pdl(down, dim3(min(ceil_div(P.d, 16), o->sms * 2)), dim3(kThreads), sd, s, P);
+template <int MT, int XR, int TMAX, int GROUP, bool ZERO>
+cudaError_t launch_up(const moe_ops_s* o, const W4LayerParams& P, cudaStream_t s) {
+  using Core = W4Core<MT, XR, GROUP, ZERO>;
+  auto* kern = w4_up_kernel<MT, XR, TMAX, GROUP, ZERO>;
+  constexpr size_t per = Core::kBytes + kSumBuffers * XR * Core::kPitch * sizeof(float);
+  const long long units = (long long)P.T * (P.k + P.slots - P.E) * (P.f / (MT * 8));
+  const int ctas = units <= o->sms ? 1 : 2;
+  const int warps = w4_warps(ctas, kW4Warps / ctas - 1, sizeof(LayerLists<TMAX>) + sizeof(LayerGates<TMAX>) + 128, per);
+  const size_t smem = warps * per;
+  MOE_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+  return launch_pdl(kern, dim3((unsigned)min(units, (long long)o->sms * ctas)), dim3((warps + 1) * 32), smem, s, P);
 }
-template <int NT> cudaError_t pick_layer(const moe_ops_s* o, const W4LayerParams& P, int group, cudaStream_t s) {
-  const bool z = P.w13.zero != nullptr;
-  if (group == 32) return z ? launch_layer<NT, 32, true>(o, P, s) : launch_layer<NT, 32, false>(o, P, s);
-  if (group == 64) return z ? launch_layer<NT, 64, true>(o, P, s) : launch_layer<NT, 64, false>(o, P, s);
-  return z ? launch_layer<NT, 128, true>(o, P, s) : launch_layer<NT, 128, false>(o, P, s);
+template <int MT, int XR, int TMAX, int GROUP, bool ZERO>
+cudaError_t launch_down(const moe_ops_s* o, const W4LayerParams& P, cudaStream_t s) {
+  using Core = W4Core<MT, XR, GROUP, ZERO>;
+  auto* kern = w4_down_kernel<MT, XR, TMAX, GROUP, ZERO>;
+  const size_t per = Core::kBytes + down_buffers(TMAX) * P.T * Core::kPitch * sizeof(float);
+  const int units = ceil_div(P.d, MT * 16);
+  const int ctas = TMAX > 16 ? 2 : units <= o->sms ? 1 : units <= 2 * o->sms ? 2 : XR == 2 ? 4 : 3;
+  const int warps = w4_warps(ctas, (ctas > 2 ? 5 : kW4Warps / ctas) - (ctas < 3), sizeof(LayerLists<TMAX>) + 128, per);
+  const size_t smem = warps * per;
+  MOE_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+  return launch_pdl(kern, dim3(min(units, o->sms * ctas)), dim3((warps + 1) * 32), smem, s, P);
+}
+template <int GROUP, bool ZERO> cudaError_t pick_layer(const moe_ops_s* o, const W4LayerParams& P, cudaStream_t s) {
+  if (P.T > 16) {
+    MOE_TRY((launch_up<2, 8, 64, GROUP, ZERO>(o, P, s)));
+    return launch_down<2, 8, 64, GROUP, ZERO>(o, P, s);
+  }
+  if (P.T <= 2) MOE_TRY((launch_up<2, 2, 16, GROUP, ZERO>(o, P, s)));
+  else MOE_TRY((launch_up<2, 8, 16, GROUP, ZERO>(o, P, s)));
+  return P.T <= 1 ? launch_down<1, 2, 16, GROUP, ZERO>(o, P, s) : launch_down<1, 8, 16, GROUP, ZERO>(o, P, s);
 }
 
 }  // namespace
@@ -333,11 +378,14 @@ cudaError_t w4_experts(const moe_ops_s* o, const moe_w4_config& c, const void* x
                        const float* gate, const moe_w4& w13, const moe_w4& wd, void* y, int out_fp32, void* ws,
                        cudaStream_t s, long long* n) {
   const auto weights = [](const moe_w4& w) { return W4{w.codes, (const bf16*)w.scale, w.zero}; };
-  const W4LayerParams P = {(const uint8_t*)x, (unsigned)(ld / 8), T, c.k, c.E, c.E + c.n_shared, c.d, c.f, idx, gate,
+  const W4LayerParams P = {(const bf16*)x, (unsigned)(ld / 8), T, c.k, c.E, c.E + c.n_shared, c.d, c.f, idx, gate,
                            weights(w13), weights(wd), {2 * c.f, c.d, ceil_div(c.d, w13.group)},
-                           {c.d, c.f, ceil_div(c.f, w13.group)}, (uint8_t*)ws, y, out_fp32, o->status};
+                           {c.d, c.f, ceil_div(c.f, w13.group)}, (bf16*)ws, y, out_fp32, o->status};
   *n += 2;
-  return T > 8 ? pick_layer<2>(o, P, w13.group, s) : pick_layer<1>(o, P, w13.group, s);
+  const bool z = w13.zero != nullptr;
+  if (w13.group == 32) return z ? pick_layer<32, true>(o, P, s) : pick_layer<32, false>(o, P, s);
+  if (w13.group == 64) return z ? pick_layer<64, true>(o, P, s) : pick_layer<64, false>(o, P, s);
+  return z ? pick_layer<128, true>(o, P, s) : pick_layer<128, false>(o, P, s);
 }
 
 }  // namespace moe

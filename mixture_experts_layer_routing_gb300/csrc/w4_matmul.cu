@@ -7,108 +7,133 @@ namespace moe {
 namespace {
 
 struct W4MatmulParams {
-  const uint8_t* x;
-  unsigned ld16;          // row of x in 16-byte units
+  const bf16* x;
+  unsigned ld16;          // row of x in units of 16 bytes
   int x_rows, M;
   const int* row_index;
   W4 w;
   W4Shape s;
   const int* off;
   int G, out_fp32;
+  int warps;              // that multiply (the CTA has one more, and 8 at least)
   void* c;
   int* status;
 };
 
-constexpr int kMmStages = 3;
-
-template <int NT, int GROUP, bool ZERO> struct W4MatmulSmem {
-  W4Stage<1, NT, GROUP, ZERO> stage[kW4Warps][kMmStages];
-  float part[2][kW4Warps][NT * 8][20];      // [row of x][16 rows of w]
-};
-
-// A CTA takes units of 16 weight rows x up to 8 NT rows of one segment; its warps split K and add up in a fixed order.
-template <int NT, int GROUP, bool ZERO>
+// A CTA takes units of MT x 16 weight rows x up to XR rows of one segment. Their chunks are dealt to its warps in turn; the
+// last warp adds up the others' sums, in a fixed order.
+template <int MT, int XR, int GROUP, bool ZERO>
 __global__ void __launch_bounds__(kW4Warps * 32, 1) w4_matmul_kernel(W4MatmulParams P) {
-  using Core = W4Core<1, NT, GROUP, ZERO>;
-  constexpr int kRows = Core::kRows;
-  extern __shared__ __align__(128) uint8_t smem_raw[];
-  auto& sm = *reinterpret_cast<W4MatmulSmem<NT, GROUP, ZERO>*>(smem_raw);
+  using Core = W4Core<MT, XR, GROUP, ZERO>;
+  constexpr int kCols = MT * 16, kPitch = Core::kPitch, kSums = XR * kPitch;
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ SegSmem seg;
+  __shared__ W4Handover<kSumBuffers> hand;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = P.warps;
+  if (tid == 0) hand.init(warps);
   griddep_wait();
   griddep_launch();
-  load_segments(seg, P.off, P.G, P.M, kRows, P.status);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int mtiles = (P.s.N + 15) / 16, units = seg.tile[P.G] * mtiles;
-  const int C = (P.s.K + kChunk - 1) / kChunk, c0 = C * warp / kW4Warps, c1 = C * (warp + 1) / kW4Warps;
-  Core core;
-  core.px = P.x;
-  int lu = blockIdx.x, lc = c0, tile_at = -1;
-  const auto issue = [&](int slot) {
-    if (lu < units && c0 < c1) {
-      if (lc == c0) {
-        const int tile = lu / mtiles, m = lu - tile * mtiles, g = segment_of(seg, P.G, tile);
-        const int row0[1] = {m * 16}, end[1] = {P.s.N};
-        core.set_weights(w4_matrix(P.w, P.s, g), P.s, row0, end, lane);
-        if (tile != tile_at) {
-          tile_at = tile;
-          const int r0 = seg.off[g] + (tile - seg.tile[g]) * kRows, R = min(kRows, seg.off[g + 1] - r0);
-          core.xn = (R + 1) / 2;
-#pragma unroll
-          for (int i = 0; i < NT * 4; ++i) {
-            const int r = (lane >> 4) + 2 * i;
-            core.xoff[i] = ~0u;
-            if (r < R) {
-              const int s = P.row_index ? P.row_index[r0 + r] : r0 + r;
-              if ((unsigned)s < (unsigned)P.x_rows) core.xoff[i] = (unsigned)s * P.ld16;
-              else set_error(P.status, MOE_ERR_DEVICE_INDEX);
-            }
-          }
+  load_segments(seg, P.off, P.G, P.M, XR, P.status);
+  float* sums = reinterpret_cast<float*>(smem + warps * Core::kBytes);     // [kSumBuffers][warp][XR][kPitch]
+  const int blocks = (P.s.N + kCols - 1) / kCols, tiles = seg.tile[P.G], C = (P.s.K + kChunk - 1) / kChunk;
+  const int units = tiles * blocks, u0 = (int)((long long)units * blockIdx.x / gridDim.x);      // this CTA's, in a row
+  const int u1 = (int)((long long)units * (blockIdx.x + 1) / gridDim.x);
+  int tile = u0 / blocks, m = u0 - tile * blocks, at = -1, r0 = 0, R = 0;
+  const auto rows = [&](int tl) {
+    at = tl;
+    const int g = segment_of(seg, P.G, tl);
+    r0 = seg.off[g] + (tl - seg.tile[g]) * XR;
+    R = min(XR, seg.off[g + 1] - r0);
+  };
+  if (warp > warps) return;
+  if (warp == warps) {
+    for (int u = u0; u < u1; ++u) {
+      if (tile != at) rows(tile);
+      hand.wait_full(u - u0, P.status);
+      const float* from = sums + (u - u0) % kSumBuffers * warps * kSums;
+      for (int i = lane; i < R * (kCols / 4); i += 32) {
+        const int r = i / (kCols / 4), j = i % (kCols / 4) * 4, col = m * kCols + j;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int w = 0; w < warps; ++w) {
+          const float4 q = *reinterpret_cast<const float4*>(from + w * kSums + r * kPitch + j);
+          v.x += q.x, v.y += q.y, v.z += q.z, v.w += q.w;
+        }
+        if (col < P.s.N) {      // (N is a multiple of 8)
+          const long long to = (long long)(r0 + r) * P.s.N + col;
+          if (P.out_fp32) *reinterpret_cast<float4*>(reinterpret_cast<float*>(P.c) + to) = v;
+          else *reinterpret_cast<uint2*>(reinterpret_cast<bf16*>(P.c) + to) = make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
         }
       }
-      core.copy_weights(sm.stage[warp][slot], P.s, lc, lane);
-      core.copy_x(sm.stage[warp][slot], P.s, lc, lane);
-      if (++lc == c1) {
-        lc = c0;
-        lu += gridDim.x;
+      hand.taken(u - u0, lane);
+      if (++m == blocks) m = 0, ++tile;
+    }
+    return;
+  }
+  Core core;
+  core.init(smem + warp * Core::kBytes, warps, lane);
+  W4Cursor w(u0, tile, m, warp, C, blocks), x = w;      // the next chunks of the weights and of x to read
+  int aimed = -1, xt = -1, xR = 0;
+  unsigned there = 0;
+  bool fresh = true;                                    // the first chunk of its unit
+  const auto issue = [&](unsigned to) {
+    if (w.u < u1) {
+      if (w.tile != aimed || (fresh && w.m + 1 == blocks)) {       // (the last block's rows may end within it)
+        aimed = w.tile;
+        int row0[MT], up0[MT];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) row0[i] = w.m * kCols + i * 16, up0[i] = row0[i] + 8;
+        core.aim(w4_matrix(P.w, P.s, segment_of(seg, P.G, w.tile)), P.s, row0, up0, P.s.N, w.c, lane);
       }
+      core.copy(P.s, to, lane);
+      const int n = w.next(warps, C, blocks);
+      fresh = n > 0;
+      for (int i = 0; i < n; ++i) core.step(P.s, kCols, C);
     }
     cp_commit();
   };
+  const auto read_x = [&]() {
+    if (x.u >= u1) return;
+    if (x.tile != xt) {
+      xt = x.tile;
+      const int g = segment_of(seg, P.G, xt), first = seg.off[g] + (xt - seg.tile[g]) * XR;
+      xR = min(XR, seg.off[g + 1] - first);
+      there = 0;
 #pragma unroll
-  for (int i = 0; i < kMmStages - 1; ++i) issue(i);
-  int slot = 0, buf = 0;
-  for (int u = blockIdx.x; u < units; u += gridDim.x, buf ^= 1) {
-    const int tile = u / mtiles, m = u - tile * mtiles, g = segment_of(seg, P.G, tile);
-    const int r0 = seg.off[g] + (tile - seg.tile[g]) * kRows, R = min(kRows, seg.off[g + 1] - r0);
-    float acc[1][NT][4] = {};
-    for (int c = c0; c < c1; ++c) {
-      cp_wait<kMmStages - 2>();
-      __syncwarp();
-      issue(slot == 0 ? kMmStages - 1 : slot - 1);
-      Core::multiply(sm.stage[warp][slot], acc, (R + 7) / 8, lane);
-      slot = slot + 1 == kMmStages ? 0 : slot + 1;
-    }
-    const int quad = lane >> 2, t = lane & 3;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      float(*p)[20] = &sm.part[buf][warp][n * 8 + 2 * t];
-      p[0][quad] = acc[0][n][0];
-      p[1][quad] = acc[0][n][1];
-      p[0][quad + 8] = acc[0][n][2];
-      p[1][quad + 8] = acc[0][n][3];
-    }
-    __syncthreads();      // (the buffer before the last one has been read by all when they are here)
-    for (int i = tid; i < R * 16; i += kW4Warps * 32) {
-      const int r = i >> 4, j = i & 15, col = m * 16 + j;
-      float v = 0.f;
-#pragma unroll
-      for (int w = 0; w < kW4Warps; ++w) v += sm.part[buf][w][r][j];
-      if (col < P.s.N) {
-        const long long at = (long long)(r0 + r) * P.s.N + col;
-        if (P.out_fp32) reinterpret_cast<float*>(P.c)[at] = v;
-        else reinterpret_cast<bf16*>(P.c)[at] = __float2bfloat16_rn(v);
+      for (int r = 0; r < XR; ++r) {
+        core.xoff[r] = 0;
+        if (r < xR) {
+          const int s = P.row_index ? P.row_index[first + r] : first + r;
+          if ((unsigned)s < (unsigned)P.x_rows) core.xoff[r] = (unsigned)s * P.ld16, there |= 1u << r;
+          else set_error(P.status, MOE_ERR_DEVICE_INDEX);
+        }
       }
     }
+    core.read_x(P.x, x.c, P.s.K, xR, there, lane);
+    x.next(warps, C, blocks);
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) issue(i * Core::kStage);
+  read_x();
+  int c = warp;
+  for (int u = u0; u < u1; ++u) {
+    if (tile != at) rows(tile);
+    float acc[MT][4] = {};
+    for (; c < C; c += warps) {
+      cp_wait<kStages - 2>();
+      __syncwarp();
+      issue(core.free_slot());
+      core.store_x(R);
+      read_x();
+      __syncwarp();
+      core.multiply(acc, P.s.K - c * kChunk, lane);
+      core.next();
+    }
+    c -= C;
+    hand.wait_empty(u - u0, P.status);
+    core.put(acc, sums + ((u - u0) % kSumBuffers * warps + warp) * kSums, R, lane);
+    hand.put(u - u0, lane);
+    if (++m == blocks) m = 0, ++tile;
   }
 }
 
@@ -160,20 +185,23 @@ __global__ void __launch_bounds__(256) quant_w4_kernel(const bf16* __restrict__ 
   }
 }
 
-template <int NT, int GROUP, bool ZERO>
-cudaError_t launch_matmul(const moe_ops_s* o, const W4MatmulParams& P, cudaStream_t s) {
-  auto* kern = w4_matmul_kernel<NT, GROUP, ZERO>;
-  const size_t smem = sizeof(W4MatmulSmem<NT, GROUP, ZERO>);
+template <int MT, int XR, int GROUP, bool ZERO>
+cudaError_t launch_matmul(const moe_ops_s* o, W4MatmulParams P, cudaStream_t s) {
+  using Core = W4Core<MT, XR, GROUP, ZERO>;
+  auto* kern = w4_matmul_kernel<MT, XR, GROUP, ZERO>;
+  constexpr size_t per = Core::kBytes + kSumBuffers * XR * Core::kPitch * sizeof(float);
+  const long long units = (long long)(ceil_div(P.M, XR) + (P.off ? min(P.G, P.M) : 0)) * ceil_div(P.s.N, MT * 16);
+  const int ctas = units <= o->sms ? 1 : 2;
+  P.warps = w4_warps(ctas, kW4Warps / ctas - 1, sizeof(SegSmem) + 128, per);
+  const size_t smem = P.warps * per;
   MOE_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-  const long long units = (long long)(ceil_div(P.M, NT * 8) + (P.off ? min(P.G, P.M) : 0)) * ceil_div(P.s.N, 16);
-  const long long grid = min(units, (long long)o->sms * 2);
-  return launch_pdl(kern, dim3((unsigned)grid), dim3(kW4Warps * 32), smem, s, P);
+  return launch_pdl(kern, dim3((unsigned)min(units, (long long)o->sms * ctas)), dim3(max(P.warps + 1, 8) * 32), smem, s, P);
 }
-template <int NT> cudaError_t pick_matmul(const moe_ops_s* o, const W4MatmulParams& P, int group, cudaStream_t s) {
+template <int MT, int XR> cudaError_t pick_matmul(const moe_ops_s* o, const W4MatmulParams& P, int group, cudaStream_t s) {
   const bool z = P.w.zero != nullptr;
-  if (group == 32) return z ? launch_matmul<NT, 32, true>(o, P, s) : launch_matmul<NT, 32, false>(o, P, s);
-  if (group == 64) return z ? launch_matmul<NT, 64, true>(o, P, s) : launch_matmul<NT, 64, false>(o, P, s);
-  return z ? launch_matmul<NT, 128, true>(o, P, s) : launch_matmul<NT, 128, false>(o, P, s);
+  if (group == 32) return z ? launch_matmul<MT, XR, 32, true>(o, P, s) : launch_matmul<MT, XR, 32, false>(o, P, s);
+  if (group == 64) return z ? launch_matmul<MT, XR, 64, true>(o, P, s) : launch_matmul<MT, XR, 64, false>(o, P, s);
+  return z ? launch_matmul<MT, XR, 128, true>(o, P, s) : launch_matmul<MT, XR, 128, false>(o, P, s);
 }
 
 }  // namespace
@@ -181,11 +209,11 @@ template <int NT> cudaError_t pick_matmul(const moe_ops_s* o, const W4MatmulPara
 cudaError_t w4_matmul(const moe_ops_s* o, const void* x, long long ld, int x_rows, const int* row_index, int M,
                       const moe_w4& w, const int* off, int G, int N, int K, void* c, int out_fp32, cudaStream_t s,
                       long long* n) {
-  const W4MatmulParams P = {(const uint8_t*)x, (unsigned)(ld / 8), x_rows, M, row_index,
-                            {w.codes, (const bf16*)w.scale, w.zero}, {N, K, ceil_div(K, w.group)}, off, G, out_fp32, c,
-                            o->status};
+  const W4MatmulParams P = {(const bf16*)x, (unsigned)(ld / 8), x_rows, M, row_index,
+                            {w.codes, (const bf16*)w.scale, w.zero}, {N, K, ceil_div(K, w.group)}, off, G, out_fp32, 0, c, o->status};
   *n += 1;
-  return M > 8 ? pick_matmul<2>(o, P, w.group, s) : pick_matmul<1>(o, P, w.group, s);
+  if (M <= 2) return pick_matmul<2, 2>(o, P, w.group, s);
+  return M <= 4 ? pick_matmul<2, 4>(o, P, w.group, s) : pick_matmul<2, 8>(o, P, w.group, s);
 }
 
 cudaError_t quant_w4(const moe_ops_s*, const void* w, int G, int N, int K, int group, uint32_t* codes, void* scale,

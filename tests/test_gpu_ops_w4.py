@@ -129,6 +129,19 @@ def test_w4_matmul_of_segments(ops, group, zero, cnt, gather):
     assert ops.status() == 0
 
 
+def test_as_many_segments_as_there_may_be(ops):
+    G, N, K = 256, 40, 96
+    cnt = [(7 * i) % 4 for i in range(G)]
+    M = sum(cnt)
+    w, v = weights(G, N, K, 32, False, seed=9)
+    x = rnd(M, K, seed=10)
+    off = torch.tensor(np.concatenate([[0], np.cumsum(cnt)]), dtype=torch.int32).cuda()
+    c = ops.w4_matmul(x.cuda(), w, off=off, out_dtype=torch.float32)
+    want, size = oo.matmul(f64(x), np.stack(v), np.concatenate([[0], np.cumsum(cnt)]))
+    near(c, want, size, 3)
+    assert ops.status() == 0
+
+
 def test_rows_of_no_segment_stay_as_they_were(ops):
     import mixture_experts_layer_routing_gb300 as moe
     w, v = weights(2, 40, 64, 32, False, seed=1)
