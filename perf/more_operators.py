@@ -367,7 +367,8 @@ def _library(s):
     if c["dir"] == "fwd":
         return ops.swiglu(s["gu"], out=out)
     if c["dir"] == "cols":
-        return ops.requant_cols(s["q"], s["scale"], off=s["off"], row_index=s["row"], out=out)
+        q, scale = ops.requant_cols(s["q"], s["scale"], off=s["off"], row_index=s["row"], out=out)
+        return dict(q=q, scale=scale)
     return ops.swiglu_backward(s["dact"], s["save"], s["save_scale"], gate=s["gate"], off=s["off"], out=out)
 
 
