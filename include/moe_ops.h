@@ -5,6 +5,7 @@
  *   moe_gate_*    routing from router logits: bias, groups, top-k, dispatch
  *   moe_quant_*   e4m3 codes with one fp32 scale for each 128 values
  *   moe_fp8_*     products of such operands, dense and by experts' rows
+ *   moe_swiglu_*, moe_requant_cols   SwiGLU with an 8-bit checkpoint, and its gradient from it
  *   moe_quant_w4, moe_w4_*   4-bit weights with a scale for a group of values: products of
  *                 few rows, and the experts' layer of a few tokens
  *
@@ -144,6 +145,33 @@ moe_status moe_fp8_matmul_workspace_size(int M, int G, int K, int gathered, size
  * without tokens. T and off as they were given to moe_quant_cols; N and K multiples of 8, scales 16-byte aligned. */
 moe_status moe_fp8_wgrad(moe_ops ops, const void* dct, const float* dct_scale, const void* xt, const float* xt_scale,
                          int T, const int32_t* off, int G, int N, int K, void* c, int out_dtype, void* stream);
+
+/* ---- SwiGLU with an 8-bit checkpoint: gu = (g, u) halves of a row, act = silu(g) * u.
+ * gu [T, 2f] bf16, rows ld elements apart; f and ld multiples of 8, 16-byte aligned. Outputs (one at least): act [T, f]
+ * bf16; q [T, f] with scale [T, ceil(f/128)], act's codes (of the unrounded values, as moe_quant_rows with swiglu); save
+ * [T, 2f] with save_scale [T, 2 ceil(f/128)], the codes of g and of u, blocks of 128 within each half, the gate's scales
+ * first (what the backward pass reads; with f a multiple of 128 they are moe_quant_rows of gu). Codes 8-byte aligned. */
+moe_status moe_swiglu_forward(moe_ops ops, const void* gu, long long ld, int T, int f, void* act, void* q, float* scale,
+                              void* save, float* save_scale, void* stream);
+/* With g, u the values of save, s = sigmoid(g), dact [T, f] bf16 the gradient of act (rows ld elements apart, a multiple
+ * of 8, 16-byte aligned) and gate [T] fp32 a factor of each row (NULL: 1):
+ *   dg = gate dact u s (1 + g (1 - s))     du = gate dact g s     dgate[t] = sum_f act dact     act' = gate act
+ * gate: where a row's product is weighted after the down product, out = sum gate (act Wd^T), dact is (dout Wd) without
+ * the gate, dgate needs no output of that product, and dWd is act' along the tokens times dout.
+ * Outputs, one at least, each pair both or neither, values quantised unrounded: dgu = (dg, du) [T, 2f] bf16; dq [T, 2f]
+ * with dq_scale [T, 2f/128], its rows' codes (f a multiple of 128); dqt [2f, Tp] with dqt_scale [Tp/128, 2f], its codes
+ * along the tokens, and with them actt [f, Tp], actt_scale [Tp/128, f], those of act', segments and padding as in
+ * moe_quant_cols; dgate [T]. off (nullable, G+1 ascending within 0 .. T) tells the segments; rows of no segment are not
+ * written. workspace: moe_swiglu_workspace_size bytes, 16-byte aligned, for dgate (else NULL). */
+moe_status moe_swiglu_workspace_size(int T, int f, size_t* bytes);
+moe_status moe_swiglu_backward(moe_ops ops, const void* save, const float* save_scale, const void* dact, long long ld,
+                               const float* gate, int T, int f, const int32_t* off, int G, void* dgu, void* dq,
+                               float* dq_scale, void* dqt, float* dqt_scale, void* actt, float* actt_scale,
+                               float* dgate, void* workspace, void* stream);
+/* moe_quant_cols of rows that are held in 8 bits (q [src_rows, C], scale [src_rows, ceil(C/128)], as moe_quant_rows and
+ * moe_norm_forward give them): the values code * scale, quantised along the tokens. C is a multiple of 8. */
+moe_status moe_requant_cols(moe_ops ops, const void* q, const float* scale, int src_rows, int T, int C,
+                            const int32_t* off, int G, const int32_t* row_index, void* qt, float* scale_t, void* stream);
 
 /* ---- 4-bit weights. A group of `group` (32, 64 or 128; the last one of a row may be shorter) consecutive values along
  * K shares a scale and, where zero is given, a zero point:

@@ -56,6 +56,15 @@ cudaError_t fp8_matmul(const moe_ops_s* o, const void* a, const float* sa, int a
 cudaError_t fp8_wgrad(const moe_ops_s* o, const void* dct, const float* sdct, const void* xt, const float* sxt, int T,
                       const int* off, int G, int N, int K, void* c, int out_fp32, cudaStream_t s, long long* n);
 
+cudaError_t swiglu_forward(const moe_ops_s* o, const void* gu, long long ld, int T, int f, void* act, void* q,
+                           float* scale, void* save, float* save_scale, cudaStream_t s, long long* n);
+cudaError_t swiglu_backward(const moe_ops_s* o, const void* save, const float* save_scale, const void* dact, long long ld,
+                            const float* gate, int T, int f, const int* off, int G, void* dgu, void* dq, float* dq_scale,
+                            void* dqt, float* dqt_scale, void* actt, float* actt_scale, float* dgate, float* ws,
+                            cudaStream_t s, long long* n);
+cudaError_t requant_cols(const moe_ops_s* o, const void* q, const float* scale, int src_rows, int T, int C, const int* off,
+                         int G, const int* row_index, void* qt, float* scale_t, cudaStream_t s, long long* n);
+
 cudaError_t quant_w4(const moe_ops_s* o, const void* w, int G, int N, int K, int group, uint32_t* codes, void* scale,
                      uint8_t* zero, cudaStream_t s, long long* n);
 cudaError_t w4_matmul(const moe_ops_s* o, const void* x, long long ld, int x_rows, const int* row_index, int M,

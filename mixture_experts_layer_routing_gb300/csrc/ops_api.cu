@@ -311,6 +311,58 @@ moe_status moe_fp8_wgrad(moe_ops ops, const void* dct, const float* dct_scale, c
                  &n_));
 }
 
+moe_status moe_swiglu_forward(moe_ops ops, const void* gu, long long ld, int T, int f, void* act, void* q, float* scale,
+                              void* save, float* save_scale, void* stream) {
+  CHECK(ops && T >= 0 && f >= 1 && ld >= 2ll * f, MOE_ERR_INVALID_ARG);
+  CHECK(f % 8 == 0 && ld % 8 == 0, MOE_ERR_UNSUPPORTED);
+  if (T == 0) return MOE_OK;
+  CHECK(gu && (act || q || save) && (q != nullptr) == (scale != nullptr) && (save != nullptr) == (save_scale != nullptr),
+        MOE_ERR_INVALID_ARG);
+  CHECK(aligned(gu, 16) && aligned(act, 16) && aligned(q, 8) && aligned(save, 8), MOE_ERR_UNSUPPORTED);
+  CHECK((long long)T * ceil_div(f, kScaleBlock) < (1ll << 31), MOE_ERR_UNSUPPORTED);
+  HANDLE(ops);
+  DONE(swiglu_forward(ops, gu, ld, T, f, act, q, scale, save, save_scale, (cudaStream_t)stream, &n_));
+}
+
+moe_status moe_swiglu_workspace_size(int T, int f, size_t* bytes) {
+  CHECK(T >= 0 && f >= 1 && bytes, MOE_ERR_INVALID_ARG);
+  *bytes = sizeof(float) * (size_t)T * ceil_div(f, kScaleBlock);
+  return MOE_OK;
+}
+
+moe_status moe_swiglu_backward(moe_ops ops, const void* save, const float* save_scale, const void* dact, long long ld,
+                               const float* gate, int T, int f, const int32_t* off, int G, void* dgu, void* dq,
+                               float* dq_scale, void* dqt, float* dqt_scale, void* actt, float* actt_scale,
+                               float* dgate, void* workspace, void* stream) {
+  CHECK(ops && T >= 0 && f >= 1 && ld >= f && G >= 1 && G <= kMaxSegs && (off || G == 1), MOE_ERR_INVALID_ARG);
+  CHECK((dq != nullptr) == (dq_scale != nullptr) && (dqt != nullptr) == (dqt_scale != nullptr) &&
+            (actt != nullptr) == (actt_scale != nullptr) && (dqt != nullptr) == (actt != nullptr),
+        MOE_ERR_INVALID_ARG);
+  CHECK(f % 8 == 0 && ld % 8 == 0 && T <= (1 << 22) && (!dq || f % kScaleBlock == 0), MOE_ERR_UNSUPPORTED);
+  if (T == 0) return MOE_OK;
+  CHECK(save && save_scale && dact && (dgu || dq || dqt || dgate), MOE_ERR_INVALID_ARG);
+  CHECK(aligned(save, 8) && aligned(dact, 16) && aligned(dgu, 16) && aligned(dq, 16) && aligned(dqt, 16) && aligned(actt, 16),
+        MOE_ERR_UNSUPPORTED);
+  CHECK(!dgate || (workspace && aligned(workspace, 16)), MOE_ERR_WORKSPACE);
+  HANDLE(ops);
+  DONE(swiglu_backward(ops, save, save_scale, dact, ld, gate, T, f, off, G, dgu, dq, dq_scale, dqt, dqt_scale, actt,
+                       actt_scale, dgate, (float*)workspace, (cudaStream_t)stream, &n_));
+}
+
+moe_status moe_requant_cols(moe_ops ops, const void* q, const float* scale, int src_rows, int T, int C,
+                            const int32_t* off, int G, const int32_t* row_index, void* qt, float* scale_t,
+                            void* stream) {
+  CHECK(ops && T >= 0 && C >= 1 && src_rows >= 0, MOE_ERR_INVALID_ARG);
+  CHECK(G >= 1 && G <= kMaxSegs && (off || G == 1), MOE_ERR_INVALID_ARG);
+  CHECK(row_index || src_rows >= T, MOE_ERR_INVALID_ARG);
+  CHECK(T <= (1 << 22) && C % 8 == 0, MOE_ERR_UNSUPPORTED);
+  if (T == 0) return MOE_OK;
+  CHECK(q && scale && qt && scale_t, MOE_ERR_INVALID_ARG);
+  CHECK(aligned(q, 8) && aligned(qt, 16) && aligned(scale_t, 16), MOE_ERR_UNSUPPORTED);
+  HANDLE(ops);
+  DONE(requant_cols(ops, q, scale, src_rows, T, C, off, G, row_index, qt, scale_t, (cudaStream_t)stream, &n_));
+}
+
 moe_status moe_quant_w4(moe_ops ops, const void* w, int G, int N, int K, int group, uint32_t* codes, void* scale,
                         uint8_t* zero, void* stream) {
   CHECK(ops && w && codes && scale && G >= 1 && N >= 1 && K >= 1, MOE_ERR_INVALID_ARG);

@@ -117,7 +117,8 @@ int to_int(int64_t v, const char* what) {
 const void* address(const Args& a, int i, const char* what) { return a.given(i) ? a.tensor(i, what).data_ptr() : nullptr; }
 
 PyObject *k_h, *k_y, *k_q, *k_scale, *k_rstd, *k_dx, *k_dw, *k_idx, *k_gate, *k_cnt, *k_off, *k_perm, *k_inv,
-    *k_dlogits, *k_qt, *k_scale_t, *k_codes, *k_zero, *k_group;
+    *k_dlogits, *k_qt, *k_scale_t, *k_codes, *k_zero, *k_group,
+    *k_act, *k_save, *k_save_scale, *k_dgu, *k_dq, *k_dq_scale, *k_dqt, *k_dqt_scale, *k_actt, *k_actt_scale, *k_dgate;
 
 template <class F>
 PyObject* guarded(F&& f) {
@@ -417,6 +418,102 @@ PyObject* fp8_wgrad(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
+// Outputs that a dict names: all of its entries have to be known.
+struct Outputs {
+  const Args& a;
+  PyObject* out;
+  Py_ssize_t found = 0;
+  void* get(PyObject* key, const char* what, at::ScalarType type, at::IntArrayRef shape) {
+    found += PyDict_Contains(out, key) == 1;
+    return a.output(out, key, what, type, shape);
+  }
+  void done() const {
+    if (found != PyDict_Size(out)) refuse(PyExc_ValueError, "out", "holds unknown outputs");
+  }
+};
+
+// gu, out
+PyObject* swiglu(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&] {
+    Args a(args, n, 5);
+    long long ld;
+    const at::Tensor& gu = bf16_rows(a, 3, "gu", &ld);
+    const int64_t T = gu.size(0), f = gu.size(1) / 2, nb = blocks(f);
+    if (gu.size(1) % 2 || f == 0) refuse(PyExc_ValueError, "gu", "an even number of columns expected");
+    Outputs o{a, a.dict(4)};
+    void* act = o.get(k_act, "act", at::kBFloat16, {T, f});
+    void* q = o.get(k_q, "q", at::kFloat8_e4m3fn, {T, f});
+    void* scale = o.get(k_scale, "scale", at::kFloat, {T, nb});
+    void* save = o.get(k_save, "save", at::kFloat8_e4m3fn, {T, 2 * f});
+    void* ss = o.get(k_save_scale, "save_scale", at::kFloat, {T, 2 * nb});
+    o.done();
+    return moe_swiglu_forward(a.ops, gu.data_ptr(), ld, to_int(T, "gu"), to_int(f, "gu"), act, q, (float*)scale, save,
+                              (float*)ss, a.stream);
+  });
+}
+
+// dact, save, save_scale, gate, off, out
+PyObject* swiglu_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&] {
+    Args a(args, n, 9);
+    long long ld;
+    const at::Tensor& d = bf16_rows(a, 3, "dact", &ld);
+    const int64_t T = d.size(0), f = d.size(1), nb = blocks(f);
+    const void* save = a.dense(4, "save", at::kFloat8_e4m3fn, {T, 2 * f}).data_ptr();
+    const void* ss = a.dense(5, "save_scale", at::kFloat, {T, 2 * nb}).data_ptr();
+    const void* gate = a.given(6) ? a.dense(6, "gate", at::kFloat, {T}).data_ptr() : nullptr;
+    const int G = segments(a, 7);
+    int Tp = 0;
+    moe_status st = moe_quant_cols_rows(to_int(T, "dact"), G, &Tp);
+    if (st != MOE_OK) return st;
+    Outputs o{a, a.dict(8)};
+    const at::ScalarType f8 = at::kFloat8_e4m3fn;
+    void* dgu = o.get(k_dgu, "dgu", at::kBFloat16, {T, 2 * f});
+    void* dq = o.get(k_dq, "dq", f8, {T, 2 * f});
+    void* dqs = o.get(k_dq_scale, "dq_scale", at::kFloat, {T, 2 * nb});
+    void* dqt = o.get(k_dqt, "dqt", f8, {2 * f, Tp});
+    void* dqts = o.get(k_dqt_scale, "dqt_scale", at::kFloat, {Tp / kBlock, 2 * f});
+    void* actt = o.get(k_actt, "actt", f8, {f, Tp});
+    void* actts = o.get(k_actt_scale, "actt_scale", at::kFloat, {Tp / kBlock, f});
+    void* dgate = o.get(k_dgate, "dgate", at::kFloat, {T});
+    o.done();
+    at::Tensor ws;
+    void* scratch = nullptr;
+    if (dgate) {
+      size_t bytes = 0;
+      st = moe_swiglu_workspace_size((int)T, to_int(f, "dact"), &bytes);
+      if (st != MOE_OK) return st;
+      ws = at::empty({(int64_t)bytes}, a.opts.dtype(at::kByte));
+      scratch = ws.data_ptr();
+    }
+    return moe_swiglu_backward(a.ops, save, (const float*)ss, d.data_ptr(), ld, (const float*)gate, (int)T,
+                               to_int(f, "dact"), (const int32_t*)address(a, 7, "off"), G, dgu, dq, (float*)dqs, dqt,
+                               (float*)dqts, actt, (float*)actts, (float*)dgate, scratch, a.stream);
+  });
+}
+
+// q, scale, off, row_index, out
+PyObject* requant_cols(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&] {
+    Args a(args, n, 8);
+    const at::Tensor& q = a.tensor(3, "q");
+    if (q.dim() != 2) refuse(PyExc_ValueError, "q", "two dimensions expected");
+    const int64_t rows = q.size(0), C = q.size(1);
+    a.dense(q, "q", at::kFloat8_e4m3fn, {rows, C});
+    const void* scale = a.dense(4, "scale", at::kFloat, {rows, blocks(C)}).data_ptr();
+    const int G = segments(a, 5), T = to_int(indexed(a, 6, rows), "row_index");
+    int Tp = 0;
+    const moe_status st = moe_quant_cols_rows(T, G, &Tp);
+    if (st != MOE_OK) return st;
+    PyObject* out = a.dict(7);
+    void* qt = a.output(out, k_q, "q", at::kFloat8_e4m3fn, {C, Tp}, true);
+    void* s = a.output(out, k_scale, "scale", at::kFloat, {Tp / kBlock, C}, true);
+    return moe_requant_cols(a.ops, q.data_ptr(), (const float*)scale, to_int(rows, "q"), T, to_int(C, "q"),
+                            (const int32_t*)address(a, 5, "off"), G, (const int32_t*)address(a, 6, "row_index"), qt,
+                            (float*)s, a.stream);
+  });
+}
+
 // Entry `key` of a dict of 4-bit weights (null if missing or None).
 PyObject* entry(PyObject* w, PyObject* key) {
   PyObject* o = PyDict_GetItemWithError(w, key);
@@ -530,7 +627,7 @@ PyObject* w4_experts(PyObject*, PyObject* const* args, Py_ssize_t n) {
 PyMethodDef methods[] = {METHOD(norm_forward), METHOD(norm_backward), METHOD(gate),         METHOD(gate_backward),
                          METHOD(quant_rows),   METHOD(quant_cols),    METHOD(quant_blocks), METHOD(fp8_matmul),
                          METHOD(fp8_wgrad),    METHOD(quant_w4),      METHOD(w4_matmul),    METHOD(w4_experts),
-                         {nullptr, nullptr, 0, nullptr}};
+                         METHOD(swiglu),       METHOD(swiglu_backward), METHOD(requant_cols), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_ops_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
@@ -540,7 +637,9 @@ PyMODINIT_FUNC PyInit__ops_binding() {
       {&k_h, "h"}, {&k_y, "y"}, {&k_q, "q"}, {&k_scale, "scale"}, {&k_rstd, "rstd"}, {&k_dx, "dx"}, {&k_dw, "dw"},
       {&k_idx, "idx"}, {&k_gate, "gate"}, {&k_cnt, "cnt"}, {&k_off, "off"}, {&k_perm, "perm"}, {&k_inv, "inv"},
       {&k_dlogits, "dlogits"}, {&k_qt, "qt"}, {&k_scale_t, "scale_t"}, {&k_codes, "codes"},
-      {&k_zero, "zero"}, {&k_group, "group"}};
+      {&k_zero, "zero"}, {&k_group, "group"}, {&k_act, "act"}, {&k_save, "save"}, {&k_save_scale, "save_scale"},
+      {&k_dgu, "dgu"}, {&k_dq, "dq"}, {&k_dq_scale, "dq_scale"}, {&k_dqt, "dqt"}, {&k_dqt_scale, "dqt_scale"},
+      {&k_actt, "actt"}, {&k_actt_scale, "actt_scale"}, {&k_dgate, "dgate"}};
   for (const auto& k : keys)
     if (!(*k.key = PyUnicode_InternFromString(k.name))) return nullptr;
   return PyModule_Create(&module_def);

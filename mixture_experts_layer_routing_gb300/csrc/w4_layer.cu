@@ -353,7 +353,7 @@ cudaError_t launch_down(const moe_ops_s* o, const W4LayerParams& P, cudaStream_t
   const size_t per = Core::kBytes + down_buffers(TMAX) * P.T * Core::kPitch * sizeof(float);
   const int units = ceil_div(P.d, MT * 16);
   const int ctas = TMAX > 16 ? 2 : units <= o->sms ? 1 : units <= 2 * o->sms ? 2 : XR == 2 ? 4 : 3;
-  const int warps = w4_warps(ctas, (ctas > 2 ? 5 : kW4Warps / ctas) - (ctas < 3), sizeof(LayerLists<TMAX>) + 128, per);
+  const int warps = w4_warps(ctas, ctas > 2 ? 4 : kW4Warps / ctas - 1, sizeof(LayerLists<TMAX>) + 128, per);
   const size_t smem = warps * per;
   MOE_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
   return launch_pdl(kern, dim3(min(units, o->sms * ctas)), dim3((warps + 1) * 32), smem, s, P);

@@ -19,7 +19,8 @@ OPS_EXPORTED = ("moe_ops_create", "moe_ops_destroy", "moe_ops_get_status", "moe_
                 "moe_norm_forward", "moe_norm_workspace_size", "moe_norm_backward", "moe_gate_workspace_size",
                 "moe_gate_forward", "moe_gate_backward", "moe_quant_rows", "moe_quant_cols_rows", "moe_quant_cols",
                 "moe_quant_blocks", "moe_fp8_matmul", "moe_fp8_matmul_workspace_size", "moe_fp8_wgrad", "moe_quant_w4",
-                "moe_w4_matmul", "moe_w4_experts_workspace_size", "moe_w4_experts")
+                "moe_w4_matmul", "moe_w4_experts_workspace_size", "moe_w4_experts", "moe_swiglu_forward",
+                "moe_swiglu_workspace_size", "moe_swiglu_backward", "moe_requant_cols")
 
 BLOCK = 128                     # values that share a scale
 _ROUTERS = {"softmax": MOE_ROUTER_SOFTMAX, "sigmoid": MOE_ROUTER_SIGMOID}
@@ -75,6 +76,10 @@ def _lib():
     lib.moe_w4_matmul.argtypes = [vp, vp, i64, i32, vp, i32, w4, vp, i32, i32, i32, vp, i32, vp]
     lib.moe_w4_experts_workspace_size.argtypes = [w4cfg, i32, P(sz)]
     lib.moe_w4_experts.argtypes = [vp, w4cfg, vp, i64, i32, vp, vp, w4, w4, vp, i32, vp, vp]
+    lib.moe_swiglu_forward.argtypes = [vp, vp, i64, i32, i32] + [vp] * 6
+    lib.moe_swiglu_workspace_size.argtypes = [i32, i32, P(sz)]
+    lib.moe_swiglu_backward.argtypes = [vp] * 4 + [i64, vp, i32, i32, vp, i32] + [vp] * 10
+    lib.moe_requant_cols.argtypes = [vp, vp, vp, i32, i32, i32, vp, i32, vp, vp, vp, vp]
     for name in OPS_EXPORTED:
         getattr(lib, name).restype = i32
     _bound = lib
@@ -276,6 +281,58 @@ class MoeOps:
         if s:
             _check(s, "moe_fp8_wgrad")
         return out
+
+    # ------------------------------------------- SwiGLU, 8-bit checkpoints
+    def swiglu(self, gu, want=("act",), out=None, stream=None) -> dict:
+        """moe_swiglu_forward. gu [T, 2f] bf16 (rows may be strided), gate half then up half.
+
+        Returns a dict of the outputs named in `want` or, with `out`, of those that it holds (None values are
+        allocated): "act" [T, f] bf16, "q" and "scale" its 8-bit rows, "save" and "save_scale" the checkpoint of gu.
+        """
+        if stream is not None:
+            return self._on(stream, self.swiglu, gu, want, out)
+        if out is None:
+            out = dict.fromkeys(want)
+            if "q" in out or "scale" in out:
+                out.update(q=None, scale=None)
+            if "save" in out or "save_scale" in out:
+                out.update(save=None, save_scale=None)
+        s = self._b.swiglu(self.h, self._index, self._stream(), gu, out)
+        if s:
+            _check(s, "moe_swiglu_forward")
+        return out
+
+    def swiglu_backward(self, dact, save, save_scale, gate=None, off=None, want=("dgu",), out=None, stream=None) -> dict:
+        """moe_swiglu_backward. dact [T, f] bf16, save and save_scale as swiglu gives them, gate [T] fp32.
+
+        Returns a dict of the outputs named in `want` or, with `out`, of those that it holds (None values are
+        allocated): "dgu" [T, 2f] bf16; "dq", "dq_scale" its 8-bit rows; "dqt", "dqt_scale", "actt", "actt_scale" it and
+        gate * act in 8 bits along the tokens, segments by off (one of them brings all four); "dgate" [T] fp32.
+        """
+        if stream is not None:
+            return self._on(stream, self.swiglu_backward, dact, save, save_scale, gate, off, want, out)
+        if out is None:
+            out = dict.fromkeys(want)
+            if "dq" in out or "dq_scale" in out:
+                out.update(dq=None, dq_scale=None)
+            if any(n in out for n in ("dqt", "dqt_scale", "actt", "actt_scale")):
+                out.update(dqt=None, dqt_scale=None, actt=None, actt_scale=None)
+        s = self._b.swiglu_backward(self.h, self._index, self._stream(), dact, save, save_scale, gate, off, out)
+        if s:
+            _check(s, "moe_swiglu_backward")
+        return out
+
+    def requant_cols(self, q, scale, off=None, row_index=None, out=None, stream=None):
+        """moe_requant_cols. 8-bit rows q [rows, C], scale -> (q [C, Tp], scale [Tp / 128, C]), as quant_cols of their
+        values."""
+        if stream is not None:
+            return self._on(stream, self.requant_cols, q, scale, off, row_index, out)
+        if out is None:
+            out = {}
+        s = self._b.requant_cols(self.h, self._index, self._stream(), q, scale, off, row_index, out)
+        if s:
+            _check(s, "moe_requant_cols")
+        return out["q"], out["scale"]
 
     # --------------------------------------------------------- 4-bit weights
     def quant_w4(self, w, group=128, zero=False, out=None, stream=None) -> dict:

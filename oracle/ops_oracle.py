@@ -220,3 +220,35 @@ def w4_experts(x, idx, gate, w13, wd, n_shared, add):
                 y[t] += wd[e] @ h
                 bound[t] += np.abs(wd[e]) @ (off + add * np.abs(h))
     return y, bound
+
+
+# ---- SwiGLU, 8-bit checkpoints
+
+def swiglu_save(gu):
+    """Codes [T, 2f] and scales of the two halves of gu, blocks within each half."""
+    f = gu.shape[1] // 2
+    (qg, sg), (qu, su) = quantise(gu[:, :f], 1), quantise(gu[:, f:], 1)
+    return np.concatenate([qg, qu], 1), np.concatenate([sg, su], 1)
+
+
+def swiglu_saved(save, scale):
+    """The values (g, u) of a checkpoint, rounded to fp32 as code * scale."""
+    f, nb = save.shape[1] // 2, scale.shape[1] // 2
+    at = np.arange(f) // BLOCK
+    mul = lambda c, s: (c.astype(np.float32) * s.astype(np.float32)[:, at]).astype(np.float64)  # noqa: E731
+    return mul(save[:, :f], scale[:, :nb]), mul(save[:, f:], scale[:, nb:])
+
+
+def swiglu(g, u):
+    return g / (1 + np.exp(-g)) * u
+
+
+def swiglu_backward(g, u, dact, gate):
+    """(dg, du, gated act, dgate) and what the first three may be off where the sigmoid is off by 2^-18 of itself."""
+    s = 1 / (1 + np.exp(-g))
+    da, act = dact * gate[:, None], g * s * u
+    dg, du = da * u * s * (1 + g * (1 - s)), da * g * s
+    off = 2.0 ** -17
+    return (dg, du, act * gate[:, None], (act * dact).sum(1),
+            off * np.abs(da * u) * s * (1 + 2 * np.abs(g)), off * np.abs(du), off * np.abs(act * gate[:, None]),
+            np.abs(act * dact).sum(1))

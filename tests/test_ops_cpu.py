@@ -298,3 +298,67 @@ def test_w4_words_and_values():
             # the scale's own rounding (2^-9 of up to 15 steps) and the zero point's (half a step) add to half a step
             assert np.all(np.abs(back - w) <= step * (0.5 + 15 * 2.0 ** -8 + (0.5 if zero else 0.0)))
     assert np.array_equal(oo.bf16(w), w.astype(np.float64))
+
+
+# ---------------------------------------------------- SwiGLU, checkpoints
+
+SWF = dict(ops=P, gu=P, ld=256, T=4, f=128, act=P, q=P, scale=P, save=P, save_scale=P, stream=None)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(ops=None), ARG), (dict(T=-1), ARG), (dict(f=0), ARG), (dict(ld=248), ARG), (dict(f=124), UNSUP),
+    (dict(ld=260), UNSUP), (dict(gu=None), ARG), (dict(q=None), ARG), (dict(scale=None), ARG), (dict(save=None), ARG),
+    (dict(save_scale=None), ARG), (dict(act=None, q=None, scale=None, save=None, save_scale=None), ARG),
+    (dict(gu=P + 8), UNSUP), (dict(act=P + 8), UNSUP), (dict(q=P + 4), UNSUP), (dict(save=P + 4), UNSUP),
+    (dict(T=(1 << 31) - 1, f=256, ld=512), UNSUP),
+])
+def test_swiglu_forward_refuses(lib, over, code):
+    assert call(lib, "moe_swiglu_forward", SWF, over) == code
+
+
+SWB = dict(ops=P, save=P, save_scale=P, dact=P, ld=128, gate=None, T=4, f=128, off=None, G=1, dgu=P, dq=P, dq_scale=P,
+           dqt=P, dqt_scale=P, actt=P, actt_scale=P, dgate=P, workspace=P, stream=None)
+NONE = dict(dgu=None, dq=None, dq_scale=None, dqt=None, dqt_scale=None, actt=None, actt_scale=None, dgate=None)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(ops=None), ARG), (dict(T=-1), ARG), (dict(f=0), ARG), (dict(ld=120), ARG), (dict(G=0), ARG), (dict(G=2), ARG),
+    (dict(G=257, off=P), ARG), (dict(dq=None), ARG), (dict(dqt_scale=None), ARG), (dict(actt=None), ARG),
+    (dict(actt=None, actt_scale=None), ARG), (NONE, ARG), (dict(f=124), UNSUP), (dict(ld=132), UNSUP),
+    (dict(f=136, ld=136), UNSUP), (dict(T=(1 << 22) + 1), UNSUP), (dict(save=None), ARG), (dict(save_scale=None), ARG),
+    (dict(dact=None), ARG), (dict(dact=P + 8), UNSUP), (dict(save=P + 4), UNSUP), (dict(dqt=P + 8), UNSUP),
+    (dict(dgu=P + 8), UNSUP), (dict(workspace=None), WS), (dict(workspace=P + 8), WS),
+])
+def test_swiglu_backward_refuses(lib, over, code):
+    assert call(lib, "moe_swiglu_backward", SWB, over) == code
+
+
+@pytest.mark.parametrize("args,code", [
+    ((P, P, P, 4, 4, 60, None, 1, None, P, P, None), UNSUP), ((P, P, P, 3, 4, 64, None, 1, None, P, P, None), ARG),
+    ((P, P, P, 4, 4, 64, None, 2, None, P, P, None), ARG), ((P, P, P, 4, 4, 64, P, 257, None, P, P, None), ARG),
+    ((P, None, P, 4, 4, 64, None, 1, None, P, P, None), ARG), ((P, P, P, 4, 4, 64, None, 1, None, P, None, None), ARG),
+    ((P, P + 4, P, 4, 4, 64, None, 1, None, P, P, None), UNSUP), ((P, P, P, 4, 4, 64, None, 1, None, P + 8, P, None), UNSUP),
+    ((P, P, P, 4, 4, 64, None, 1, None, P, P + 4, None), UNSUP), ((P, P, P, 4, -1, 64, None, 1, None, P, P, None), ARG),
+])
+def test_requant_cols_refuses(lib, args, code):
+    assert lib.moe_requant_cols(*args) == code
+
+
+def test_swiglu_of_no_rows_does_nothing(lib):
+    n = ctypes.c_size_t()
+    assert call(lib, "moe_swiglu_forward", SWF, dict(T=0, gu=None, act=None, q=None, scale=None)) == OK
+    assert call(lib, "moe_swiglu_backward", SWB, {**NONE, "T": 0, "save": None}) == OK
+    assert lib.moe_requant_cols(P, None, None, 0, 0, 64, None, 1, None, None, None, None) == OK
+    assert lib.moe_swiglu_workspace_size(10, 136, ctypes.byref(n)) == OK and n.value == 4 * 10 * 2
+    assert lib.moe_swiglu_workspace_size(10, 136, None) == ARG
+
+
+def test_swiglu_gradient_against_differences():
+    rng = np.random.default_rng(4)
+    g, u, dact, gate = rng.normal(size=(3, 10)) * 2, rng.normal(size=(3, 10)), rng.normal(size=(3, 10)), rng.normal(size=3)
+    dg, du, act, dgate, *_ = oo.swiglu_backward(g, u, dact, gate)
+    f = lambda a, b, w: (oo.swiglu(a, b) * dact * w[:, None]).sum()  # noqa: E731
+    assert np.allclose(dg, _numeric(lambda z: f(z, u, gate), g), atol=1e-7)
+    assert np.allclose(du, _numeric(lambda z: f(g, z, gate), u), atol=1e-7)
+    assert np.allclose(dgate, _numeric(lambda z: f(g, u, z), gate), atol=1e-7)
+    assert np.allclose(act, oo.swiglu(g, u) * gate[:, None])
