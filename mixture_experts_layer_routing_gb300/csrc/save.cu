@@ -1,5 +1,7 @@
 // SwiGLU with an 8-bit checkpoint of its input, its gradient from the checkpoint, and 8-bit rows quantised anew along the
 // token axis (moe_swiglu_*, moe_requant_cols).
+#include <type_traits>
+
 #include "fp8_quant.cuh"
 #include "launch.cuh"
 #include "segs.cuh"
@@ -122,16 +124,82 @@ __global__ void __launch_bounds__(256) swiglu_fwd_kernel(const bf16* __restrict_
   if (first) scale[i] = block_scale(m);
 }
 
-// SwiGLU's gradient from g, u and what arrives at act (da): of the gate half, of the up half, and act itself (not gated).
-struct Grad { float dg, du, a; };
-__device__ __forceinline__ Grad swiglu_grad(float g, float u, float da) {
-  const float s = sigmoid_f(g), gs = g * s;
-  Grad r;
-  r.a = gs * u;
-  r.du = da * gs;
-  r.dg = da * u * (s + gs * (1.f - s));
+// The larger of m and two magnitudes; NaN if one is.
+__device__ __forceinline__ float amax3(float m, float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(fabsf(a)), "f"(fabsf(b)));
   return r;
 }
+
+// SwiGLU's gradient, two values at a time: from g, u and what arrives at act (da) that of the gate half and of the up
+// half, and act itself (not gated).
+struct Grad2 { uint64_t dg, du, a; };
+__device__ __forceinline__ Grad2 swiglu_grad2(uint64_t g, uint64_t u, uint64_t da) {
+  float x, y;
+  f32x2_get(f32x2_mul(g, f32x2(-1.44269504f, -1.44269504f)), x, y);
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(x));
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(y));
+  const uint64_t one = f32x2(1.f, 1.f);
+  f32x2_get(f32x2_fma(f32x2(x, y), one, one), x, y);
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(x));
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(y));
+  const uint64_t s = f32x2(x, y), gs = f32x2_mul(g, s), rest = f32x2_fma(s, f32x2(-1.f, -1.f), one);
+  Grad2 r;
+  r.a = f32x2_mul(gs, u);
+  r.du = f32x2_mul(da, gs);
+  r.dg = f32x2_mul(f32x2_mul(da, u), f32x2_fma(gs, rest, s));
+  return r;
+}
+__device__ __forceinline__ uint64_t codes_f32x2(uint32_t c, uint64_t scale) {
+  const float2 v = from_codes2(c);
+  return f32x2_mul(f32x2(v.x, v.y), scale);
+}
+__device__ __forceinline__ uint64_t bf16_f32x2(uint32_t w) {
+  return f32x2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+// Codes of 16 values (8 pairs) of a block with the largest magnitude m.
+__device__ __forceinline__ uint4 codes_of_pairs(const uint64_t (&v)[8], float m) {
+  const Divisor d(m);
+  float f[16];
+  if (d.plain) {
+    const uint64_t rr = f32x2(d.r, d.r), nm = f32x2(-m, -m);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f32x2_get(code2(v[i], rr, nm), f[2 * i], f[2 * i + 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      f32x2_get(v[i], f[2 * i], f[2 * i + 1]);
+      f[2 * i] = code_value(f[2 * i], m);
+      f[2 * i + 1] = code_value(f[2 * i + 1], m);
+    }
+  }
+  return make_uint4(pack_codes4(f[0], f[1], f[2], f[3]), pack_codes4(f[4], f[5], f[6], f[7]),
+                    pack_codes4(f[8], f[9], f[10], f[11]), pack_codes4(f[12], f[13], f[14], f[15]));
+}
+
+// Four neighbouring columns' divisors; codes of four tokens' values, PLAIN where no quotient needs a division.
+struct Divisor4 {
+  float m[4];
+  uint64_t r0, r1, n0, n1;
+  bool plain;
+  __device__ __forceinline__ explicit Divisor4(const float4& v) : m{v.x, v.y, v.z, v.w} {
+    const Divisor a(m[0]), b(m[1]), c(m[2]), d(m[3]);
+    plain = a.plain && b.plain && c.plain && d.plain;
+    r0 = f32x2(a.r, b.r), r1 = f32x2(c.r, d.r), n0 = f32x2(-m[0], -m[1]), n1 = f32x2(-m[2], -m[3]);
+  }
+  // lo, hi: columns 0, 1 and 2, 3 -> the quotients, by column
+  template <bool PLAIN> __device__ __forceinline__ void quotients(uint64_t lo, uint64_t hi, float (&q)[4]) const {
+    if (PLAIN) {
+      f32x2_get(code2(lo, r0, n0), q[0], q[1]);
+      f32x2_get(code2(hi, r1, n1), q[2], q[3]);
+    } else {
+      f32x2_get(lo, q[0], q[1]);
+      f32x2_get(hi, q[2], q[3]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q[i] = code_value(q[i], m[i]);
+    }
+  }
+};
 
 struct SaveBwdParams {
   const uint8_t* save;
@@ -153,20 +221,52 @@ struct SaveBwdParams {
 
 constexpr int kOutPitch = 144;     // bytes of a column's 128 codes, 16 apart in the banks
 
+// The tile in shared memory that the columns are computed from. Their codes are put where it was.
+struct BwdTile {
+  uint2 d[128][32];        // dact: [token][four columns a lane]
+  uint32_t g[128][32], u[128][32];
+};
+static_assert(3 * 128 * kOutPitch <= sizeof(BwdTile), "the codes fit where the tile was");
+
+// Codes of a warp's 16 tokens and a lane's four columns, of dg, du and act: [output][column][token / 4].
+template <bool PLAIN>
+__device__ __forceinline__ void column_codes(const BwdTile& tile, const float4* row_of, const Divisor4 (&div)[3], int warp,
+                                             int lane, uint32_t (&w)[3][4][4]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float v[3][4][4];      // [output][token][column]
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int lr = warp * 16 + q * 4 + i;
+      const float4 z = row_of[lr];
+      const uint2 d = tile.d[lr][lane];
+      const uint32_t g = tile.g[lr][lane], u = tile.u[lr][lane];
+      const uint64_t zg = f32x2(z.x, z.x), zu = f32x2(z.y, z.y), gate = f32x2(z.z, z.z);
+      const Grad2 a = swiglu_grad2(codes_f32x2(g, zg), codes_f32x2(u, zu), f32x2_mul(bf16_f32x2(d.x), gate));
+      const Grad2 b = swiglu_grad2(codes_f32x2(g >> 16, zg), codes_f32x2(u >> 16, zu), f32x2_mul(bf16_f32x2(d.y), gate));
+      div[0].quotients<PLAIN>(a.dg, b.dg, v[0][i]);
+      div[1].quotients<PLAIN>(a.du, b.du, v[1][i]);
+      div[2].quotients<PLAIN>(f32x2_mul(a.a, gate), f32x2_mul(b.a, gate), v[2][i]);
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) w[k][c][q] = pack_codes4(v[k][0][c], v[k][1][c], v[k][2][c], v[k][3][c]);
+  }
+}
+
 // CTA per 128 tokens of a segment and 128 columns of f. Rows first: eight lanes a row, 16 columns each, whose maxima by
 // rows are shuffles and by columns stay in registers until the last row. Then (COLS) columns: a warp takes 16 tokens, a
-// lane two neighbouring columns, and the values are computed again from the tile in shared memory, which costs less than
+// lane four neighbouring columns, and the values are computed again from the tile in shared memory, which costs less than
 // keeping three fp32 values of each.
 template <bool COLS>
 __global__ void __launch_bounds__(256, 2) swiglu_bwd_kernel(SaveBwdParams P) {
   __shared__ SegSmem seg;
   __shared__ float4 row_of[128];          // scales of g and u, gate
   extern __shared__ __align__(16) uint8_t smem[];
-  uint4(*sd)[16] = reinterpret_cast<uint4(*)[16]>(smem);                     // dact: [token][128 columns]
-  uint4(*sg)[8] = reinterpret_cast<uint4(*)[8]>(smem + 32768);               // codes of g, u
-  uint4(*su)[8] = reinterpret_cast<uint4(*)[8]>(smem + 49152);
-  float(*red)[3][128] = reinterpret_cast<float(*)[3][128]>(smem + 65536);    // [warp]: maxima of columns
-  uint8_t(*out)[64][kOutPitch] = reinterpret_cast<uint8_t(*)[64][kOutPitch]>(smem + 65536);   // after them: dg, du, act
+  BwdTile& tile = *reinterpret_cast<BwdTile*>(smem);
+  uint8_t(*out)[128][kOutPitch] = reinterpret_cast<uint8_t(*)[128][kOutPitch]>(smem);       // dg, du, act
+  float(*red)[3][128] = reinterpret_cast<float(*)[3][128]>(smem + sizeof(BwdTile));         // [16 groups of rows]: maxima
   griddep_wait();
   griddep_launch();
   load_segments(seg, P.off, P.G, P.T, kScaleBlock, P.status);
@@ -184,6 +284,7 @@ __global__ void __launch_bounds__(256, 2) swiglu_bwd_kernel(SaveBwdParams P) {
   }
 #pragma unroll 1
   for (int i = 0; i < 4; ++i) {
+    if (row0 + i * 32 >= row1) break;      // (a segment's last tile)
     const int lr = i * 32 + (tid >> 3);
     const long long row = row0 + lr;
     const bool in = row < row1;
@@ -200,42 +301,57 @@ __global__ void __launch_bounds__(256, 2) swiglu_bwd_kernel(SaveBwdParams P) {
       if (P.gate) gate = P.gate[row];
     }
     if (COLS) {
-      sd[lr][(tid & 7) * 2] = d[0];
-      sd[lr][(tid & 7) * 2 + 1] = d[1];
-      sg[lr][tid & 7] = g;
-      su[lr][tid & 7] = u;
+      reinterpret_cast<uint4*>(tile.d[lr])[(tid & 7) * 2] = d[0];
+      reinterpret_cast<uint4*>(tile.d[lr])[(tid & 7) * 2 + 1] = d[1];
+      reinterpret_cast<uint4*>(tile.g[lr])[tid & 7] = g;
+      reinterpret_cast<uint4*>(tile.u[lr])[tid & 7] = u;
       if ((tid & 7) == 0) row_of[lr] = make_float4(zg, zu, gate, 0.f);
     }
     const uint32_t wd[8] = {d[0].x, d[0].y, d[0].z, d[0].w, d[1].x, d[1].y, d[1].z, d[1].w};
     const uint32_t wg[4] = {g.x, g.y, g.z, g.w}, wu[4] = {u.x, u.y, u.z, u.w};
-    float dg[16], du[16], mg = 0.f, mu = 0.f, dot = 0.f;
+    const uint64_t z2g = f32x2(zg, zg), z2u = f32x2(zu, zu), gate2 = f32x2(gate, gate);
+    uint64_t dg[8], du[8], dot2 = 0;
+    float mg = 0.f, mu = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float2 gv = from_codes2(wg[j >> 1] >> (16 * (j & 1))), uv = from_codes2(wu[j >> 1] >> (16 * (j & 1)));
-      const float d0 = __uint_as_float(wd[j] << 16), d1 = __uint_as_float(wd[j] & 0xffff0000u);
-      const Grad r0 = swiglu_grad(gv.x * zg, uv.x * zu, d0 * gate), r1 = swiglu_grad(gv.y * zg, uv.y * zu, d1 * gate);
-      dg[2 * j] = r0.dg, dg[2 * j + 1] = r1.dg;
-      du[2 * j] = r0.du, du[2 * j + 1] = r1.du;
-      mg = max_nan(max_nan(mg, fabsf(r0.dg)), fabsf(r1.dg));
-      mu = max_nan(max_nan(mu, fabsf(r0.du)), fabsf(r1.du));
-      dot = fmaf(r1.a, d1, fmaf(r0.a, d0, dot));
+      const uint64_t da = bf16_f32x2(wd[j]);
+      const Grad2 r = swiglu_grad2(codes_f32x2(wg[j >> 1] >> (16 * (j & 1)), z2g), codes_f32x2(wu[j >> 1] >> (16 * (j & 1)), z2u),
+                                   f32x2_mul(da, gate2));
+      dg[j] = r.dg;
+      du[j] = r.du;
+      dot2 = f32x2_fma(r.a, da, dot2);
+      float x, y;
+      f32x2_get(r.dg, x, y);
+      mg = amax3(mg, x, y);
+      if (COLS) cm[0][2 * j] = max_nan(cm[0][2 * j], fabsf(x)), cm[0][2 * j + 1] = max_nan(cm[0][2 * j + 1], fabsf(y));
+      f32x2_get(r.du, x, y);
+      mu = amax3(mu, x, y);
       if (COLS) {
-        cm[0][2 * j] = max_nan(cm[0][2 * j], fabsf(r0.dg)), cm[0][2 * j + 1] = max_nan(cm[0][2 * j + 1], fabsf(r1.dg));
-        cm[COLS ? 1 : 0][2 * j] = max_nan(cm[COLS ? 1 : 0][2 * j], fabsf(r0.du));
-        cm[COLS ? 1 : 0][2 * j + 1] = max_nan(cm[COLS ? 1 : 0][2 * j + 1], fabsf(r1.du));
-        cm[COLS ? 2 : 0][2 * j] = max_nan(cm[COLS ? 2 : 0][2 * j], fabsf(r0.a * gate));
-        cm[COLS ? 2 : 0][2 * j + 1] = max_nan(cm[COLS ? 2 : 0][2 * j + 1], fabsf(r1.a * gate));
+        cm[COLS ? 1 : 0][2 * j] = max_nan(cm[COLS ? 1 : 0][2 * j], fabsf(x));
+        cm[COLS ? 1 : 0][2 * j + 1] = max_nan(cm[COLS ? 1 : 0][2 * j + 1], fabsf(y));
+        f32x2_get(f32x2_mul(r.a, gate2), x, y);
+        cm[COLS ? 2 : 0][2 * j] = max_nan(cm[COLS ? 2 : 0][2 * j], fabsf(x));
+        cm[COLS ? 2 : 0][2 * j + 1] = max_nan(cm[COLS ? 2 : 0][2 * j + 1], fabsf(y));
       }
     }
     if (P.dgu && in) {
       bf16* dst = P.dgu + row * 2 * P.f + c;
+      uint32_t x[8], y[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float p, q;
+        f32x2_get(dg[j], p, q);
+        x[j] = pack2(p, q);
+        f32x2_get(du[j], p, q);
+        y[j] = pack2(p, q);
+      }
       if (one) {
-        *reinterpret_cast<uint4*>(dst) = pack8(dg);
-        *reinterpret_cast<uint4*>(dst + P.f) = pack8(du);
+        *reinterpret_cast<uint4*>(dst) = make_uint4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<uint4*>(dst + P.f) = make_uint4(y[0], y[1], y[2], y[3]);
       }
       if (two) {
-        *reinterpret_cast<uint4*>(dst + 8) = pack8(dg + 8);
-        *reinterpret_cast<uint4*>(dst + P.f + 8) = pack8(du + 8);
+        *reinterpret_cast<uint4*>(dst + 8) = make_uint4(x[4], x[5], x[6], x[7]);
+        *reinterpret_cast<uint4*>(dst + P.f + 8) = make_uint4(y[4], y[5], y[6], y[7]);
       }
     }
     if (P.dq) {              // (f is a multiple of 128)
@@ -245,11 +361,8 @@ __global__ void __launch_bounds__(256, 2) swiglu_bwd_kernel(SaveBwdParams P) {
         mu = max_nan(mu, __shfl_xor_sync(0xffffffffu, mu, o));
       }
       if (in) {
-        uint32_t w[4];
-        codes<16>(dg, mg, w);
-        *reinterpret_cast<uint4*>(P.dq + row * 2 * P.f + c) = make_uint4(w[0], w[1], w[2], w[3]);
-        codes<16>(du, mu, w);
-        *reinterpret_cast<uint4*>(P.dq + row * 2 * P.f + P.f + c) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(P.dq + row * 2 * P.f + c) = codes_of_pairs(dg, mg);
+        *reinterpret_cast<uint4*>(P.dq + row * 2 * P.f + P.f + c) = codes_of_pairs(du, mu);
         if ((tid & 7) == 0) {
           P.dq_scale[row * 2 * P.nb + b] = block_scale(mg);
           P.dq_scale[row * 2 * P.nb + P.nb + b] = block_scale(mu);
@@ -257,6 +370,9 @@ __global__ void __launch_bounds__(256, 2) swiglu_bwd_kernel(SaveBwdParams P) {
       }
     }
     if (P.part) {
+      float x, y;
+      f32x2_get(dot2, x, y);
+      float dot = x + y;
 #pragma unroll
       for (int o = 4; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
       if (in && (tid & 7) == 0) P.part[(long long)b * P.T + row] = dot;
@@ -266,90 +382,55 @@ __global__ void __launch_bounds__(256, 2) swiglu_bwd_kernel(SaveBwdParams P) {
 #pragma unroll
   for (int k = 0; k < 3; ++k)
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      float m = cm[COLS ? k : 0][j];
-      m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 8));
-      m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 16));
-      if (lane < 8) red[warp][k][lane * 16 + j] = m;
+    for (int j = 0; j < 16; j += 4) {
+      float4 m;
+      float* v = &cm[COLS ? k : 0][j];
+      m.x = max_nan(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
+      m.y = max_nan(v[1], __shfl_xor_sync(0xffffffffu, v[1], 16));
+      m.z = max_nan(v[2], __shfl_xor_sync(0xffffffffu, v[2], 16));
+      m.w = max_nan(v[3], __shfl_xor_sync(0xffffffffu, v[3], 16));
+      if (lane < 16) *reinterpret_cast<float4*>(&red[warp * 2 + (lane >> 3)][k][(lane & 7) * 16 + j]) = m;
     }
   __syncthreads();
-  float mx[2][3][2];         // [half of the columns][output][column of the pair]
+  // one warp an output, four columns a lane: the first three warps finish the maxima
+  if (warp < 3) {
+    float4 m = *reinterpret_cast<const float4*>(&red[0][warp][lane * 4]);
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      float2 m = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < 8; ++w) {
-        const float2 v = *reinterpret_cast<const float2*>(&red[w][k][h * 64 + 2 * lane]);
-        m.x = max_nan(m.x, v.x);
-        m.y = max_nan(m.y, v.y);
-      }
-      mx[h][k][0] = m.x, mx[h][k][1] = m.y;
+    for (int i = 1; i < 16; ++i) {
+      const float4 v = *reinterpret_cast<const float4*>(&red[i][warp][lane * 4]);
+      m.x = max_nan(m.x, v.x), m.y = max_nan(m.y, v.y), m.z = max_nan(m.z, v.z), m.w = max_nan(m.w, v.w);
     }
-  __syncthreads();           // (out lies where the maxima were)
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int c0 = b * kScaleBlock + h * 64;
-    if (c0 >= P.f) break;
-    uint64_t rr[3], nm[3];
-    bool plain = true;
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      const Divisor x(mx[h][k][0]), y(mx[h][k][1]);
-      plain = plain && x.plain && y.plain;
-      rr[k] = f32x2(x.r, y.r);
-      nm[k] = f32x2(-mx[h][k][0], -mx[h][k][1]);
-    }
-#pragma unroll 1
-    for (int q = 0; q < 4; ++q) {
-      float v[3][2][4];      // codes' values of four tokens
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int lr = warp * 16 + q * 4 + i;
-        const float4 z = row_of[lr];
-        const uint32_t wd = reinterpret_cast<const uint32_t*>(&sd[lr][0])[h * 32 + lane];
-        const float2 gv = from_codes2(reinterpret_cast<const uint16_t*>(&sg[lr][0])[h * 32 + lane]);
-        const float2 uv = from_codes2(reinterpret_cast<const uint16_t*>(&su[lr][0])[h * 32 + lane]);
-        const Grad r0 = swiglu_grad(gv.x * z.x, uv.x * z.y, __uint_as_float(wd << 16) * z.z);
-        const Grad r1 = swiglu_grad(gv.y * z.x, uv.y * z.y, __uint_as_float(wd & 0xffff0000u) * z.z);
-        const float p[3][2] = {{r0.dg, r1.dg}, {r0.du, r1.du}, {r0.a * z.z, r1.a * z.z}};
-#pragma unroll
-        for (int k = 0; k < 3; ++k) {
-          if (plain) {
-            f32x2_get(code2(f32x2(p[k][0], p[k][1]), rr[k], nm[k]), v[k][0][i], v[k][1][i]);
-          } else {
-            v[k][0][i] = code_value(p[k][0], mx[h][k][0]);
-            v[k][1][i] = code_value(p[k][1], mx[h][k][1]);
-          }
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < 3; ++k)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          *reinterpret_cast<uint32_t*>(&out[k][e * 32 + lane][warp * 16 + q * 4]) =
-              pack_codes4(v[k][e][0], v[k][e][1], v[k][e][2], v[k][e][3]);
-    }
-    const int cl = c0 + 2 * lane;
-    if (warp < 3 && cl < P.f) {     // f is even
+    *reinterpret_cast<float4*>(&red[0][warp][lane * 4]) = m;
+    const int cl = b * kScaleBlock + lane * 4;
+    if (cl < P.f) {            // f is a multiple of 8
       float* s = warp == 2 ? P.actt_scale + (long long)t * P.f + cl : P.dqt_scale + (long long)t * 2 * P.f + warp * P.f + cl;
-      const float x = warp == 0 ? mx[h][0][0] : warp == 1 ? mx[h][1][0] : mx[h][2][0];
-      const float y = warp == 0 ? mx[h][0][1] : warp == 1 ? mx[h][1][1] : mx[h][2][1];
-      s[0] = block_scale(x);
-      s[1] = block_scale(y);
+      s[0] = block_scale(m.x), s[1] = block_scale(m.y), s[2] = block_scale(m.z), s[3] = block_scale(m.w);
     }
-    __syncthreads();
+  }
+  __syncthreads();
+  const Divisor4 div[3] = {Divisor4(*reinterpret_cast<const float4*>(&red[0][0][lane * 4])),
+                           Divisor4(*reinterpret_cast<const float4*>(&red[0][1][lane * 4])),
+                           Divisor4(*reinterpret_cast<const float4*>(&red[0][2][lane * 4]))};
+  uint32_t w[3][4][4] = {};
+  if (row0 + warp * 16 < row1) {
+    if (div[0].plain && div[1].plain && div[2].plain) column_codes<true>(tile, row_of, div, warp, lane, w);
+    else column_codes<false>(tile, row_of, div, warp, lane, w);
+  }
+  __syncthreads();           // (the codes go where the tile is)
 #pragma unroll
-    for (int i = 0; i < 6; ++i) {
-      const int k = i >> 1, e = i & 1, r = e * 32 + (tid >> 3), col = c0 + 2 * (r & 31) + e;
-      if (col < P.f) {
-        uint8_t* dst = k == 2 ? P.actt + (long long)col * P.Tp : P.dqt + (long long)(k * P.f + col) * P.Tp;
-        *reinterpret_cast<uint4*>(dst + (long long)t * kScaleBlock + (tid & 7) * 16) =
-            *reinterpret_cast<const uint4*>(&out[k][r][(tid & 7) * 16]);
-      }
+  for (int k = 0; k < 3; ++k)
+#pragma unroll
+    for (int c4 = 0; c4 < 4; ++c4)
+      *reinterpret_cast<uint4*>(&out[k][c4 * 32 + lane][warp * 16]) = make_uint4(w[k][c4][0], w[k][c4][1], w[k][c4][2], w[k][c4][3]);
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 12; ++i) {
+    const int k = i >> 2, e = i & 3, r = e * 32 + (tid >> 3), col = b * kScaleBlock + 4 * (r & 31) + e;
+    if (col < P.f) {
+      uint8_t* dst = k == 2 ? P.actt + (long long)col * P.Tp : P.dqt + (long long)(k * P.f + col) * P.Tp;
+      *reinterpret_cast<uint4*>(dst + (long long)t * kScaleBlock + (tid & 7) * 16) =
+          *reinterpret_cast<const uint4*>(&out[k][r][(tid & 7) * 16]);
     }
-    __syncthreads();
   }
 }
 
@@ -369,13 +450,17 @@ __global__ void __launch_bounds__(256) sum_parts_kernel(const float* __restrict_
 }
 
 // CTA per 128 tokens and 128 columns: 8-bit rows to 8-bit columns, of the values code * scale. A warp takes 16 tokens, a
-// lane four neighbouring columns; its 16 words of codes are decoded twice, for the maxima and for the codes.
-__global__ void __launch_bounds__(256) requant_cols_kernel(const uint8_t* __restrict__ q, const float* __restrict__ scale,
-                                                           int src_rows, int T, int C, int nb, const int* __restrict__ off,
-                                                           int G, const int* __restrict__ row_index, uint8_t* __restrict__ qt,
-                                                           float* __restrict__ scale_t, long long Tp, int* status) {
+// lane four neighbouring columns; its 16 words of codes are decoded twice, for the maxima and for the codes. 12,288
+// gathered rows x 2048 in 24 us (4.5 at the copy rate): instructions, some 12 a value. Runs of 2, 4 or 8 column blocks a
+// CTA with the next block's words on their way took 25, 26 and 27.
+__global__ void __launch_bounds__(256, 4) requant_cols_kernel(const uint8_t* __restrict__ q, const float* __restrict__ scale,
+                                                              int src_rows, int T, int C, int nb, const int* __restrict__ off,
+                                                              int G, const int* __restrict__ row_index,
+                                                              uint8_t* __restrict__ qt, float* __restrict__ scale_t,
+                                                              long long Tp, int* status) {
   __shared__ SegSmem seg;
   __shared__ float4 red[8][32];
+  __shared__ float row_scale[8][16];
   __shared__ __align__(16) uint8_t out[128][kOutPitch];       // [column of four, four columns][token]
   griddep_wait();
   griddep_launch();
@@ -385,35 +470,41 @@ __global__ void __launch_bounds__(256) requant_cols_kernel(const uint8_t* __rest
   const int g = segment_of(seg, G, t);
   const int row0 = seg.off[g] + (t - seg.tile[g]) * kScaleBlock, row1 = seg.off[g + 1];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.x, c = b * kScaleBlock + lane * 4;
+  const bool any = row0 + warp * 16 < row1;        // (else the warp's columns are zeros)
   // lane i < 16 looks token i of the warp up
   int src = -1;
-  float z = 0.f;
   if (lane < 16 && row0 + warp * 16 + lane < row1) {
     src = row0 + warp * 16 + lane;
     if (row_index) src = row_index[src];
     if ((unsigned)src >= (unsigned)src_rows) {
       set_error(status, MOE_ERR_DEVICE_INDEX);
       src = -1;
-    } else {
-      z = scale[(long long)src * nb + b];
     }
   }
-  uint32_t w[16];
-  float s[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int r = __shfl_sync(0xffffffffu, src, i);
-    s[i] = __shfl_sync(0xffffffffu, z, i);
-    w[i] = r >= 0 && c < C ? *reinterpret_cast<const uint32_t*>(q + (long long)r * C + c) : 0u;
-  }
+  uint32_t x[16];
   float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (any) {
+    const float z = src >= 0 ? scale[(long long)src * nb + b] : 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float2 x = from_codes2(w[i]), y = from_codes2(w[i] >> 16);
-    m.x = max_nan(m.x, fabsf(x.x * s[i]));
-    m.y = max_nan(m.y, fabsf(x.y * s[i]));
-    m.z = max_nan(m.z, fabsf(y.x * s[i]));
-    m.w = max_nan(m.w, fabsf(y.y * s[i]));
+    for (int i = 0; i < 16; ++i) {
+      const int r = __shfl_sync(0xffffffffu, src, i);
+      x[i] = r >= 0 && c < C ? *reinterpret_cast<const uint32_t*>(q + (long long)r * C + c) : 0u;
+    }
+    if (lane < 16) row_scale[warp][lane] = z;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+      const float s0 = row_scale[warp][i], s1 = row_scale[warp][i + 1];
+      float a0, a1, a2, a3, c0, c1, c2, c3;
+      f32x2_get(codes_f32x2(x[i], f32x2(s0, s0)), a0, a1);
+      f32x2_get(codes_f32x2(x[i] >> 16, f32x2(s0, s0)), a2, a3);
+      f32x2_get(codes_f32x2(x[i + 1], f32x2(s1, s1)), c0, c1);
+      f32x2_get(codes_f32x2(x[i + 1] >> 16, f32x2(s1, s1)), c2, c3);
+      m.x = amax3(m.x, a0, c0);
+      m.y = amax3(m.y, a1, c1);
+      m.z = amax3(m.z, a2, c2);
+      m.w = amax3(m.w, a3, c3);
+    }
   }
   red[warp][lane] = m;
   __syncthreads();
@@ -422,27 +513,29 @@ __global__ void __launch_bounds__(256) requant_cols_kernel(const uint8_t* __rest
     const float4 v = red[i][lane];
     m.x = max_nan(m.x, v.x), m.y = max_nan(m.y, v.y), m.z = max_nan(m.z, v.z), m.w = max_nan(m.w, v.w);
   }
-  const Divisor dx(m.x), dy(m.y), dz(m.z), dw(m.w);
-  const bool plain = dx.plain && dy.plain && dz.plain && dw.plain;
-  const uint64_t r0 = f32x2(dx.r, dy.r), r1 = f32x2(dz.r, dw.r), n0 = f32x2(-m.x, -m.y), n1 = f32x2(-m.z, -m.w);
+  const Divisor4 div(m);
+  const auto codes_to = [&](auto plain) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    float v[4][4];           // [column][token]
+    for (int k = 0; k < 4; ++k) {
+      float v[4][4];         // [token][column]
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 x = from_codes2(w[4 * k + i]), y = from_codes2(w[4 * k + i] >> 16);
-      const float e = s[4 * k + i];
-      if (plain) {
-        f32x2_get(code2(f32x2(x.x * e, x.y * e), r0, n0), v[0][i], v[1][i]);
-        f32x2_get(code2(f32x2(y.x * e, y.y * e), r1, n1), v[2][i], v[3][i]);
-      } else {
-        v[0][i] = code_value(x.x * e, m.x), v[1][i] = code_value(x.y * e, m.y);
-        v[2][i] = code_value(y.x * e, m.z), v[3][i] = code_value(y.y * e, m.w);
+      for (int i = 0; i < 4; ++i) {
+        const float s = row_scale[warp][4 * k + i];
+        div.quotients<decltype(plain)::value>(codes_f32x2(x[4 * k + i], f32x2(s, s)), codes_f32x2(x[4 * k + i] >> 16, f32x2(s, s)),
+                                              v[i]);
       }
-    }
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      *reinterpret_cast<uint32_t*>(&out[j * 32 + lane][warp * 16 + k * 4]) = pack_codes4(v[j][0], v[j][1], v[j][2], v[j][3]);
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<uint32_t*>(&out[j * 32 + lane][warp * 16 + k * 4]) = pack_codes4(v[0][j], v[1][j], v[2][j], v[3][j]);
+    }
+  };
+  if (!any) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(&out[j * 32 + lane][warp * 16]) = make_uint4(0u, 0u, 0u, 0u);
+  } else if (div.plain) {
+    codes_to(std::true_type{});
+  } else {
+    codes_to(std::false_type{});
   }
   if (warp == 0 && c < C)    // C is a multiple of 8
     *reinterpret_cast<float4*>(scale_t + (long long)t * C + c) =
@@ -479,8 +572,7 @@ cudaError_t swiglu_backward(const moe_ops_s* o, const void* save, const float* s
   const dim3 grid(nb, Tp / kScaleBlock);
   *n += 1;
   if (dqt) {
-    constexpr int smem = 65536 + 3 * 64 * kOutPitch;
-    static_assert(3 * 64 * kOutPitch >= 8 * 3 * 128 * 4, "the maxima fit where the codes go");
+    constexpr int smem = sizeof(BwdTile) + 16 * 3 * 128 * sizeof(float);
     MOE_TRY(cudaFuncSetAttribute(swiglu_bwd_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     MOE_TRY(launch_pdl(swiglu_bwd_kernel<true>, grid, dim3(256), smem, s, P));
   } else {
