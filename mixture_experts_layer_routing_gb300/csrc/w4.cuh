@@ -337,10 +337,11 @@ struct W4Cursor {
 };
 constexpr int kSumBuffers = 2;       // of a warp
 
-// The warps of a CTA whose shared memory is there when `ctas` CTAs share an SM; `fixed` of it is the CTA's own.
-inline int w4_warps(int ctas, int most, size_t fixed, size_t per_warp) {
-  const size_t fit = (227 * 1024 / ctas - fixed - 1024) / per_warp;
-  return (int)min(fit, (size_t)most);
+// One CTA on an SM: the warps that multiply and, one more, the warp that joins; as many as its shared memory holds with
+// `fixed` bytes of the CTA's own. (Two CTAs of 8 warps each took 34.7 us for 32,768 x 7168 and one row, one of 16 takes
+// 30.3: half as many ranges of units, so the longest is nearer to the average.)
+inline int w4_warps(size_t fixed, size_t per_warp) {
+  return (int)min((227 * 1024 - fixed) / per_warp, (size_t)kW4Warps - 1);
 }
 
 // Sums of N units between the warps of a product and the warp that joins them, so that no product waits for another

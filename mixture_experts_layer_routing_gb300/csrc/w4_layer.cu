@@ -340,11 +340,10 @@ cudaError_t launch_up(const moe_ops_s* o, const W4LayerParams& P, cudaStream_t s
   auto* kern = w4_up_kernel<MT, XR, TMAX, GROUP, ZERO>;
   constexpr size_t per = Core::kBytes + kSumBuffers * XR * Core::kPitch * sizeof(float);
   const long long units = (long long)P.T * (P.k + P.slots - P.E) * (P.f / (MT * 8));
-  const int ctas = units <= o->sms ? 1 : 2;
-  const int warps = w4_warps(ctas, kW4Warps / ctas - 1, sizeof(LayerLists<TMAX>) + sizeof(LayerGates<TMAX>) + 128, per);
+  const int warps = w4_warps(sizeof(LayerLists<TMAX>) + sizeof(LayerGates<TMAX>) + 1024, per);
   const size_t smem = warps * per;
   MOE_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-  return launch_pdl(kern, dim3((unsigned)min(units, (long long)o->sms * ctas)), dim3((warps + 1) * 32), smem, s, P);
+  return launch_pdl(kern, dim3((unsigned)min(units, (long long)o->sms)), dim3((warps + 1) * 32), smem, s, P);
 }
 template <int MT, int XR, int TMAX, int GROUP, bool ZERO>
 cudaError_t launch_down(const moe_ops_s* o, const W4LayerParams& P, cudaStream_t s) {
@@ -352,11 +351,10 @@ cudaError_t launch_down(const moe_ops_s* o, const W4LayerParams& P, cudaStream_t
   auto* kern = w4_down_kernel<MT, XR, TMAX, GROUP, ZERO>;
   const size_t per = Core::kBytes + down_buffers(TMAX) * P.T * Core::kPitch * sizeof(float);
   const int units = ceil_div(P.d, MT * 16);
-  const int ctas = TMAX > 16 ? 2 : units <= o->sms ? 1 : units <= 2 * o->sms ? 2 : XR == 2 ? 4 : 3;
-  const int warps = w4_warps(ctas, ctas > 2 ? 4 : kW4Warps / ctas - 1, sizeof(LayerLists<TMAX>) + 128, per);
+  const int warps = w4_warps(sizeof(LayerLists<TMAX>) + 1024, per);
   const size_t smem = warps * per;
   MOE_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-  return launch_pdl(kern, dim3(min(units, o->sms * ctas)), dim3((warps + 1) * 32), smem, s, P);
+  return launch_pdl(kern, dim3(min(units, o->sms)), dim3((warps + 1) * 32), smem, s, P);
 }
 template <int GROUP, bool ZERO> cudaError_t pick_layer(const moe_ops_s* o, const W4LayerParams& P, cudaStream_t s) {
   if (P.T > 16) {
