@@ -86,6 +86,10 @@ __device__ __forceinline__ void decode8(uint32_t v, uint32_t off, uint32_t magic
   p[3] = bf16x2_sub(pair_of(v >> 12, magic), off);
 }
 
+// A value that is the same in all lanes, told to the compiler: what depends on it runs in the uniform pipe, and branches
+// on it need no reconvergence.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // A matrix of 4-bit weights: codes [N, K/8], scale [KG, N], zero [KG, N].
 struct W4 {
   const uint32_t* codes;

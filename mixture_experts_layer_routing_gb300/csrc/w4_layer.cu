@@ -96,12 +96,12 @@ __device__ __forceinline__ void build_lists(LayerLists<TMAX>& L, LayerGates<TMAX
   }
   __syncthreads();
 }
-// Slot of a tile, its first pair and how many.
+// Slot of a tile, its first pair and how many (by a whole warp).
 template <int TMAX>
 __device__ __forceinline__ int find_tile(const LayerLists<TMAX>& L, int tile, int rows, int& pair0, int& R) {
-  const int e = L.slot_of_tile[tile];
-  pair0 = L.pair[e] + (tile - L.tile[e]) * rows;
-  R = min(rows, L.pair[e + 1] - pair0);
+  const int e = uniform(L.slot_of_tile[tile]);
+  pair0 = uniform(L.pair[e] + (tile - L.tile[e]) * rows);
+  R = uniform(min(rows, L.pair[e + 1] - pair0));
   return e;
 }
 
@@ -116,13 +116,13 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) w4_up_kernel(W4LayerParams P
   __shared__ LayerLists<TMAX> L;
   __shared__ LayerGates<TMAX> gates;
   __shared__ W4Handover<kSumBuffers> hand;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = (blockDim.x >> 5) - 1;
+  const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5), warps = (blockDim.x >> 5) - 1;
   if (tid == 0) hand.init(warps);
   griddep_wait();
   griddep_launch();
   build_lists(L, &gates, P, XR);
   float* sums = reinterpret_cast<float*>(smem + warps * Core::kBytes);     // [kSumBuffers][warp][XR][kPitch]
-  const int blocks = P.f / kCols, tiles = L.tile[P.slots], C = (P.d + kChunk - 1) / kChunk;
+  const int blocks = P.f / kCols, tiles = uniform(L.tile[P.slots]), C = (P.d + kChunk - 1) / kChunk;
   const int units = tiles * blocks, u0 = (int)((long long)units * blockIdx.x / gridDim.x);      // this CTA's, in a row
   const int u1 = (int)((long long)units * (blockIdx.x + 1) / gridDim.x);
   int tile = u0 / blocks, m = u0 - tile * blocks, pair0 = 0, R = 0;
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) w4_up_kernel(W4LayerParams P
         int row0[MT], up0[MT];
 #pragma unroll
         for (int i = 0; i < MT; ++i) row0[i] = w.m * kCols + i * 8, up0[i] = P.f + row0[i];
-        core.aim(w4_matrix(P.w13, P.s13, L.slot_of_tile[aimed]), P.s13, row0, up0, 2 * P.f, w.c, lane);
+        core.aim(w4_matrix(P.w13, P.s13, uniform(L.slot_of_tile[aimed])), P.s13, row0, up0, 2 * P.f, w.c, lane);
       }
       core.copy(P.s13, to, lane);
       for (int n = w.next(warps, C, blocks); n > 0; --n) core.step(P.s13, kCols, C);
@@ -189,9 +189,9 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) w4_up_kernel(W4LayerParams P
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) issue(i * Core::kStage);
   read_x();
-  int c = warp;
+  int c = warp, at = -1;
   for (int u = u0; u < u1; ++u) {
-    find_tile(L, tile, XR, pair0, R);
+    if (tile != at) find_tile(L, at = tile, XR, pair0, R);
     float acc[MT][4] = {};
     for (; c < C; c += warps) {
       cp_wait<kStages - 2>();
@@ -223,13 +223,13 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) w4_down_kernel(W4LayerParams
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ LayerLists<TMAX> L;
   __shared__ W4Handover<kBufs> hand;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, quad = lane >> 2, t = lane & 3;
+  const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5), quad = lane >> 2, t = lane & 3;
   const int warps = (blockDim.x >> 5) - 1;
   if (tid == 0) hand.init(warps);
   // idx was written before the kernel in front of this one began; only h is that kernel's
   build_lists(L, (LayerGates<TMAX>*)nullptr, P, kPairs);
   float(*sums)[kPitch] = reinterpret_cast<float(*)[kPitch]>(smem + warps * Core::kBytes);   // [kBufs][warp][token][kCols]
-  const int units = (P.d + kCols - 1) / kCols, C = (P.f + kChunk - 1) / kChunk, items = L.tile[P.slots] * C;
+  const int units = (P.d + kCols - 1) / kCols, C = (P.f + kChunk - 1) / kChunk, items = uniform(L.tile[P.slots]) * C;
   if (warp == warps) {
     griddep_wait();
     griddep_launch();
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) w4_down_kernel(W4LayerParams
         int row0[MT], up0[MT];
 #pragma unroll
         for (int i = 0; i < MT; ++i) row0[i] = lu * kCols + i * 16, up0[i] = row0[i] + 8;
-        core.aim(w4_matrix(P.wd, P.sd, L.slot_of_tile[ltile]), P.sd, row0, up0, P.d, lc, lane);
+        core.aim(w4_matrix(P.wd, P.sd, uniform(L.slot_of_tile[ltile])), P.sd, row0, up0, P.d, lc, lane);
       }
       core.copy(P.sd, to, lane);
       ++lc;

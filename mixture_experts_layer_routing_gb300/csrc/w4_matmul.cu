@@ -29,21 +29,21 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) w4_matmul_kernel(W4MatmulPar
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ SegSmem seg;
   __shared__ W4Handover<kSumBuffers> hand;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = P.warps;
+  const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5), warps = P.warps;
   if (tid == 0) hand.init(warps);
   griddep_wait();
   griddep_launch();
   load_segments(seg, P.off, P.G, P.M, XR, P.status);
   float* sums = reinterpret_cast<float*>(smem + warps * Core::kBytes);     // [kSumBuffers][warp][XR][kPitch]
-  const int blocks = (P.s.N + kCols - 1) / kCols, tiles = seg.tile[P.G], C = (P.s.K + kChunk - 1) / kChunk;
+  const int blocks = (P.s.N + kCols - 1) / kCols, tiles = uniform(seg.tile[P.G]), C = (P.s.K + kChunk - 1) / kChunk;
   const int units = tiles * blocks, u0 = (int)((long long)units * blockIdx.x / gridDim.x);      // this CTA's, in a row
   const int u1 = (int)((long long)units * (blockIdx.x + 1) / gridDim.x);
   int tile = u0 / blocks, m = u0 - tile * blocks, at = -1, r0 = 0, R = 0;
   const auto rows = [&](int tl) {
     at = tl;
-    const int g = segment_of(seg, P.G, tl);
-    r0 = seg.off[g] + (tl - seg.tile[g]) * XR;
-    R = min(XR, seg.off[g + 1] - r0);
+    const int g = uniform(segment_of(seg, P.G, tl));
+    r0 = uniform(seg.off[g] + (tl - seg.tile[g]) * XR);
+    R = uniform(min(XR, seg.off[g + 1] - r0));
   };
   if (warp > warps) return;
   if (warp == warps) {
@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) w4_matmul_kernel(W4MatmulPar
         int row0[MT], up0[MT];
 #pragma unroll
         for (int i = 0; i < MT; ++i) row0[i] = w.m * kCols + i * 16, up0[i] = row0[i] + 8;
-        core.aim(w4_matrix(P.w, P.s, segment_of(seg, P.G, w.tile)), P.s, row0, up0, P.s.N, w.c, lane);
+        core.aim(w4_matrix(P.w, P.s, uniform(segment_of(seg, P.G, w.tile))), P.s, row0, up0, P.s.N, w.c, lane);
       }
       core.copy(P.s, to, lane);
       const int n = w.next(warps, C, blocks);
@@ -96,8 +96,8 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) w4_matmul_kernel(W4MatmulPar
     if (x.u >= u1) return;
     if (x.tile != xt) {
       xt = x.tile;
-      const int g = segment_of(seg, P.G, xt), first = seg.off[g] + (xt - seg.tile[g]) * XR;
-      xR = min(XR, seg.off[g + 1] - first);
+      const int g = uniform(segment_of(seg, P.G, xt)), first = uniform(seg.off[g] + (xt - seg.tile[g]) * XR);
+      xR = uniform(min(XR, seg.off[g + 1] - first));
       there = 0;
 #pragma unroll
       for (int r = 0; r < XR; ++r) {
