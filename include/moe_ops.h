@@ -196,9 +196,10 @@ moe_status moe_quant_w4(moe_ops ops, const void* w, int G, int N, int K, int gro
                         uint8_t* zero, void* stream);
 /* c[m, n] = sum over K of x[r(m), k] w[g(m), n, k], r(m) = row_index[m] or m: x [x_rows, K] bf16, rows ld_x elements
  * apart (a multiple of 8, 16-byte aligned); c [M, N] of out_dtype (MOE_BF16 or MOE_FP32); off, G, row_index and rows of
- * no segment as in moe_fp8_matmul. The values of x and w - zero meet on the tensor cores unrounded, sums are fp32, one
- * rounding at the end. Made for few rows: a segment's weights are read once for every 8 (M up to 8) or 16 of its rows,
- * so past some 64 rows the 8-bit products are the faster ones. */
+ * no segment as in moe_fp8_matmul; c 16-byte aligned. The values of x and code - zero meet on the tensor cores
+ * unrounded, sums are fp32 (a group's before its scale: |x| up to 2^116 cannot overflow), one rounding at the end. Made
+ * for few rows: the weights are decoded once for every 8 rows of a segment, so past some 32 rows the 8-bit products are
+ * the faster ones. */
 moe_status moe_w4_matmul(moe_ops ops, const void* x, long long ld_x, int x_rows, const int32_t* row_index, int M,
                          const moe_w4* w, const int32_t* off, int G, int N, int K, void* c, int out_dtype, void* stream);
 
@@ -215,7 +216,7 @@ typedef struct {
  * x [T, d] bf16, rows ld_x elements apart (a multiple of 8, 16-byte aligned); idx [T, k], gate [T, k] fp32 as
  * moe_gate_forward gives them (an expert may be named twice by a token: its gates add up); w13 of [E+n_shared, 2f, d]
  * (gate half, up half), wd of [E+n_shared, d, f], with one group size and both with zero points or neither; y [T, d]
- * of out_dtype. An index outside 0..E-1 is left out and records MOE_ERR_DEVICE_INDEX. h is kept to 16 bits of
+ * of out_dtype, 16-byte aligned. An index outside 0..E-1 is left out and records MOE_ERR_DEVICE_INDEX. h is kept to 16 bits of
  * mantissa, the other sums in fp32; one rounding at the end. Only experts in use are read. workspace:
  * moe_w4_experts_workspace_size bytes, 16-byte aligned; calls that may run at once need one each. */
 moe_status moe_w4_experts_workspace_size(const moe_w4_config* cfg, int T, size_t* bytes);

@@ -1,10 +1,17 @@
 // Few rows times 4-bit weights: what the kernels of w4.cu share.
 //
-// A warp takes 256 values of K (a chunk) of MT x 16 weight rows at a time and multiplies them with up to NT x 8 rows of
-// x on the legacy MMA (m16n8k16, weights as its 16 rows, x's rows as its columns): at one to eight rows the product is
-// bound by the weights' bytes, and an MMA issued by the warp that decoded its operand needs no hand-over through shared
-// or tensor memory. Chunks go through a ring of the warp's own in shared memory, filled by cp.async of 16 bytes, so no
-// warp waits for another one inside a product.
+// A warp takes 256 values of K (a chunk) of MT x 16 weight rows at a time and multiplies them with up to 8 rows of x on
+// the legacy MMA (m16n8k16, weights as its 16 rows, x's rows as its columns): at so few rows tensor throughput is no
+// limit (20% of this MMA's), and one issued by the warp that decoded its operand needs no hand-over through shared or
+// tensor memory. Chunks go through a ring of the warp's own in shared memory, filled by cp.async of 16 bytes, so no warp
+// waits for another one inside a product.
+//
+// What bounds it. The floor is the weights' bytes. Copies alone reach 83% of the copy rate (three stages of 4 KB for each
+// of 14 or 15 warps; with x in the same ring and two stages it was 55%). The products alone take longer: decoding 32 x 256
+// codes is 224 shifts and LOP3s on a pipe that issues one in two cycles and 128 subtractions, of some 640 instructions in
+// all, at 16 warps of 128 registers on an SM. 32,768 x 7168 by one row in 28.9 us (17.8 at the copy rate), by eight in
+// 37.3. Shifts as multiplications on the other pipe (mul.hi) were slower, and so were 24 warps of 80 registers, bulk
+// prefetches of the next units to L2, and two barriers a unit instead of a warp that joins.
 //
 // Decoding. A word holds eight values, the even ones in its low half, so (word >> 4i) & 0x000f000f is a pair of
 // neighbours; in the last bits of a bf16 mantissa under the exponent of 128 a code c reads 128 + c, and one packed
@@ -344,9 +351,8 @@ constexpr int kSumBuffers = 2;       // of a warp
 // One CTA on an SM: the warps that multiply and, one more, the warp that joins; as many as its shared memory holds with
 // `fixed` bytes of the CTA's own. (Two CTAs of 8 warps each took 34.7 us for 32,768 x 7168 and one row, one of 16 takes
 // 30.3: half as many ranges of units, so the longest is nearer to the average.)
-inline int w4_warps(size_t fixed, size_t per_warp) {
-  return (int)min((227 * 1024 - fixed) / per_warp, (size_t)kW4Warps - 1);
-}
+constexpr size_t w4_smem(size_t fixed) { return 227 * 1024 - 1024 - fixed; }
+inline int w4_warps(size_t fixed, size_t per_warp) { return (int)min(w4_smem(fixed) / per_warp, (size_t)kW4Warps - 1); }
 
 // Sums of N units between the warps of a product and the warp that joins them, so that no product waits for another
 // warp's or for the join.

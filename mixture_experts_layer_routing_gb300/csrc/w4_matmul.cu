@@ -191,9 +191,10 @@ cudaError_t launch_matmul(const moe_ops_s* o, W4MatmulParams P, cudaStream_t s) 
   auto* kern = w4_matmul_kernel<MT, XR, GROUP, ZERO>;
   constexpr size_t per = Core::kBytes + kSumBuffers * XR * Core::kPitch * sizeof(float);
   const long long units = (long long)(ceil_div(P.M, XR) + (P.off ? min(P.G, P.M) : 0)) * ceil_div(P.s.N, MT * 16);
-  P.warps = w4_warps(sizeof(SegSmem) + 1024, per);
+  constexpr size_t fixed = sizeof(SegSmem) + 128;
+  P.warps = w4_warps(fixed, per);
   const size_t smem = P.warps * per;
-  MOE_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+  MOE_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)w4_smem(fixed)));
   return launch_pdl(kern, dim3((unsigned)min(units, (long long)o->sms)), dim3(max(P.warps + 1, 8) * 32), smem, s, P);
 }
 template <int MT, int XR> cudaError_t pick_matmul(const moe_ops_s* o, const W4MatmulParams& P, int group, cudaStream_t s) {

@@ -313,3 +313,37 @@ def test_the_layer_behind_the_gate_and_its_two_products(ops):
     dense = torch.einsum("tkf,tkdf->tkd", h.float()[r["inv"].view(T, k).long()], Wd.float()[r["idx"].long()])
     assert ((o[r["inv"].view(T, k).long()] - dense).norm() / dense.norm()).item() < 0.15
     assert ops.status() == 0
+
+
+def test_host_threads_with_other_numbers_of_tokens(ops):
+    """One kernel's shared memory differs with the number of tokens: host threads that share the handle and launch at
+    once (a ctypes call lets other threads run) get their launches and their results."""
+    import ctypes
+    import threading
+
+    from mixture_experts_layer_routing_gb300 import ops as mops
+    d, f, E, k = 256, 96, 8, 3
+    _, (x, idx, gate, w13, wd) = layer(ops, 16, d, f, E, k, 0, 32, False)
+    pack = lambda w: mops.moe_w4(w["codes"].data_ptr(), w["scale"].data_ptr(), None, 32)  # noqa: E731
+    a, b, cfg = pack(w13), pack(wd), mops.moe_w4_config(E, 0, k, d, f)
+    counts = [3, 16, 5, 12]
+    want = [ops.w4_experts(x[:T], idx[:T], gate[:T], w13, wd, out_dtype=torch.float32) for T in counts]
+    out = [torch.zeros_like(w) for w in want]
+    ws = [torch.empty(T * k * 2 * f * 2, dtype=torch.uint8, device="cuda") for T in counts]
+    streams, bad = [torch.cuda.Stream() for _ in counts], []
+    torch.cuda.synchronize()
+
+    def work(i):
+        for _ in range(2000):
+            bad.append(ops._lib.moe_w4_experts(ops.h, ctypes.byref(cfg), x.data_ptr(), d, counts[i], idx.data_ptr(),
+                                               gate.data_ptr(), ctypes.byref(a), ctypes.byref(b), out[i].data_ptr(), 0,
+                                               ws[i].data_ptr(), ctypes.c_void_p(streams[i].cuda_stream)))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not any(bad) and ops.status() == 0
+    assert all(torch.equal(o, w) for o, w in zip(out, want))
