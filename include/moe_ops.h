@@ -207,8 +207,8 @@ typedef struct {
   int E;              /* routed experts, 1..256 */
   int n_shared;       /* experts E .. E+n_shared-1 that every token takes with a gate of 1, 0..8 */
   int k;              /* routed experts of a token, 1..8 */
-  int d;              /* a multiple of 32 */
-  int f;              /* a multiple of 32 */
+  int d;              /* a multiple of 32 up to 2^20 */
+  int f;              /* likewise */
 } moe_w4_config;
 /* The experts' layer of T = 0..64 tokens, behind the routing, in two kernels:
  *   y_t = sum_j gate[t, j] FFN_idx[t, j](x_t) + sum of the shared experts' FFN(x_t)

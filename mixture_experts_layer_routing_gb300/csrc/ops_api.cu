@@ -62,7 +62,7 @@ moe_status check_w4(const moe_w4* w, int N, int K) {
 moe_status check_w4_experts(const moe_w4_config* c, int T) {
   CHECK(c && c->E >= 1 && c->k >= 1 && c->n_shared >= 0 && c->d >= 1 && c->f >= 1 && T >= 0, MOE_ERR_INVALID_ARG);
   CHECK(c->E <= 256 && c->k <= 8 && c->n_shared <= 8 && T <= 64, MOE_ERR_UNSUPPORTED);
-  CHECK(c->d % 32 == 0 && c->f % 32 == 0 && c->d < (1 << 24) && c->f < (1 << 24), MOE_ERR_UNSUPPORTED);
+  CHECK(c->d % 32 == 0 && c->f % 32 == 0 && c->d <= (1 << 20) && c->f <= (1 << 20), MOE_ERR_UNSUPPORTED);
   return MOE_OK;
 }
 

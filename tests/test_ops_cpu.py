@@ -250,7 +250,8 @@ W4L = dict(ops=P, cfg=None, x=P, ld=256, T=4, idx=P, gate=P, w13=None, wd=None, 
     ({}, dict(ops=None), {}, ARG), (dict(E=0), {}, {}, ARG), (dict(k=0), {}, {}, ARG), (dict(n_shared=-1), {}, {}, ARG),
     (dict(d=0), {}, {}, ARG), (dict(f=0), {}, {}, ARG), ({}, dict(T=-1), {}, ARG), (dict(E=257), {}, {}, UNSUP),
     (dict(k=9), {}, {}, UNSUP), (dict(n_shared=9), {}, {}, UNSUP), ({}, dict(T=65), {}, UNSUP),
-    (dict(d=240), {}, {}, UNSUP), (dict(f=80), {}, {}, UNSUP), ({}, dict(out=2), {}, ARG), ({}, dict(x=None), {}, ARG),
+    (dict(d=240), {}, {}, UNSUP), (dict(f=80), {}, {}, UNSUP), (dict(f=(1 << 20) + 32), {}, {}, UNSUP),
+    (dict(d=(1 << 20) + 32), {}, {}, UNSUP), ({}, dict(out=2), {}, ARG), ({}, dict(x=None), {}, ARG),
     ({}, dict(idx=None), {}, ARG), ({}, dict(gate=None), {}, ARG), ({}, dict(y=None), {}, ARG), ({}, dict(ld=128), {}, ARG),
     ({}, dict(ld=260), {}, UNSUP), ({}, dict(x=P + 8), {}, UNSUP), ({}, dict(y=P + 2), {}, UNSUP),
     ({}, dict(workspace=None), {}, WS), ({}, dict(workspace=P + 8), {}, WS), ({}, {}, dict(group=32), UNSUP),
