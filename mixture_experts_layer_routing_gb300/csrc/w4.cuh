@@ -166,6 +166,10 @@ template <int MT, int XR, int GROUP, bool ZERO> struct W4Core {
     wx = kX + (lane >> 4) * (XR * 256) + p * 16;
     rx = kX + (quad & (XR - 1)) * 256 + (quad & 1) * 64 + t * 16;      // (columns from XR on repeat others, unused)
     slot = 0;
+    // rows are stored only after they were read, but by two counts that the compiler cannot relate: without values here it
+    // may let a row that a tile in front did not have keep what the register held
+#pragma unroll
+    for (int i = 0; i < XR; ++i) x[i] = make_uint4(0u, 0u, 0u, 0u);
   }
   // From chunk c on of rows row0[i] .. +8 and up0[i] .. +8 (i = 0 .. MT) of the matrix w, as far as they are below `end`
   // (a multiple of 8, above row0[0]); others repeat some and get scales of zero.

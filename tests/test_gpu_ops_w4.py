@@ -229,6 +229,19 @@ def test_w4_experts_all_tokens_on_one_expert(ops, rows):
     layer(ops, rows, 96, 64, 3, 1, 0, 32, False, idx=torch.full((rows, 1), 2, dtype=torch.int32))
 
 
+@pytest.mark.parametrize("rows", [2, 3, 4, 8, 16, 24, 64])
+def test_w4_experts_whose_tokens_grow_and_shrink(ops, rows):
+    """One, then all, then two tokens an expert, over and over: each warp meets tiles with more rows than the one in front."""
+    E, k = 60, 8
+    idx = torch.full((rows, k), -1, dtype=torch.int32)
+    idx[:, 0], idx[:, 1], idx[:, 2] = 1, 30, 58
+    for t in range(rows):
+        idx[t, 3:] = torch.tensor([2 + (5 * t + j) % 28 if j < 3 else 31 + (3 * t + j) % 27 for j in range(5)])
+    layer(ops, rows, 256, 96, E, k, 0, 32, False, idx=idx)
+    layer(ops, rows, 96, 288, E, k, 1, 128, True, idx=idx, seed=3)
+    assert ops.status() == 0
+
+
 def test_w4_experts_named_twice_and_out_of_range(ops):
     import mixture_experts_layer_routing_gb300 as moe
     idx = torch.tensor([[1, 1, 1], [0, 2, 0], [2, 3, 3]], dtype=torch.int32)
