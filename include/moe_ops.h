@@ -217,7 +217,7 @@ typedef struct {
  * moe_gate_forward gives them (an expert may be named twice by a token: its gates add up); w13 of [E+n_shared, 2f, d]
  * (gate half, up half), wd of [E+n_shared, d, f], with one group size and both with zero points or neither; y [T, d]
  * of out_dtype, 16-byte aligned. An index outside 0..E-1 is left out and records MOE_ERR_DEVICE_INDEX. h is kept to 16 bits of
- * mantissa, the other sums in fp32; one rounding at the end. Only experts in use are read. workspace:
+ * mantissa (24 for fp32 outputs), the other sums in fp32; one rounding at the end. Only experts in use are read. workspace:
  * moe_w4_experts_workspace_size bytes, 16-byte aligned; calls that may run at once need one each. */
 moe_status moe_w4_experts_workspace_size(const moe_w4_config* cfg, int T, size_t* bytes);
 moe_status moe_w4_experts(moe_ops ops, const moe_w4_config* cfg, const void* x, long long ld_x, int T,

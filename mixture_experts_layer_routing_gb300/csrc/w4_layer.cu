@@ -33,7 +33,8 @@ struct W4LayerParams {
   const float* gate;
   W4 w13, wd;
   W4Shape s13, sd;
-  bf16* h;                // [pairs][2][f] bf16: rounded, and what the rounding left
+  bf16* h;                // [pairs][parts][f]: rounded, what the rounding left, and (3) what its rounding left
+  int parts;
   void* y;
   int out_fp32;
   int* status;
@@ -143,13 +144,17 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) w4_up_kernel(W4LayerParams P
           up += from[w * kSums + at + 8];
         }
         const float h = silu_f(g) * up * gate;
-        // h as a sum of two bf16 (16 bits of mantissa), so that the layer rounds once, at its output
+        // h as a sum of bf16 values, two (16 bits of mantissa) or for fp32 outputs three (24), so that the layer rounds
+        // once, at its output. (Two for fp32 outputs were off by up to 3.2e-6 of y's norm, three are by 2.1e-7; 16 tokens
+        // of 32 experts, d = 7168, take 273 us instead of 212, one token 49 instead of 47.)
+        bf16* dst = P.h + (long long)(pair0 + r) * P.parts * P.f + m * kCols + j;
         const bf16 hi = __float2bfloat16_rn(h);
-        const float rest = h - __bfloat162float(hi);
-        const bf16 lo = __float2bfloat16_rn(fabsf(rest) <= 3.3895314e38f ? rest : 0.f);
-        bf16* dst = P.h + (long long)(pair0 + r) * 2 * P.f + m * kCols + j;
+        float rest = h - __bfloat162float(hi);
+        if (!(fabsf(rest) <= 3.3895314e38f)) rest = 0.f;        // (an infinity or a NaN has left nothing)
+        const bf16 lo = __float2bfloat16_rn(rest);
         dst[0] = hi;
         dst[P.f] = lo;
+        if (P.parts == 3) dst[2 * (long long)P.f] = __float2bfloat16_rn(rest - __bfloat162float(lo));
       }
       hand.taken(u - u0, lane);
       if (++m == blocks) m = 0, ++tile;
@@ -213,13 +218,13 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) w4_up_kernel(W4LayerParams P
 
 constexpr int down_buffers(int tmax) { return tmax > 16 ? 1 : 2; }      // (of all tokens' sums, a warp)
 
-// MT x 16 values of y for all tokens a unit. The chunks of all experts in use are dealt to the warps in runs; rows 2r and
-// 2r + 1 of a tile are the two parts of pair r's h, and a warp adds an expert's product to its own sums of the tokens,
-// which the last warp adds up.
-template <int MT, int XR, int TMAX, int GROUP, bool ZERO>
+// MT x 16 values of y for all tokens a unit. The chunks of all experts in use are dealt to the warps in runs; the rows of
+// a tile are the parts of its pairs' h, 2 a pair, or 3 and a row of zeros, and a warp adds an expert's product to its own
+// sums of the tokens, which the last warp adds up.
+template <int MT, int XR, int PARTS, int TMAX, int GROUP, bool ZERO>
 __global__ void __launch_bounds__(kW4Warps * 32, 1) w4_down_kernel(W4LayerParams P) {
   using Core = W4Core<MT, XR, GROUP, ZERO>;
-  constexpr int kPairs = XR / 2, kCols = MT * 16, kPitch = Core::kPitch, kBufs = down_buffers(TMAX);
+  constexpr int kRows = PARTS == 3 ? 4 : 2, kPairs = XR / kRows, kCols = MT * 16, kPitch = Core::kPitch, kBufs = down_buffers(TMAX);
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ LayerLists<TMAX> L;
   __shared__ W4Handover<kBufs> hand;
@@ -284,9 +289,10 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) w4_down_kernel(W4LayerParams
       int p0;
       find_tile(L, xtile, kPairs, p0, xR);
 #pragma unroll
-      for (int r = 0; r < XR; ++r) core.xoff[r] = r < 2 * xR ? (unsigned)(2 * p0 + r) * (unsigned)(P.f / 8) : 0u;
+      for (int r = 0; r < XR; ++r)
+        core.xoff[r] = r / kRows < xR && r % kRows < PARTS ? (unsigned)((p0 + r / kRows) * PARTS + r % kRows) * (unsigned)(P.f / 8) : 0u;
     }
-    core.read_x(P.h, xc, P.f, 2 * xR, ~0u, lane);
+    core.read_x(P.h, xc, P.f, kRows * xR, PARTS == 3 ? 0x77u : 0xffu, lane);
     ++xc;
     if (--xleft == 0) xu += gridDim.x;
   };
@@ -307,7 +313,7 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) w4_down_kernel(W4LayerParams
       cp_wait<kStages - 2>();
       __syncwarp();
       issue(core.free_slot());
-      core.store_x(2 * R);
+      core.store_x(kRows * R);
       read_h();
       __syncwarp();
       core.multiply(acc, P.f - c * kChunk, lane);
@@ -315,10 +321,16 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) w4_down_kernel(W4LayerParams
       if (++c == C || q == n) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          if (t < R) {
-            float* dst = mine[L.token[pair0 + t]] + mt * 16 + quad;
-            dst[0] += acc[mt][0] + acc[mt][1];
-            dst[8] += acc[mt][2] + acc[mt][3];
+          float lo = acc[mt][0] + acc[mt][1], hi = acc[mt][2] + acc[mt][3];
+          if (PARTS == 3) {        // two lanes a pair
+            lo += __shfl_xor_sync(0xffffffffu, lo, 1);
+            hi += __shfl_xor_sync(0xffffffffu, hi, 1);
+          }
+          const int r = PARTS == 3 ? t >> 1 : t;
+          if (r < R && (PARTS == 2 || !(t & 1))) {
+            float* dst = mine[L.token[pair0 + r]] + mt * 16 + quad;
+            dst[0] += lo;
+            dst[8] += hi;
           }
 #pragma unroll
           for (int k = 0; k < 4; ++k) acc[mt][k] = 0.f;
@@ -346,10 +358,10 @@ cudaError_t launch_up(const moe_ops_s* o, const W4LayerParams& P, cudaStream_t s
   MOE_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)w4_smem(fixed)));
   return launch_pdl(kern, dim3((unsigned)min(units, (long long)o->sms)), dim3((warps + 1) * 32), smem, s, P);
 }
-template <int MT, int XR, int TMAX, int GROUP, bool ZERO>
+template <int MT, int XR, int PARTS, int TMAX, int GROUP, bool ZERO>
 cudaError_t launch_down(const moe_ops_s* o, const W4LayerParams& P, cudaStream_t s) {
   using Core = W4Core<MT, XR, GROUP, ZERO>;
-  auto* kern = w4_down_kernel<MT, XR, TMAX, GROUP, ZERO>;
+  auto* kern = w4_down_kernel<MT, XR, PARTS, TMAX, GROUP, ZERO>;
   const size_t per = Core::kBytes + down_buffers(TMAX) * P.T * Core::kPitch * sizeof(float);
   const int units = ceil_div(P.d, MT * 16);
   constexpr size_t fixed = sizeof(LayerLists<TMAX>) + 128;
@@ -362,20 +374,21 @@ cudaError_t launch_down(const moe_ops_s* o, const W4LayerParams& P, cudaStream_t
 template <int GROUP, bool ZERO> cudaError_t pick_layer(const moe_ops_s* o, const W4LayerParams& P, cudaStream_t s) {
   if (P.T > 16) {
     MOE_TRY((launch_up<2, 8, 64, GROUP, ZERO>(o, P, s)));
-    return launch_down<2, 8, 64, GROUP, ZERO>(o, P, s);
+    return P.parts == 3 ? launch_down<2, 8, 3, 64, GROUP, ZERO>(o, P, s) : launch_down<2, 8, 2, 64, GROUP, ZERO>(o, P, s);
   }
   // (4 rows a tile instead of 8 for 3 or 4 tokens, or where experts have one pair on average, measured within 2% and up to
   // 7% slower at 8 tokens of 64 experts; 32 weight rows a unit of the down product instead of 16 takes 222 us instead of
   // 210 for 16 tokens of 32 experts at d = 7168, and 94 instead of 75 at d = 2048: fewer units than SMs)
   if (P.T <= 2) MOE_TRY((launch_up<2, 2, 16, GROUP, ZERO>(o, P, s)));
   else MOE_TRY((launch_up<2, 8, 16, GROUP, ZERO>(o, P, s)));
-  return P.T <= 1 ? launch_down<1, 2, 16, GROUP, ZERO>(o, P, s) : launch_down<1, 8, 16, GROUP, ZERO>(o, P, s);
+  if (P.parts == 3) return launch_down<1, 8, 3, 16, GROUP, ZERO>(o, P, s);
+  return P.T <= 1 ? launch_down<1, 2, 2, 16, GROUP, ZERO>(o, P, s) : launch_down<1, 8, 2, 16, GROUP, ZERO>(o, P, s);
 }
 
 }  // namespace
 
 size_t w4_experts_workspace(const moe_w4_config& c, int T) {
-  return (size_t)T * (c.k + c.n_shared) * 2 * c.f * sizeof(bf16);
+  return (size_t)T * (c.k + c.n_shared) * 3 * c.f * sizeof(bf16);
 }
 
 cudaError_t w4_experts(const moe_ops_s* o, const moe_w4_config& c, const void* x, long long ld, int T, const int* idx,
@@ -384,7 +397,7 @@ cudaError_t w4_experts(const moe_ops_s* o, const moe_w4_config& c, const void* x
   const auto weights = [](const moe_w4& w) { return W4{w.codes, (const bf16*)w.scale, w.zero}; };
   const W4LayerParams P = {(const bf16*)x, (unsigned)(ld / 8), T, c.k, c.E, c.E + c.n_shared, c.d, c.f, idx, gate,
                            weights(w13), weights(wd), {2 * c.f, c.d, ceil_div(c.d, w13.group)},
-                           {c.d, c.f, ceil_div(c.f, w13.group)}, (bf16*)ws, y, out_fp32, o->status};
+                           {c.d, c.f, ceil_div(c.f, w13.group)}, (bf16*)ws, out_fp32 ? 3 : 2, y, out_fp32, o->status};
   *n += 2;
   const bool z = w13.zero != nullptr;
   if (w13.group == 32) return z ? pick_layer<32, true>(o, P, s) : pick_layer<32, false>(o, P, s);

@@ -200,10 +200,11 @@ def quant_w4(w, group, with_zero):
     return codes, scale, zero
 
 
-def w4_experts(x, idx, gate, w13, wd, n_shared, add):
+def w4_experts(x, idx, gate, w13, wd, n_shared, add, kept=16):
     """(y, bound) of the experts' layer: w13 and wd lists of [2f, d] and [d, f] values. `add` is what an fp32 sum over
     d or f may be off, relative to the sum of its terms' magnitudes; bound is what y may be off before it is rounded:
-    the products' sums, SwiGLU with the fast exponential and division (2^-18), and h kept to 2^-16."""
+    the products' sums, SwiGLU with the fast exponential and division (2^-18), and h kept to
+    2^-kept (16 for bf16 outputs, 24 for fp32 ones)."""
     T = x.shape[0]
     E = len(w13) - n_shared
     y, bound = np.zeros((T, wd[0].shape[0])), np.zeros((T, wd[0].shape[0]))
@@ -216,7 +217,7 @@ def w4_experts(x, idx, gate, w13, wd, n_shared, add):
                 a, u, sa, su = gu[:f], gu[f:], size[:f], size[f:]
                 s = a / (1 + np.exp(-a))
                 h = g * s * u
-                off = np.abs(g) * add * (1.1 * np.abs(u) * sa + np.abs(s) * su) + (2.0 ** -18 + 2.0 ** -16) * np.abs(h)
+                off = np.abs(g) * add * (1.1 * np.abs(u) * sa + np.abs(s) * su) + (2.0 ** -18 + 2.0 ** -kept) * np.abs(h)
                 y[t] += wd[e] @ h
                 bound[t] += np.abs(wd[e]) @ (off + add * np.abs(h))
     return y, bound

@@ -203,7 +203,7 @@ def layer(ops, T, d, f, E, k, shared, group, zero, out=torch.float32, seed=0, id
     gate = torch.rand(T, idx.shape[1], generator=g) - 0.2
     y = ops.w4_experts(x.cuda(), idx.cuda(), gate.cuda(), w13, wd, n_shared=shared, out_dtype=out)
     add = (24 + max(-(-d // group), (idx.shape[1] + shared) * -(-f // group))) * 2.0 ** -23
-    want, bound = oo.w4_experts(f64(x), idx.numpy(), f64(gate), v13, vd, shared, add)
+    want, bound = oo.w4_experts(f64(x), idx.numpy(), f64(gate), v13, vd, shared, add, 24 if out == torch.float32 else 16)
     err = np.abs(f64(y) - want)
     tol = bound + HALF[out] * (np.abs(want) + bound)
     assert np.all(err <= tol), (np.unravel_index(np.argmax(err - tol), err.shape), err.max())
@@ -342,7 +342,7 @@ def test_host_threads_with_other_numbers_of_tokens(ops):
     counts = [3, 16, 5, 12]
     want = [ops.w4_experts(x[:T], idx[:T], gate[:T], w13, wd, out_dtype=torch.float32) for T in counts]
     out = [torch.zeros_like(w) for w in want]
-    ws = [torch.empty(T * k * 2 * f * 2, dtype=torch.uint8, device="cuda") for T in counts]
+    ws = [torch.empty(T * k * 3 * f * 2, dtype=torch.uint8, device="cuda") for T in counts]
     streams, bad = [torch.cuda.Stream() for _ in counts], []
     torch.cuda.synchronize()
 
