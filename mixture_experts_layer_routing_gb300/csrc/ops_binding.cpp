@@ -567,7 +567,10 @@ PyObject* quant_w4(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const int64_t KG = (K + g - 1) / g;
     void* codes = get(k_codes, "codes", at::kInt, N, K / 8);
     void* scale = get(k_scale, "scale", at::kBFloat16, KG, N);
-    void* zero = PyObject_IsTrue(a.a[5]) ? get(k_zero, "zero", at::kByte, KG, N) : nullptr;
+    const int points = PyObject_IsTrue(a.a[5]);
+    if (points < 0) throw Refused();
+    if (!points && entry(out, k_zero)) refuse(PyExc_ValueError, "out", "holds zero points that the weights would not have");
+    void* zero = points ? get(k_zero, "zero", at::kByte, KG, N) : nullptr;
     return moe_quant_w4(a.ops, w.data_ptr(), to_int(G, "w"), to_int(N, "w"), to_int(K, "w"), (int)g, (uint32_t*)codes,
                         scale, (uint8_t*)zero, a.stream);
   });

@@ -119,3 +119,54 @@ def test_decoding_with_4_bit_experts(example, T, d, f, E, k, group, zero):
     assert block.ops.status() == 0
     # and not far from the bf16 weights: half a step of a fifteenth of a group's range, twice, some 5-7% each
     assert far(out, plain(block, x, res, r["idx"].long(), r["gate"], block.W13, block.Wd)[0].detach()) < 0.3
+
+
+def test_tensors_that_do_not_fit_are_refused():
+    """By the binding, before anything is launched: nothing runs, no status is recorded."""
+    import mixture_experts_layer_routing_gb300 as moe
+    ops = moe.default_ops()
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    f32 = lambda *s: torch.zeros(s, device="cuda")  # noqa: E731
+    w, w3, wd = ops.quant_w4(bf(64, 96), 32), ops.quant_w4(bf(3, 64, 96), 32), ops.quant_w4(bf(3, 96, 32), 32)
+    x, idx, gate = bf(4, 96), i32(4, 2), f32(4, 2)
+    f = ops.swiglu(bf(4, 256), want=("q", "save"))
+    before = ops.launch_count()
+    E = (ValueError, TypeError, RuntimeError)
+    bad = [
+        lambda: ops.quant_w4(bf(64, 96), 48), lambda: ops.quant_w4(bf(64, 80), 32), lambda: ops.quant_w4(bf(60, 96), 32),
+        lambda: ops.quant_w4(f32(64, 96), 32), lambda: ops.quant_w4(bf(64, 192)[:, ::2], 32), lambda: ops.quant_w4(bf(96), 32),
+        lambda: ops.quant_w4(bf(64, 96), 32, out=dict(codes=i32(64, 11))),
+        # weights without zero points into a dict that keeps another's
+        lambda: ops.quant_w4(bf(64, 96), 32, zero=False, out=dict(zero=torch.zeros(3, 64, dtype=torch.uint8, device="cuda"))),
+        lambda: ops.w4_matmul(bf(4, 64), w), lambda: ops.w4_matmul(x.float(), w), lambda: ops.w4_matmul(x.cpu(), w),
+        lambda: ops.w4_matmul(x, w3), lambda: ops.w4_matmul(x, w, off=i32(2)), lambda: ops.w4_matmul(x, w3, off=i32(3)),
+        lambda: ops.w4_matmul(x, dict(w, group=64)), lambda: ops.w4_matmul(x, dict(codes=w["codes"], group=32)),
+        lambda: ops.w4_matmul(x, dict(w, scale=w["scale"].float())), lambda: ops.w4_matmul(x, dict(w, zero=w["scale"])),
+        lambda: ops.w4_matmul(x, w, out=f32(4, 63)), lambda: ops.w4_matmul(x, w, out_dtype=torch.float16),
+        lambda: ops.w4_matmul(x, w, row_index=i32(4).long()), lambda: ops.w4_matmul(bf(4, 97)[:, 1:], w),
+        lambda: ops.w4_matmul(x.t().contiguous().t(), w),
+        lambda: ops.w4_experts(x, idx, gate, w3, w3), lambda: ops.w4_experts(x, idx.long(), gate, w3, wd),
+        lambda: ops.w4_experts(x, idx, gate[:, :1], w3, wd), lambda: ops.w4_experts(x, idx, gate, w3, wd, n_shared=3),
+        lambda: ops.w4_experts(x, idx, gate, w3, wd, n_shared=-1), lambda: ops.w4_experts(x, idx[0], gate, w3, wd),
+        lambda: ops.w4_experts(bf(65, 96), i32(65, 2), f32(65, 2), w3, wd),
+        lambda: ops.w4_experts(x, i32(4, 0), f32(4, 0), w3, wd), lambda: ops.w4_experts(x, idx, gate, w3, wd, out=bf(4, 95)),
+        lambda: ops.swiglu(bf(4, 255)), lambda: ops.swiglu(bf(4, 24)), lambda: ops.swiglu(f32(4, 256)),
+        lambda: ops.swiglu(bf(4, 256), out=dict(other=None)), lambda: ops.swiglu(bf(4, 256), out={}),
+        lambda: ops.swiglu(bf(4, 256), out=dict(q=None)), lambda: ops.swiglu(bf(4, 256), out=dict(act=f32(4, 128))),
+        lambda: ops.swiglu_backward(bf(4, 120), f["save"], f["save_scale"]),
+        lambda: ops.swiglu_backward(bf(4, 128), f["save"], f["save_scale"][:, :1].contiguous()),
+        lambda: ops.swiglu_backward(bf(4, 128), f["save"], f["save_scale"], gate=f32(3)),
+        lambda: ops.swiglu_backward(bf(4, 128), f["save"], f["save_scale"], want=("x",)),
+        lambda: ops.swiglu_backward(bf(4, 128), f["save"], f["save_scale"], out=dict(actt=None, actt_scale=None)),
+        lambda: ops.swiglu_backward(bf(4, 136), torch.zeros(4, 272, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn),
+                                    f32(4, 4), want=("dq",)),
+        lambda: ops.requant_cols(f["q"], f["scale"].double()), lambda: ops.requant_cols(f["q"].view(torch.uint8), f["scale"]),
+        lambda: ops.requant_cols(f["q"], f["scale"], row_index=i32(4, 1)), lambda: ops.requant_cols(f["q"].t(), f["scale"]),
+        lambda: ops.requant_cols(f["q"], f["scale"], out=dict(q=f["q"])),
+    ]
+    for i, call in enumerate(bad):
+        with pytest.raises(E):
+            call()
+            raise AssertionError(i)
+    assert ops.launch_count() == before and ops.status() == 0
