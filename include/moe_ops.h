@@ -147,7 +147,7 @@ moe_status moe_fp8_wgrad(moe_ops ops, const void* dct, const float* dct_scale, c
                          int T, const int32_t* off, int G, int N, int K, void* c, int out_dtype, void* stream);
 
 /* ---- SwiGLU with an 8-bit checkpoint: gu = (g, u) halves of a row, act = silu(g) * u.
- * gu [T, 2f] bf16, rows ld elements apart; f and ld multiples of 8, 16-byte aligned. Outputs (one at least): act [T, f]
+ * gu [T, 2f] bf16, rows ld elements apart; f (below 2^28) and ld multiples of 8, gu and act 16-byte aligned. Outputs (one at least): act [T, f]
  * bf16; q [T, f] with scale [T, ceil(f/128)], act's codes (of the unrounded values, as moe_quant_rows with swiglu); save
  * [T, 2f] with save_scale [T, 2 ceil(f/128)], the codes of g and of u, blocks of 128 within each half, the gate's scales
  * first (what the backward pass reads; with f a multiple of 128 they are moe_quant_rows of gu). Codes 8-byte aligned. */
@@ -162,14 +162,16 @@ moe_status moe_swiglu_forward(moe_ops ops, const void* gu, long long ld, int T, 
  * with dq_scale [T, 2f/128], its rows' codes (f a multiple of 128); dqt [2f, Tp] with dqt_scale [Tp/128, 2f], its codes
  * along the tokens, and with them actt [f, Tp], actt_scale [Tp/128, f], those of act', segments and padding as in
  * moe_quant_cols; dgate [T]. off (nullable, G+1 ascending within 0 .. T) tells the segments; rows of no segment are not
- * written. workspace: moe_swiglu_workspace_size bytes, 16-byte aligned, for dgate (else NULL). */
+ * written. save is 8-byte aligned, dgu, dq, dqt and actt 16-byte. workspace: moe_swiglu_workspace_size bytes, 16-byte
+ * aligned, for dgate (else NULL). */
 moe_status moe_swiglu_workspace_size(int T, int f, size_t* bytes);
 moe_status moe_swiglu_backward(moe_ops ops, const void* save, const float* save_scale, const void* dact, long long ld,
                                const float* gate, int T, int f, const int32_t* off, int G, void* dgu, void* dq,
                                float* dq_scale, void* dqt, float* dqt_scale, void* actt, float* actt_scale,
                                float* dgate, void* workspace, void* stream);
 /* moe_quant_cols of rows that are held in 8 bits (q [src_rows, C], scale [src_rows, ceil(C/128)], as moe_quant_rows and
- * moe_norm_forward give them): the values code * scale, quantised along the tokens. C is a multiple of 8. */
+ * moe_norm_forward give them): the values code * scale, quantised along the tokens. C is a multiple of 8 below 2^28; q 8-byte aligned, qt
+ * and scale_t 16-byte. */
 moe_status moe_requant_cols(moe_ops ops, const void* q, const float* scale, int src_rows, int T, int C,
                             const int32_t* off, int G, const int32_t* row_index, void* qt, float* scale_t, void* stream);
 

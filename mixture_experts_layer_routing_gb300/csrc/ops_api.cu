@@ -314,7 +314,7 @@ moe_status moe_fp8_wgrad(moe_ops ops, const void* dct, const float* dct_scale, c
 moe_status moe_swiglu_forward(moe_ops ops, const void* gu, long long ld, int T, int f, void* act, void* q, float* scale,
                               void* save, float* save_scale, void* stream) {
   CHECK(ops && T >= 0 && f >= 1 && ld >= 2ll * f, MOE_ERR_INVALID_ARG);
-  CHECK(f % 8 == 0 && ld % 8 == 0, MOE_ERR_UNSUPPORTED);
+  CHECK(f % 8 == 0 && ld % 8 == 0 && f < (1 << 28), MOE_ERR_UNSUPPORTED);
   if (T == 0) return MOE_OK;
   CHECK(gu && (act || q || save) && (q != nullptr) == (scale != nullptr) && (save != nullptr) == (save_scale != nullptr),
         MOE_ERR_INVALID_ARG);
@@ -326,6 +326,7 @@ moe_status moe_swiglu_forward(moe_ops ops, const void* gu, long long ld, int T, 
 
 moe_status moe_swiglu_workspace_size(int T, int f, size_t* bytes) {
   CHECK(T >= 0 && f >= 1 && bytes, MOE_ERR_INVALID_ARG);
+  CHECK(f < (1 << 28), MOE_ERR_UNSUPPORTED);
   *bytes = sizeof(float) * (size_t)T * ceil_div(f, kScaleBlock);
   return MOE_OK;
 }
@@ -338,7 +339,7 @@ moe_status moe_swiglu_backward(moe_ops ops, const void* save, const float* save_
   CHECK((dq != nullptr) == (dq_scale != nullptr) && (dqt != nullptr) == (dqt_scale != nullptr) &&
             (actt != nullptr) == (actt_scale != nullptr) && (dqt != nullptr) == (actt != nullptr),
         MOE_ERR_INVALID_ARG);
-  CHECK(f % 8 == 0 && ld % 8 == 0 && T <= (1 << 22) && (!dq || f % kScaleBlock == 0), MOE_ERR_UNSUPPORTED);
+  CHECK(f % 8 == 0 && ld % 8 == 0 && f < (1 << 28) && T <= (1 << 22) && (!dq || f % kScaleBlock == 0), MOE_ERR_UNSUPPORTED);
   if (T == 0) return MOE_OK;
   CHECK(save && save_scale && dact && (dgu || dq || dqt || dgate), MOE_ERR_INVALID_ARG);
   CHECK(aligned(save, 8) && aligned(dact, 16) && aligned(dgu, 16) && aligned(dq, 16) && aligned(dqt, 16) && aligned(actt, 16),
@@ -355,7 +356,7 @@ moe_status moe_requant_cols(moe_ops ops, const void* q, const float* scale, int 
   CHECK(ops && T >= 0 && C >= 1 && src_rows >= 0, MOE_ERR_INVALID_ARG);
   CHECK(G >= 1 && G <= kMaxSegs && (off || G == 1), MOE_ERR_INVALID_ARG);
   CHECK(row_index || src_rows >= T, MOE_ERR_INVALID_ARG);
-  CHECK(T <= (1 << 22) && C % 8 == 0, MOE_ERR_UNSUPPORTED);
+  CHECK(T <= (1 << 22) && C % 8 == 0 && C < (1 << 28), MOE_ERR_UNSUPPORTED);
   if (T == 0) return MOE_OK;
   CHECK(q && scale && qt && scale_t, MOE_ERR_INVALID_ARG);
   CHECK(aligned(q, 8) && aligned(qt, 16) && aligned(scale_t, 16), MOE_ERR_UNSUPPORTED);

@@ -311,7 +311,8 @@ SWF = dict(ops=P, gu=P, ld=256, T=4, f=128, act=P, q=P, scale=P, save=P, save_sc
     (dict(ld=260), UNSUP), (dict(gu=None), ARG), (dict(q=None), ARG), (dict(scale=None), ARG), (dict(save=None), ARG),
     (dict(save_scale=None), ARG), (dict(act=None, q=None, scale=None, save=None, save_scale=None), ARG),
     (dict(gu=P + 8), UNSUP), (dict(act=P + 8), UNSUP), (dict(q=P + 4), UNSUP), (dict(save=P + 4), UNSUP),
-    (dict(T=(1 << 31) - 1, f=256, ld=512), UNSUP),
+    (dict(T=(1 << 31) - 1, f=256, ld=512), UNSUP), (dict(T=1, f=1 << 28, ld=1 << 29), UNSUP),
+    (dict(T=1, f=(1 << 31) - 8, ld=1 << 32), UNSUP),
 ])
 def test_swiglu_forward_refuses(lib, over, code):
     assert call(lib, "moe_swiglu_forward", SWF, over) == code
@@ -329,6 +330,7 @@ NONE = dict(dgu=None, dq=None, dq_scale=None, dqt=None, dqt_scale=None, actt=Non
     (dict(f=136, ld=136), UNSUP), (dict(T=(1 << 22) + 1), UNSUP), (dict(save=None), ARG), (dict(save_scale=None), ARG),
     (dict(dact=None), ARG), (dict(dact=P + 8), UNSUP), (dict(save=P + 4), UNSUP), (dict(dqt=P + 8), UNSUP),
     (dict(dgu=P + 8), UNSUP), (dict(workspace=None), WS), (dict(workspace=P + 8), WS),
+    (dict(T=1, f=(1 << 31) - 128, ld=1 << 32), UNSUP),
 ])
 def test_swiglu_backward_refuses(lib, over, code):
     assert call(lib, "moe_swiglu_backward", SWB, over) == code
@@ -340,6 +342,7 @@ def test_swiglu_backward_refuses(lib, over, code):
     ((P, None, P, 4, 4, 64, None, 1, None, P, P, None), ARG), ((P, P, P, 4, 4, 64, None, 1, None, P, None, None), ARG),
     ((P, P + 4, P, 4, 4, 64, None, 1, None, P, P, None), UNSUP), ((P, P, P, 4, 4, 64, None, 1, None, P + 8, P, None), UNSUP),
     ((P, P, P, 4, 4, 64, None, 1, None, P, P + 4, None), UNSUP), ((P, P, P, 4, -1, 64, None, 1, None, P, P, None), ARG),
+    ((P, P, P, 1, 1, (1 << 31) - 8, None, 1, None, P, P, None), UNSUP),
 ])
 def test_requant_cols_refuses(lib, args, code):
     assert lib.moe_requant_cols(*args) == code
@@ -352,6 +355,7 @@ def test_swiglu_of_no_rows_does_nothing(lib):
     assert lib.moe_requant_cols(P, None, None, 0, 0, 64, None, 1, None, None, None, None) == OK
     assert lib.moe_swiglu_workspace_size(10, 136, ctypes.byref(n)) == OK and n.value == 4 * 10 * 2
     assert lib.moe_swiglu_workspace_size(10, 136, None) == ARG
+    assert lib.moe_swiglu_workspace_size(1, (1 << 31) - 8, ctypes.byref(n)) == UNSUP
 
 
 def test_swiglu_gradient_against_differences():
