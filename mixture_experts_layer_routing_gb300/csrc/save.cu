@@ -5,6 +5,7 @@
 #include "fp8_quant.cuh"
 #include "launch.cuh"
 #include "segs.cuh"
+#include "tc_ptx.cuh"
 
 namespace moe {
 namespace {
@@ -255,6 +256,17 @@ __device__ __forceinline__ void column_codes(const BwdTile& tile, const float4* 
   }
 }
 
+// Copies to shared memory; nothing is read where `there` is not set, and zeros are written.
+__device__ __forceinline__ void cp16_or_zeros(void* dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp8_or_zeros(void* dst, const void* src, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 8 : 0) : "memory");
+}
+__device__ __forceinline__ void cp4_or_zeros(void* dst, const void* src, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 4 : 0) : "memory");
+}
+
 // CTA per 128 tokens of a segment and 128 columns of f. Rows first: eight lanes a row, 16 columns each, whose maxima by
 // rows are shuffles and by columns stay in registers until the last row. Then (COLS) columns: a warp takes 16 tokens, a
 // lane four neighbouring columns, and the values are computed again from the tile in shared memory, which costs less than
@@ -282,6 +294,31 @@ __global__ void __launch_bounds__(256, 2) swiglu_bwd_kernel(SaveBwdParams P) {
 #pragma unroll
     for (int j = 0; j < 16; ++j) cm[0][j] = cm[COLS ? 1 : 0][j] = cm[COLS ? 2 : 0][j] = 0.f;
   }
+  // the whole tile is on its way before the first row is looked at
+  if (COLS) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int lr = i * 32 + (tid >> 3);
+      const bool in = row0 + lr < row1;
+      const long long row = in ? row0 + lr : row0;
+      const bf16* p = P.dact + row * P.ld + (one ? c : 0);
+      cp16_or_zeros(&tile.d[lr][(tid & 7) * 4], p, in && one);
+      cp16_or_zeros(&tile.d[lr][(tid & 7) * 4 + 2], two ? p + 8 : p, in && two);
+      const uint8_t* g = P.save + row * 2 * P.f + (one ? c : 0);
+      cp8_or_zeros(&tile.g[lr][(tid & 7) * 4], g, in && one);
+      cp8_or_zeros(&tile.g[lr][(tid & 7) * 4 + 2], two ? g + 8 : g, in && two);
+      cp8_or_zeros(&tile.u[lr][(tid & 7) * 4], g + P.f, in && one);
+      cp8_or_zeros(&tile.u[lr][(tid & 7) * 4 + 2], two ? g + P.f + 8 : g, in && two);
+      const float* z = P.save_scale + row * 2 * P.nb + b;
+      if ((tid & 7) == 0) cp4_or_zeros(&row_of[lr].x, z, in);
+      if ((tid & 7) == 1) cp4_or_zeros(&row_of[lr].y, z + P.nb, in);
+      if ((tid & 7) == 2) {
+        if (P.gate) cp4_or_zeros(&row_of[lr].z, P.gate + row, in);
+        else row_of[lr].z = 1.f;
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+  }
 #pragma unroll 1
   for (int i = 0; i < 4; ++i) {
     if (row0 + i * 32 >= row1) break;      // (a segment's last tile)
@@ -290,7 +327,19 @@ __global__ void __launch_bounds__(256, 2) swiglu_bwd_kernel(SaveBwdParams P) {
     const bool in = row < row1;
     uint4 d[2] = {}, g = {}, u = {};
     float zg = 0.f, zu = 0.f, gate = 1.f;
-    if (in) {
+    if (COLS) {              // a thread reads what it copied, and its eight lanes' scales
+      if (i == 0) asm volatile("cp.async.wait_group 3;" ::: "memory");
+      else if (i == 1) asm volatile("cp.async.wait_group 2;" ::: "memory");
+      else if (i == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+      else asm volatile("cp.async.wait_group 0;" ::: "memory");
+      __syncwarp();
+      d[0] = reinterpret_cast<const uint4*>(tile.d[lr])[(tid & 7) * 2];
+      d[1] = reinterpret_cast<const uint4*>(tile.d[lr])[(tid & 7) * 2 + 1];
+      g = reinterpret_cast<const uint4*>(tile.g[lr])[tid & 7];
+      u = reinterpret_cast<const uint4*>(tile.u[lr])[tid & 7];
+      const float4 z = row_of[lr];
+      zg = z.x, zu = z.y, gate = z.z;
+    } else if (in) {
       const bf16* p = P.dact + row * P.ld + c;
       if (one) d[0] = *reinterpret_cast<const uint4*>(p);
       if (two) d[1] = *reinterpret_cast<const uint4*>(p + 8);
@@ -299,13 +348,6 @@ __global__ void __launch_bounds__(256, 2) swiglu_bwd_kernel(SaveBwdParams P) {
       zg = P.save_scale[row * 2 * P.nb + b];
       zu = P.save_scale[row * 2 * P.nb + P.nb + b];
       if (P.gate) gate = P.gate[row];
-    }
-    if (COLS) {
-      reinterpret_cast<uint4*>(tile.d[lr])[(tid & 7) * 2] = d[0];
-      reinterpret_cast<uint4*>(tile.d[lr])[(tid & 7) * 2 + 1] = d[1];
-      reinterpret_cast<uint4*>(tile.g[lr])[tid & 7] = g;
-      reinterpret_cast<uint4*>(tile.u[lr])[tid & 7] = u;
-      if ((tid & 7) == 0) row_of[lr] = make_float4(zg, zu, gate, 0.f);
     }
     const uint32_t wd[8] = {d[0].x, d[0].y, d[0].z, d[0].w, d[1].x, d[1].y, d[1].z, d[1].w};
     const uint32_t wg[4] = {g.x, g.y, g.z, g.w}, wu[4] = {u.x, u.y, u.z, u.w};
@@ -379,6 +421,7 @@ __global__ void __launch_bounds__(256, 2) swiglu_bwd_kernel(SaveBwdParams P) {
     }
   }
   if (!COLS) return;
+  asm volatile("cp.async.wait_group 0;" ::: "memory");     // (rows behind the segment's end: the codes go where they are)
 #pragma unroll
   for (int k = 0; k < 3; ++k)
 #pragma unroll
