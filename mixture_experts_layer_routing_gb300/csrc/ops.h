@@ -58,6 +58,7 @@ cudaError_t fp8_wgrad(const moe_ops_s* o, const void* dct, const float* sdct, co
 
 cudaError_t swiglu_forward(const moe_ops_s* o, const void* gu, long long ld, int T, int f, void* act, void* q,
                            float* scale, void* save, float* save_scale, cudaStream_t s, long long* n);
+size_t swiglu_workspace(int T, int f);
 cudaError_t swiglu_backward(const moe_ops_s* o, const void* save, const float* save_scale, const void* dact, long long ld,
                             const float* gate, int T, int f, const int* off, int G, void* dgu, void* dq, float* dq_scale,
                             void* dqt, float* dqt_scale, void* actt, float* actt_scale, float* dgate, float* ws,

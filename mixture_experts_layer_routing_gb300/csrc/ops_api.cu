@@ -327,7 +327,7 @@ moe_status moe_swiglu_forward(moe_ops ops, const void* gu, long long ld, int T, 
 moe_status moe_swiglu_workspace_size(int T, int f, size_t* bytes) {
   CHECK(T >= 0 && f >= 1 && bytes, MOE_ERR_INVALID_ARG);
   CHECK(f < (1 << 28), MOE_ERR_UNSUPPORTED);
-  *bytes = sizeof(float) * (size_t)T * ceil_div(f, kScaleBlock);
+  *bytes = swiglu_workspace(T, f);
   return MOE_OK;
 }
 
@@ -344,7 +344,7 @@ moe_status moe_swiglu_backward(moe_ops ops, const void* save, const float* save_
   CHECK(save && save_scale && dact && (dgu || dq || dqt || dgate), MOE_ERR_INVALID_ARG);
   CHECK(aligned(save, 8) && aligned(dact, 16) && aligned(dgu, 16) && aligned(dq, 16) && aligned(dqt, 16) && aligned(actt, 16),
         MOE_ERR_UNSUPPORTED);
-  CHECK(!dgate || (workspace && aligned(workspace, 16)), MOE_ERR_WORKSPACE);
+  CHECK(!dgate || swiglu_workspace(T, f) == 0 || (workspace && aligned(workspace, 16)), MOE_ERR_WORKSPACE);
   HANDLE(ops);
   DONE(swiglu_backward(ops, save, save_scale, dact, ld, gate, T, f, off, G, dgu, dq, dq_scale, dqt, dqt_scale, actt,
                        actt_scale, dgate, (float*)workspace, (cudaStream_t)stream, &n_));

@@ -483,8 +483,10 @@ PyObject* swiglu_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
       size_t bytes = 0;
       st = moe_swiglu_workspace_size((int)T, to_int(f, "dact"), &bytes);
       if (st != MOE_OK) return st;
-      ws = at::empty({(int64_t)bytes}, a.opts.dtype(at::kByte));
-      scratch = ws.data_ptr();
+      if (bytes) {
+        ws = at::empty({(int64_t)bytes}, a.opts.dtype(at::kByte));
+        scratch = ws.data_ptr();
+      }
     }
     return moe_swiglu_backward(a.ops, save, (const float*)ss, d.data_ptr(), ld, (const float*)gate, (int)T,
                                to_int(f, "dact"), (const int32_t*)address(a, 7, "off"), G, dgu, dq, (float*)dqs, dqt,

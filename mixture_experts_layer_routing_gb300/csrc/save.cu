@@ -183,7 +183,10 @@ struct Divisor4 {
   float m[4];
   uint64_t r0, r1, n0, n1;
   bool plain;
-  __device__ __forceinline__ explicit Divisor4(const float4& v) : m{v.x, v.y, v.z, v.w} {
+  // (not `there`: columns behind the last one, whose codes nobody reads, need no division; taken as columns of zeros they
+  // brought it to the whole warp, 301 x 392 by columns 26 us instead of 13)
+  __device__ __forceinline__ Divisor4(const float4& v, bool there)
+      : m{there ? v.x : 1.f, there ? v.y : 1.f, there ? v.z : 1.f, there ? v.w : 1.f} {
     const Divisor a(m[0]), b(m[1]), c(m[2]), d(m[3]);
     plain = a.plain && b.plain && c.plain && d.plain;
     r0 = f32x2(a.r, b.r), r1 = f32x2(c.r, d.r), n0 = f32x2(-m[0], -m[1]), n1 = f32x2(-m[2], -m[3]);
@@ -215,11 +218,18 @@ struct SaveBwdParams {
   float* dq_scale;
   uint8_t *dqt, *actt;
   float *dqt_scale, *actt_scale;
-  float* part;             // [nb][T]: the gates' gradient by column blocks
+  float* dgate;            // written here by a cluster of all column blocks,
+  float* part;             // else [nb][T]: by column blocks, for sum_parts_kernel
   long long Tp;
   int* status;
 };
 
+// The gates' gradient is added up by clusters of all column blocks (8 CTAs at most) where tiles are few: a launch
+// less (301 x 392 with bf16 outputs 3.7 us a call among others instead of 6.3, in a graph 3.4 and 3.5, 512 x 1024 4.0 and
+// 3.7). With more tiles the CTAs of a cluster wait for one another: 1024 x 1024 8.0 us instead of 7.1, 12,288 x 1024 34.6
+// instead of 29.0.
+constexpr int kClusterBlocks = 8, kClusterTiles = 32;
+inline bool clustered(int T, int nb) { return nb <= kClusterBlocks && ceil_div(T, kScaleBlock) * nb <= kClusterTiles; }
 constexpr int kOutPitch = 144;     // bytes of a column's 128 codes, 16 apart in the banks
 
 // The tile in shared memory that the columns are computed from. Their codes are put where it was.
@@ -275,6 +285,7 @@ template <bool COLS>
 __global__ void __launch_bounds__(256, 2) swiglu_bwd_kernel(SaveBwdParams P) {
   __shared__ SegSmem seg;
   __shared__ float4 row_of[128];          // scales of g and u, gate
+  __shared__ float dots[128];             // act dact of this column block
   extern __shared__ __align__(16) uint8_t smem[];
   BwdTile& tile = *reinterpret_cast<BwdTile*>(smem);
   uint8_t(*out)[128][kOutPitch] = reinterpret_cast<uint8_t(*)[128][kOutPitch]>(smem);       // dg, du, act
@@ -412,14 +423,32 @@ __global__ void __launch_bounds__(256, 2) swiglu_bwd_kernel(SaveBwdParams P) {
         }
       }
     }
-    if (P.part) {
+    if (P.part || P.dgate) {
       float x, y;
       f32x2_get(dot2, x, y);
       float dot = x + y;
 #pragma unroll
       for (int o = 4; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-      if (in && (tid & 7) == 0) P.part[(long long)b * P.T + row] = dot;
+      if (in && (tid & 7) == 0) {
+        if (P.dgate) dots[lr] = dot;
+        else P.part[(long long)b * P.T + row] = dot;
+      }
     }
+  }
+  if (P.dgate) {             // column blocks in their order
+    cluster_sync();
+    const int lr = i0 * 32 + tid;
+    if (b == 0 && tid < each * 32 && row0 + lr < row1) {
+      const uint32_t at = smem_u32(&dots[lr]);
+      float v = 0.f;
+      for (int r = 0; r < P.nb; ++r) {
+        float x;
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(mapa_shared(at, r)) : "memory");
+        v += x;
+      }
+      P.dgate[row0 + lr] = v;
+    }
+    cluster_sync();          // (a CTA's sums are read until here)
   }
   if (!COLS) return;
   asm volatile("cp.async.wait_group 0;" ::: "memory");     // (rows behind the segment's end: the codes go where they are)
@@ -452,9 +481,10 @@ __global__ void __launch_bounds__(256, 2) swiglu_bwd_kernel(SaveBwdParams P) {
     }
   }
   __syncthreads();
-  const Divisor4 div[3] = {Divisor4(*reinterpret_cast<const float4*>(&red[0][0][lane * 4])),
-                           Divisor4(*reinterpret_cast<const float4*>(&red[0][1][lane * 4])),
-                           Divisor4(*reinterpret_cast<const float4*>(&red[0][2][lane * 4]))};
+  const bool there = b * kScaleBlock + lane * 4 < P.f;
+  const Divisor4 div[3] = {Divisor4(*reinterpret_cast<const float4*>(&red[0][0][lane * 4]), there),
+                           Divisor4(*reinterpret_cast<const float4*>(&red[0][1][lane * 4]), there),
+                           Divisor4(*reinterpret_cast<const float4*>(&red[0][2][lane * 4]), there)};
   uint32_t w[3][4][4] = {};
   if (row0 + warp * 16 < row1) {
     if (div[0].plain && div[1].plain && div[2].plain) column_codes<true>(tile, row_of, div, warp, lane, w);
@@ -557,7 +587,7 @@ __global__ void __launch_bounds__(256, 4) requant_cols_kernel(const uint8_t* __r
     const float4 v = red[i][lane];
     m.x = max_nan(m.x, v.x), m.y = max_nan(m.y, v.y), m.z = max_nan(m.z, v.z), m.w = max_nan(m.w, v.w);
   }
-  const Divisor4 div(m);
+  const Divisor4 div(m, c < C);
   const auto codes_to = [&](auto plain) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -594,7 +624,31 @@ __global__ void __launch_bounds__(256, 4) requant_cols_kernel(const uint8_t* __r
   }
 }
 
+// launch_pdl with clusters of `cluster` CTAs along x.
+cudaError_t launch_cluster(void (*kern)(SaveBwdParams), dim3 grid, unsigned cluster, size_t smem, cudaStream_t s,
+                           const SaveBwdParams& P) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, P);
+}
+
 }  // namespace
+
+size_t swiglu_workspace(int T, int f) {
+  const int nb = ceil_div(f, kScaleBlock);
+  return clustered(T, nb) ? 0 : sizeof(float) * (size_t)T * nb;
+}
 
 cudaError_t swiglu_forward(const moe_ops_s*, const void* gu, long long ld, int T, int f, void* act, void* q, float* scale,
                            void* save, float* save_scale, cudaStream_t s, long long* n) {
@@ -610,23 +664,25 @@ cudaError_t swiglu_backward(const moe_ops_s* o, const void* save, const float* s
                             void* dqt, float* dqt_scale, void* actt, float* actt_scale, float* dgate, float* ws,
                             cudaStream_t s, long long* n) {
   const int nb = ceil_div(f, kScaleBlock), Tp = quant_cols_rows(T, G);
+  const bool joined = dgate && clustered(T, nb);
+  const unsigned cluster = joined ? nb : 1;
   const SaveBwdParams P = {(const uint8_t*)save, save_scale, (const bf16*)dact, ld, gate, off, G, T, f, nb, (bf16*)dgu,
                            (uint8_t*)dq, dq_scale, (uint8_t*)dqt, (uint8_t*)actt, dqt_scale, actt_scale,
-                           dgate ? ws : nullptr, Tp, o->status};
+                           joined ? dgate : nullptr, dgate && !joined ? ws : nullptr, Tp, o->status};
   const dim3 grid(nb, Tp / kScaleBlock);
   *n += 1;
   if (dqt) {
     constexpr int smem = sizeof(BwdTile) + 16 * 3 * 128 * sizeof(float);
     MOE_TRY(cudaFuncSetAttribute(swiglu_bwd_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-    MOE_TRY(launch_pdl(swiglu_bwd_kernel<true>, grid, dim3(256), smem, s, P));
+    MOE_TRY(launch_cluster(swiglu_bwd_kernel<true>, grid, cluster, smem, s, P));
   } else {
     // Without columns a tile's rows may go to four CTAs: where tiles are no more than the CTAs that run at once (with the
     // gates' gradient 301 x 392 take 3.4 us instead of 6.1, 1024 x 2048 of 8 segments 9.5 and 9.7, 2048 x 2048 of them,
     // 384 tiles, 13.5 instead of 11.3).
     const bool split = (long long)grid.x * grid.y <= 2ll * o->sms;
-    MOE_TRY(launch_pdl(swiglu_bwd_kernel<false>, dim3(grid.x, grid.y, split ? 4 : 1), dim3(256), 0, s, P));
+    MOE_TRY(launch_cluster(swiglu_bwd_kernel<false>, dim3(grid.x, grid.y, split ? 4 : 1), cluster, 0, s, P));
   }
-  if (!dgate) return cudaSuccess;
+  if (!P.part) return cudaSuccess;
   *n += 1;
   return launch_pdl(sum_parts_kernel, dim3(ceil_div(T, 256)), dim3(256), 0, s, ws, nb, T, off, G, dgate, o->status);
 }

@@ -96,7 +96,8 @@ def backward_inputs(T, f, seed, gate=True):
 
 
 @pytest.mark.parametrize("T,f,cnt", [(1, 8, None), (5, 136, None), (128, 128, None), (129, 392, None), (300, 256, None),
-                                     (300, 200, [0, 1, 127, 128, 0, 44, 0]), (257, 384, [129, 0, 128]), (77, 128, [0, 0, 77])])
+                                     (300, 200, [0, 1, 127, 128, 0, 44, 0]), (257, 384, [129, 0, 128]), (77, 128, [0, 0, 77]),
+                                     (140, 1024, [70, 0, 70]), (140, 1032, [70, 0, 70]), (600, 904, [1, 0, 599]), (40, 1408, None)])
 @pytest.mark.parametrize("gated", [True, False])
 def test_swiglu_backward(ops, T, f, cnt, gated):
     gu, dact, gate = backward_inputs(T, f, T + f, gated)

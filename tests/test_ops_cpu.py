@@ -329,7 +329,7 @@ NONE = dict(dgu=None, dq=None, dq_scale=None, dqt=None, dqt_scale=None, actt=Non
     (dict(actt=None, actt_scale=None), ARG), (NONE, ARG), (dict(f=124), UNSUP), (dict(ld=132), UNSUP),
     (dict(f=136, ld=136), UNSUP), (dict(T=(1 << 22) + 1), UNSUP), (dict(save=None), ARG), (dict(save_scale=None), ARG),
     (dict(dact=None), ARG), (dict(dact=P + 8), UNSUP), (dict(save=P + 4), UNSUP), (dict(dqt=P + 8), UNSUP),
-    (dict(dgu=P + 8), UNSUP), (dict(workspace=None), WS), (dict(workspace=P + 8), WS),
+    (dict(dgu=P + 8), UNSUP), (dict(f=1152, ld=1152, workspace=None), WS), (dict(f=1152, ld=1152, workspace=P + 8), WS),
     (dict(T=1, f=(1 << 31) - 128, ld=1 << 32), UNSUP),
 ])
 def test_swiglu_backward_refuses(lib, over, code):
@@ -353,7 +353,9 @@ def test_swiglu_of_no_rows_does_nothing(lib):
     assert call(lib, "moe_swiglu_forward", SWF, dict(T=0, gu=None, act=None, q=None, scale=None)) == OK
     assert call(lib, "moe_swiglu_backward", SWB, {**NONE, "T": 0, "save": None}) == OK
     assert lib.moe_requant_cols(P, None, None, 0, 0, 64, None, 1, None, None, None, None) == OK
-    assert lib.moe_swiglu_workspace_size(10, 136, ctypes.byref(n)) == OK and n.value == 4 * 10 * 2
+    assert lib.moe_swiglu_workspace_size(10, 1032, ctypes.byref(n)) == OK and n.value == 4 * 10 * 9
+    assert lib.moe_swiglu_workspace_size(10, 1024, ctypes.byref(n)) == OK and n.value == 0
+    assert lib.moe_swiglu_workspace_size(513, 1024, ctypes.byref(n)) == OK and n.value == 4 * 513 * 8
     assert lib.moe_swiglu_workspace_size(10, 136, None) == ARG
     assert lib.moe_swiglu_workspace_size(1, (1 << 31) - 8, ctypes.byref(n)) == UNSUP
 
