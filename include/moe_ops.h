@@ -192,8 +192,8 @@ typedef struct {
  *   scale = bf16(m / 7)              code = clamp(rint(w / scale) + 8)
  * with zero, lo and hi being the smallest and the largest of a group's values and 0:
  *   scale = bf16((hi - lo) / 15)     zero = clamp(rint(-lo / scale))     code = clamp(rint(w / scale) + zero)
- * clamped to 0..15, quotients in fp32. A group of zeros has scale 0 and reads zeros; one that holds a NaN or an
- * infinity reads NaN. */
+ * clamped to 0..15, quotients in fp32 (that of a span hi - lo beyond fp32's largest value too). A group of zeros has
+ * scale 0 and reads zeros; one that holds a NaN or an infinity reads NaN, any other one finite values. */
 moe_status moe_quant_w4(moe_ops ops, const void* w, int G, int N, int K, int group, uint32_t* codes, void* scale,
                         uint8_t* zero, void* stream);
 /* c[m, n] = sum over K of x[r(m), k] w[g(m), n, k], r(m) = row_index[m] or m: x [x_rows, K] bf16, rows ld_x elements

@@ -166,7 +166,11 @@ __global__ void __launch_bounds__(256) quant_w4_kernel(const bf16* __restrict__ 
     asm("max.NaN.f32 %0, %0, %1;" : "+f"(hi) : "f"(h));
     asm("min.NaN.f32 %0, %0, %1;" : "+f"(lo) : "f"(m));
   }
-  const bf16 sb = __float2bfloat16_rn(ZERO ? __fdiv_rn(hi - lo, 15.f) : __fdiv_rn(hi, 7.f));
+  // (finite values may span more than fp32 holds: half the span over half of 15 is the same quotient)
+  const float span = hi - lo;
+  const bf16 sb = __float2bfloat16_rn(!ZERO                 ? __fdiv_rn(hi, 7.f)
+                                      : span > 3.4028235e38f ? __fdiv_rn(0.5f * hi - 0.5f * lo, 7.5f)
+                                                             : __fdiv_rn(span, 15.f));
   const float s = __bfloat162float(sb);
   const bool plain = s > 0.f && s <= 3.3895314e38f;     // (else all codes are the zero point: 0, or NaN, times the scale)
   const float z = !ZERO ? 8.f : plain ? fminf(fmaxf(rintf(__fdiv_rn(-lo, s)), 0.f), 15.f) : 0.f;

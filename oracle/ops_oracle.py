@@ -190,7 +190,9 @@ def quant_w4(w, group, with_zero):
         for i in range(KG):
             v = w[:, i * group:(i + 1) * group]
             lo, hi = np.minimum(v.min(1), 0), np.maximum(v.max(1), 0)
-            s = bf16((hi - lo) / np.float32(15) if with_zero else np.abs(v).max(1) / np.float32(7)).astype(np.float32)
+            # (half the span where the whole one is beyond fp32)
+            span = np.where(np.isinf(hi - lo), (hi * np.float32(0.5) - lo * np.float32(0.5)) / np.float32(7.5), (hi - lo) / np.float32(15))
+            s = bf16(span if with_zero else np.abs(v).max(1) / np.float32(7)).astype(np.float32)
             live = (s > 0) & np.isfinite(s)
             z = np.clip(np.rint(-lo / s), 0, 15) if with_zero else np.full(N, 8.0, np.float32)
             z = np.where(live, z, 0.0 if with_zero else 8.0)
