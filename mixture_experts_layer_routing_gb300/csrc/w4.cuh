@@ -145,6 +145,7 @@ template <int MT, int XR, int GROUP, bool ZERO> struct W4Core {
   int every;               // chunks from one to the next
   // x
   uint4 x[XR];             // the next chunk
+  int rows;                // of x that hold it
   unsigned xoff[XR];       // its rows, in units of 16 bytes
   unsigned wx, rx;         // offsets that this lane writes to and reads from
 
@@ -166,10 +167,16 @@ template <int MT, int XR, int GROUP, bool ZERO> struct W4Core {
     wx = kX + (lane >> 4) * (XR * 256) + p * 16;
     rx = kX + (quad & (XR - 1)) * 256 + (quad & 1) * 64 + t * 16;      // (columns from XR on repeat others, unused)
     slot = 0;
-    // rows are stored only after they were read, but by two counts that the compiler cannot relate: without values here it
-    // may let a row that a tile in front did not have keep what the register held
+    // No register of this state is without a value. Without the zeros in x the layer's fp32 form gave wrong sums wherever a
+    // warp's first tile has fewer rows than a later one, also with the rows' count carried beside them, while starting
+    // values of 1 and of NaN give the right ones: no result reads them, but code made for undefined registers was wrong.
+    rows = k_left = g_left = 0;
+    row4 = 0ull;
+    ps = pz = nullptr;
 #pragma unroll
-    for (int i = 0; i < XR; ++i) x[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = 0; i < MT; ++i) pa[i] = nullptr, row8[i] = 0ull;
+#pragma unroll
+    for (int i = 0; i < XR; ++i) x[i] = make_uint4(0u, 0u, 0u, 0u), xoff[i] = 0u;
   }
   // From chunk c on of rows row0[i] .. +8 and up0[i] .. +8 (i = 0 .. MT) of the matrix w, as far as they are below `end`
   // (a multiple of 8, above row0[0]); others repeat some and get scales of zero.
@@ -231,6 +238,7 @@ template <int MT, int XR, int GROUP, bool ZERO> struct W4Core {
     const int k = c * kChunk + lane * 8;
     const uint8_t* p = reinterpret_cast<const uint8_t*>(x0 + k);
     const unsigned in = k < K ? there : 0u;
+    rows = n;
 #pragma unroll
     for (int r = 0; r < XR; ++r) {
       if (r > 0 && r >= n) break;
@@ -241,10 +249,10 @@ template <int MT, int XR, int GROUP, bool ZERO> struct W4Core {
     }
   }
   // and puts them where multiply() reads them; a __syncwarp before and after
-  __device__ __forceinline__ void store_x(int n) const {
+  __device__ __forceinline__ void store_x() const {
 #pragma unroll
     for (int r = 0; r < XR; ++r) {
-      if (r > 0 && r >= n) break;
+      if (r > 0 && r >= rows) break;
       *reinterpret_cast<uint4*>(ring + (wx ^ (r & 1) * 64) + r * 256) = x[r];
     }
   }

@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) w4_up_kernel(W4LayerParams P
       cp_wait<kStages - 2>();
       __syncwarp();
       issue(core.free_slot());
-      core.store_x(R);
+      core.store_x();
       read_x();
       __syncwarp();
       core.multiply(acc, P.d - c * kChunk, lane);
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) w4_down_kernel(W4LayerParams
       cp_wait<kStages - 2>();
       __syncwarp();
       issue(core.free_slot());
-      core.store_x(kRows * R);
+      core.store_x();
       read_h();
       __syncwarp();
       core.multiply(acc, P.f - c * kChunk, lane);

@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) w4_matmul_kernel(W4MatmulPar
       cp_wait<kStages - 2>();
       __syncwarp();
       issue(core.free_slot());
-      core.store_x(R);
+      core.store_x();
       read_x();
       __syncwarp();
       core.multiply(acc, P.s.K - c * kChunk, lane);

@@ -94,3 +94,70 @@ def test_finite_weights_read_finite(ops, group, zero):
     step = q["scale"].double().t().repeat_interleave(group, 1)
     assert bool(torch.isfinite(step).all())
     assert bool(((back - w.double()).abs() <= step * (0.5 + 15 * 2.0 ** -9 + (0.5 if zero else 0.0))).all())
+
+
+@pytest.mark.parametrize("N,K,group,zero", [(4008, 2080, 32, True), (12008, 1056, 128, False), (4008, 7200, 64, False),
+                                            (40008, 96, 32, False)])
+def test_segments_that_grow_and_shrink(ops, N, K, group, zero):
+    """A warp of these products meets tiles of one row, of eight and of none in between, in several chunks each."""
+    cnt = [1, 8, 0, 3, 17, 1, 1, 9, 0, 0, 25, 2, 7]
+    ends = [0] + list(np.cumsum(cnt))
+    g = gen(N)
+    w, x = weights(g, len(cnt), N, K, group, zero), rnd(g, 19, K)
+    index = torch.randint(0, 19, (ends[-1],), generator=g, device="cuda", dtype=torch.int32)
+    off = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    c = ops.w4_matmul(x, w, off=off, row_index=index, out_dtype=torch.float32)
+    a = x.double()[index.long()]
+    for e, (lo, hi) in enumerate(zip(ends[:-1], ends[1:])):
+        if hi > lo:
+            v = dense(w, e)
+            near(c[lo:hi], a[lo:hi] @ v.t(), a[lo:hi].abs() @ v.abs().t(), -(-K // group))
+    assert ops.status() == 0
+
+
+# ---------------------------------------------------------------- long layers
+
+def layer(ops, T, d, f, E, k, shared, group, zero, out, idx=None, seed=0):
+    """The layer against 64 bits. Its bound: the sums of both products, SwiGLU, h to 16 (fp32 outputs: 24) bits."""
+    g = gen(seed + T + d + f)
+    x, w13, wd = rnd(g, T, d), weights(g, E + shared, 2 * f, d, group, zero), weights(g, E + shared, d, f, group, zero)
+    if idx is None:
+        idx = torch.rand(T, E, generator=g, device="cuda").topk(k, 1).indices.to(torch.int32)
+    gate = torch.rand(T, k, generator=g, device="cuda") - 0.2
+    y = ops.w4_experts(x, idx, gate, w13, wd, n_shared=shared, out_dtype=out)
+    add = (30 + max(-(-d // group), (k + shared) * -(-f // group))) * 2.0 ** -23
+    kept = 2.0 ** -18 + 2.0 ** (-24 if out == torch.float32 else -16)
+    want, bound = torch.zeros(T, d, dtype=torch.float64, device="cuda"), torch.zeros(T, d, dtype=torch.float64, device="cuda")
+    per = torch.zeros(T, E, dtype=torch.float64, device="cuda")
+    per.scatter_add_(1, idx.long().clamp(0, E - 1), torch.where((idx >= 0) & (idx < E), gate, 0.0).double())
+    for e in range(E + shared):
+        t = (idx == e).any(1).nonzero().flatten() if e < E else torch.arange(T, device="cuda")
+        if t.numel() == 0:
+            continue
+        v, xe, ge = dense(w13, e), x[t].double(), per[t, e, None] if e < E else 1.0
+        (a, u), (sa, su) = (xe @ v.t()).chunk(2, 1), (xe.abs() @ v.abs().t()).chunk(2, 1)
+        s = a * torch.special.expit(a)
+        h = ge * s * u
+        off = (ge.abs() if e < E else 1.0) * add * (1.1 * u.abs() * sa + s.abs() * su) + kept * h.abs()
+        v = dense(wd, e)
+        want.index_add_(0, t, h @ v.t())
+        bound.index_add_(0, t, (off + add * h.abs()) @ v.abs().t())
+    err = (y.double() - want).abs()
+    tol = bound + HALF[out] * (want.abs() + bound)
+    assert bool((err <= tol).all()), (err - tol).max().item()
+    return (y.double() - want).norm() / want.norm()
+
+
+@pytest.mark.parametrize("rows", [2, 3, 8, 16, 17, 64])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+def test_layers_whose_tiles_grow_and_shrink(ops, rows, out):
+    """One, then all, then a few tokens an expert, over and over, in several units a CTA and several chunks a warp: a
+    warp of either kernel meets tiles with more rows than the one in front, and with fewer."""
+    E, k = 60, 8
+    idx = torch.full((rows, k), -1, dtype=torch.int32)
+    idx[:, 0], idx[:, 1], idx[:, 2] = 1, 30, 58
+    for t in range(rows):
+        idx[t, 3:] = torch.tensor([2 + (5 * t + j) % 28 if j < 3 else 31 + (3 * t + j) % 27 for j in range(5)])
+    layer(ops, rows, 4128, 1056, E, k, 0, 32, False, out, idx=idx.cuda())
+    layer(ops, rows, 7200, 288, E, k, 1, 128, True, out, idx=idx.cuda(), seed=3)
+    assert ops.status() == 0
