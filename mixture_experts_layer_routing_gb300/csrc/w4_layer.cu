@@ -143,7 +143,9 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) w4_up_kernel(W4LayerParams P
           g += from[w * kSums + at];
           up += from[w * kSums + at + 8];
         }
-        const float h = silu_f(g) * up * gate;
+        // (The full exponential and quotient, with no difference in time: the fast ones were off by 14 units of 2^-23 where
+        // |g| is 40, these by 4 at most.)
+        const float h = g / (1.f + expf(-g)) * up * gate;
         // h as a sum of bf16 values, two (16 bits of mantissa) or for fp32 outputs three (24), so that the layer rounds
         // once, at its output. (Two for fp32 outputs were off by up to 3.2e-6 of y's norm, three are by 2.1e-7; 16 tokens
         // of 32 experts, d = 7168, take 273 us instead of 212, one token 49 instead of 47.)

@@ -161,3 +161,31 @@ def test_layers_whose_tiles_grow_and_shrink(ops, rows, out):
     layer(ops, rows, 4128, 1056, E, k, 0, 32, False, out, idx=idx.cuda())
     layer(ops, rows, 7200, 288, E, k, 1, 128, True, out, idx=idx.cuda(), seed=3)
     assert ops.status() == 0
+
+
+# ---------------------------------------------------- h's precision, fp32 outputs
+
+def one_code(n, N, K, at):
+    """Matrices of which row r holds one 1 (code 9, scale 1), at column at[r]."""
+    codes = torch.full((n, N, K), 8, dtype=torch.int64)
+    codes[:, torch.arange(N), at] = 9
+    words = torch.from_numpy(oo.w4_pack(codes.numpy())).cuda()
+    return dict(codes=words, scale=torch.ones(n, K // 32, N, dtype=torch.bfloat16, device="cuda"), group=32)
+
+
+@pytest.mark.parametrize("T", [1, 2, 16, 33])
+def test_fp32_outputs_carry_24_bits_of_h(ops, T):
+    """Each y is one h, and g and u are values of x, so that nothing but h's own rounding counts: the exponential (2^-23),
+    1 + e, the quotient and the products with u and with the gate (2^-24 each), h's three parts (2^-26) and their sum
+    (2^-24 twice): below 2^-23 + 7 * 2^-24 = 4.5 * 2^-23."""
+    d, f, E = 128, 64, 3
+    g = gen(T)
+    x = (torch.rand(T, d, generator=g, device="cuda") * 80 - 40).to(torch.bfloat16)
+    w13, wd = one_code(E, 2 * f, d, torch.arange(2 * f)), one_code(E, d, f, torch.arange(d) % f)
+    idx = torch.randint(0, E, (T, 1), generator=g, device="cuda", dtype=torch.int32)
+    gate = torch.rand(T, 1, generator=g, device="cuda") + 0.5
+    y = ops.w4_experts(x, idx, gate, w13, wd, out_dtype=torch.float32).double()
+    a, u = x.double().chunk(2, 1)
+    want = (a * torch.special.expit(a) * u * gate.double()).repeat(1, 2)
+    off = ((y - want).abs() / want.abs()).max().item()
+    assert off <= 4.5 * 2.0 ** -23, off * 2 ** 23
