@@ -147,15 +147,18 @@ moe_status moe_fp8_wgrad(moe_ops ops, const void* dct, const float* dct_scale, c
                          int T, const int32_t* off, int G, int N, int K, void* c, int out_dtype, void* stream);
 
 /* ---- SwiGLU with an 8-bit checkpoint: gu = (g, u) halves of a row, act = silu(g) * u.
- * gu [T, 2f] bf16, rows ld elements apart; f (below 2^28) and ld multiples of 8, gu and act 16-byte aligned. Outputs (one at least): act [T, f]
- * bf16; q [T, f] with scale [T, ceil(f/128)], act's codes (of the unrounded values, as moe_quant_rows with swiglu); save
- * [T, 2f] with save_scale [T, 2 ceil(f/128)], the codes of g and of u, blocks of 128 within each half, the gate's scales
- * first (what the backward pass reads; with f a multiple of 128 they are moe_quant_rows of gu). Codes 8-byte aligned. */
+ * gu [T, 2f] bf16, rows ld elements apart; f (below 2^28) and ld multiples of 8, gu and act 16-byte aligned. The
+ * exponential and the quotient are the fast ones: act is off by up to (5 + 1.2 |g|) 2^-23 of itself before it is rounded
+ * or quantised, and 0 where g is below -87.3. Outputs (one at least): act [T, f] bf16; q [T, f] with scale
+ * [T, ceil(f/128)], act's codes (of the unrounded values, as moe_quant_rows with swiglu); save [T, 2f] with save_scale
+ * [T, 2 ceil(f/128)], the codes of g and of u, blocks of 128 within each half, the gate's scales first (what the
+ * backward pass reads; with f a multiple of 128 they are moe_quant_rows of gu). Codes 8-byte aligned. */
 moe_status moe_swiglu_forward(moe_ops ops, const void* gu, long long ld, int T, int f, void* act, void* q, float* scale,
                               void* save, float* save_scale, void* stream);
 /* With g, u the values of save, s = sigmoid(g), dact [T, f] bf16 the gradient of act (rows ld elements apart, a multiple
  * of 8, 16-byte aligned) and gate [T] fp32 a factor of each row (NULL: 1):
  *   dg = gate dact u s (1 + g (1 - s))     du = gate dact g s     dgate[t] = sum_f act dact     act' = gate act
+ * s is off by up to (4 + 0.7 |g|) 2^-23 of itself (0 where g is below -87.3), everything else is 32-bit arithmetic.
  * gate: where a row's product is weighted after the down product, out = sum gate (act Wd^T), dact is (dout Wd) without
  * the gate, dgate needs no output of that product, and dWd is act' along the tokens times dout.
  * Outputs, one at least, each pair both or neither, values quantised unrounded: dgu = (dg, du) [T, 2f] bf16; dq [T, 2f]
@@ -170,8 +173,8 @@ moe_status moe_swiglu_backward(moe_ops ops, const void* save, const float* save_
                                float* dq_scale, void* dqt, float* dqt_scale, void* actt, float* actt_scale,
                                float* dgate, void* workspace, void* stream);
 /* moe_quant_cols of rows that are held in 8 bits (q [src_rows, C], scale [src_rows, ceil(C/128)], as moe_quant_rows and
- * moe_norm_forward give them): the values code * scale, quantised along the tokens. C is a multiple of 8 below 2^28; q 8-byte aligned, qt
- * and scale_t 16-byte. */
+ * moe_norm_forward give them): the values code * scale, quantised along the tokens. C is a multiple of 8 below 2^28; q
+ * 8-byte aligned, qt and scale_t 16-byte. */
 moe_status moe_requant_cols(moe_ops ops, const void* q, const float* scale, int src_rows, int T, int C,
                             const int32_t* off, int G, const int32_t* row_index, void* qt, float* scale_t, void* stream);
 
@@ -193,7 +196,7 @@ typedef struct {
  * with zero, lo and hi being the smallest and the largest of a group's values and 0:
  *   scale = bf16((hi - lo) / 15)     zero = clamp(rint(-lo / scale))     code = clamp(rint(w / scale) + zero)
  * clamped to 0..15, quotients in fp32 (that of a span hi - lo beyond fp32's largest value too). A group of zeros has
- * scale 0 and reads zeros; one that holds a NaN or an infinity reads NaN, any other one finite values. */
+ * scale 0 and reads zeros; one that holds a NaN or an infinity reads NaN, no other one does. */
 moe_status moe_quant_w4(moe_ops ops, const void* w, int G, int N, int K, int group, uint32_t* codes, void* scale,
                         uint8_t* zero, void* stream);
 /* c[m, n] = sum over K of x[r(m), k] w[g(m), n, k], r(m) = row_index[m] or m: x [x_rows, K] bf16, rows ld_x elements
@@ -218,9 +221,10 @@ typedef struct {
  * x [T, d] bf16, rows ld_x elements apart (a multiple of 8, 16-byte aligned); idx [T, k], gate [T, k] fp32 as
  * moe_gate_forward gives them (an expert may be named twice by a token: its gates add up); w13 of [E+n_shared, 2f, d]
  * (gate half, up half), wd of [E+n_shared, d, f], with one group size and both with zero points or neither; y [T, d]
- * of out_dtype, 16-byte aligned. An index outside 0..E-1 is left out and records MOE_ERR_DEVICE_INDEX. h is kept to 16 bits of
- * mantissa (24 for fp32 outputs), the other sums in fp32; one rounding at the end. Only experts in use are read. workspace:
- * moe_w4_experts_workspace_size bytes, 16-byte aligned; calls that may run at once need one each. */
+ * of out_dtype, 16-byte aligned. An index outside 0..E-1 is left out and records MOE_ERR_DEVICE_INDEX. h, with the gate
+ * in it, is kept to 16 bits of mantissa (24 for fp32 outputs), the other sums in fp32; one rounding at the end. Only
+ * experts in use are read. workspace: moe_w4_experts_workspace_size bytes, 16-byte aligned; calls that may run at once
+ * need one each. */
 moe_status moe_w4_experts_workspace_size(const moe_w4_config* cfg, int T, size_t* bytes);
 moe_status moe_w4_experts(moe_ops ops, const moe_w4_config* cfg, const void* x, long long ld_x, int T,
                           const int32_t* idx, const float* gate, const moe_w4* w13, const moe_w4* wd, void* y,

@@ -134,6 +134,12 @@ __device__ __forceinline__ float amax3(float m, float a, float b) {
 
 // SwiGLU's gradient, two values at a time: from g, u and what arrives at act (da) that of the gate half and of the up
 // half, and act itself (not gated).
+//
+// The exponential is exp2 of the rounded -g log2(e), and the reciprocal the approximate one. The full exponential is closer
+// where the sigmoid is small: act, in units of 2^-23, is off by 2.6 at most for |g| < 4 (0.63 in the root mean square) and by
+// 15 for g in -40 .. -10, there with 1.8 (0.54) and 2.0. In sums over a row and behind e4m3's or bf16's rounding that does
+// not show (12,288 x 1408: dgate is off by 1.20e-7 of its norm, in plain 32-bit operations by 1.19e-7), but
+// 12,288 x 1408 take 89.5 us with all 8-bit forms instead of 81.7, and 43.0 instead of 41.0 with bf16 rows.
 struct Grad2 { uint64_t dg, du, a; };
 __device__ __forceinline__ Grad2 swiglu_grad2(uint64_t g, uint64_t u, uint64_t da) {
   float x, y;
