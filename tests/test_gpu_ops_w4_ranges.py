@@ -96,6 +96,23 @@ def test_finite_weights_read_finite(ops, group, zero):
     assert bool(((back - w.double()).abs() <= step * (0.5 + 15 * 2.0 ** -9 + (0.5 if zero else 0.0))).all())
 
 
+# -------------------------------------------------------------- long products
+
+@pytest.mark.parametrize("M,N,K,group,zero", [
+    (1, 20008, 7200, 128, False), (4, 12008, 7200, 32, True), (8, 12008, 7200, 64, False), (8, 20008, 7200, 128, True),
+    (1, 194568, 96, 32, True), (3, 194568, 96, 64, False), (8, 194568, 288, 32, False), (2, 97288, 1312, 128, False),
+    (21, 40008, 544, 64, True)])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+def test_products_of_many_units(ops, M, N, K, group, zero, out):
+    """Several units a CTA and several chunks a warp; the last block of rows ends within it; K ends within a chunk."""
+    g = gen(N + K)
+    w, x = weights(g, 1, N, K, group, zero), rnd(g, M, K)
+    c = ops.w4_matmul(x, first(w), out_dtype=out)
+    v = dense(w, 0)
+    near(c, x.double() @ v.t(), x.double().abs() @ v.abs().t(), -(-K // group))
+    assert ops.status() == 0
+
+
 @pytest.mark.parametrize("N,K,group,zero", [(4008, 2080, 32, True), (12008, 1056, 128, False), (4008, 7200, 64, False),
                                             (40008, 96, 32, False)])
 def test_segments_that_grow_and_shrink(ops, N, K, group, zero):
@@ -146,6 +163,18 @@ def layer(ops, T, d, f, E, k, shared, group, zero, out, idx=None, seed=0):
     tol = bound + HALF[out] * (want.abs() + bound)
     assert bool((err <= tol).all()), (err - tol).max().item()
     return (y.double() - want).norm() / want.norm()
+
+
+@pytest.mark.parametrize("T,d,f,E,k,shared,group,zero", [
+    (1, 7200, 96, 6, 3, 1, 128, False), (1, 14368, 544, 4, 2, 0, 32, True), (3, 7200, 288, 9, 4, 0, 64, True),
+    (16, 7200, 160, 12, 6, 1, 32, False), (16, 14368, 96, 8, 3, 0, 128, True), (64, 14368, 96, 12, 4, 1, 64, False),
+    (64, 7200, 544, 5, 2, 0, 128, True), (16, 2080, 2080, 12, 4, 1, 32, True), (40, 1056, 2080, 12, 8, 0, 128, False),
+    (2, 2080, 4128, 6, 4, 1, 64, False)])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+def test_layers_of_many_units(ops, T, d, f, E, k, shared, group, zero, out):
+    """Several units a CTA of either kernel: rings that wrap, pointers that step from rows to rows, sums taken over."""
+    layer(ops, T, d, f, E, k, shared, group, zero, out)
+    assert ops.status() == 0
 
 
 @pytest.mark.parametrize("rows", [2, 3, 8, 16, 17, 64])
