@@ -235,20 +235,20 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) w4_down_kernel(W4LayerParams
   if (tid == 0) hand.init(warps);
   // idx was written before the kernel in front of this one began; only h is that kernel's
   build_lists(L, (LayerGates<TMAX>*)nullptr, P, kPairs);
-  float(*sums)[kPitch] = reinterpret_cast<float(*)[kPitch]>(smem + warps * Core::kBytes);   // [kBufs][warp][token][kCols]
+  float* sums = reinterpret_cast<float*>(smem + warps * Core::kBytes);     // [kBufs][warp][token][kPitch]
   const int units = (P.d + kCols - 1) / kCols, C = (P.f + kChunk - 1) / kChunk, items = uniform(L.tile[P.slots]) * C;
   if (warp == warps) {
     griddep_wait();
     griddep_launch();
     for (int u = blockIdx.x, i = 0; u < units; u += gridDim.x, ++i) {
       hand.wait_full(i, P.status);
-      const float(*from)[kPitch] = sums + (i % kBufs) * warps * P.T;
+      const float* from = sums + (i % kBufs) * warps * P.T * kPitch;
       for (int q = lane; q < P.T * (kCols / 4); q += 32) {
         const int r = q / (kCols / 4), j = q % (kCols / 4) * 4, col = u * kCols + j;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
         for (int w = 0; w < warps; ++w) {
-          const float4 a = *reinterpret_cast<const float4*>(&from[w * P.T + r][j]);
+          const float4 a = *reinterpret_cast<const float4*>(from + (w * P.T + r) * kPitch + j);
           v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
         }
         if (col < P.d) {       // (d is a multiple of 32)
@@ -305,9 +305,9 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) w4_down_kernel(W4LayerParams
   griddep_launch();
   read_h();
   for (int u = blockIdx.x, i = 0; u < units; u += gridDim.x, ++i) {
-    float(*mine)[kPitch] = sums + ((i % kBufs) * warps + warp) * P.T;
+    float* mine = sums + ((i % kBufs) * warps + warp) * P.T * kPitch;
     hand.wait_empty(i, P.status);
-    for (int j = lane; j < P.T * kPitch; j += 32) mine[0][j] = 0.f;
+    for (int j = lane; j < P.T * kPitch; j += 32) mine[j] = 0.f;
     float acc[MT][4] = {};
     int tile = tile0, c = c0, pair0 = 0, R = 0;
     if (n) find_tile(L, tile, kPairs, pair0, R);
@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) w4_down_kernel(W4LayerParams
           }
           const int r = PARTS == 3 ? t >> 1 : t;
           if (r < R && (PARTS == 2 || !(t & 1))) {
-            float* dst = mine[L.token[pair0 + r]] + mt * 16 + quad;
+            float* dst = mine + L.token[pair0 + r] * kPitch + mt * 16 + quad;
             dst[0] += lo;
             dst[8] += hi;
           }
