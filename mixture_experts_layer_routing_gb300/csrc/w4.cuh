@@ -364,7 +364,10 @@ constexpr int kSumBuffers = 2;       // of a warp
 // `fixed` bytes of the CTA's own. (Two CTAs of 8 warps each took 34.7 us for 32,768 x 7168 and one row, one of 16 takes
 // 30.3: half as many ranges of units, so the longest is nearer to the average.)
 constexpr size_t w4_smem(size_t fixed) { return 227 * 1024 - 1024 - fixed; }
-inline int w4_warps(size_t fixed, size_t per_warp) { return (int)min(w4_smem(fixed) / per_warp, (size_t)kW4Warps - 1); }
+constexpr int w4_warps(size_t fixed, size_t per_warp) {
+  const size_t n = w4_smem(fixed) / per_warp;
+  return n < kW4Warps - 1 ? (int)n : kW4Warps - 1;
+}
 
 // Sums of N units between the warps of a product and the warp that joins them, so that no product waits for another
 // warp's or for the join.

@@ -7,7 +7,7 @@ namespace moe {
 namespace {
 
 constexpr int kMaxSlots = 264;               // experts, shared ones included
-constexpr int kSlotsEach = 3;                // of a thread that counts: CTAs have at least 4 warps
+constexpr int kSlotsEach = 3;                // of a thread that counts, in CTAs of at least 4 warps
 
 // The experts in use and their tokens, made by every CTA of both kernels from idx alone. Pairs (token, expert) are
 // sorted by expert, then token; an expert that a token names twice is one pair with both gates. A tile is up to `rows`
@@ -355,18 +355,19 @@ cudaError_t launch_up(const moe_ops_s* o, const W4LayerParams& P, cudaStream_t s
   constexpr size_t per = Core::kBytes + kSumBuffers * XR * Core::kPitch * sizeof(float);
   const long long units = (long long)P.T * (P.k + P.slots - P.E) * (P.f / (MT * 8));
   constexpr size_t fixed = sizeof(LayerLists<TMAX>) + sizeof(LayerGates<TMAX>) + 128;
-  const int warps = w4_warps(fixed, per);
-  const size_t smem = warps * per;
+  constexpr int warps = w4_warps(fixed, per);
+  static_assert((warps + 1) * 32 * kSlotsEach > kMaxSlots, "a place for every slot");
   MOE_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)w4_smem(fixed)));
-  return launch_pdl(kern, dim3((unsigned)min(units, (long long)o->sms)), dim3((warps + 1) * 32), smem, s, P);
+  return launch_pdl(kern, dim3((unsigned)min(units, (long long)o->sms)), dim3((warps + 1) * 32), warps * per, s, P);
 }
 template <int MT, int XR, int PARTS, int TMAX, int GROUP, bool ZERO>
 cudaError_t launch_down(const moe_ops_s* o, const W4LayerParams& P, cudaStream_t s) {
   using Core = W4Core<MT, XR, GROUP, ZERO>;
   auto* kern = w4_down_kernel<MT, XR, PARTS, TMAX, GROUP, ZERO>;
-  const size_t per = Core::kBytes + down_buffers(TMAX) * P.T * Core::kPitch * sizeof(float);
+  constexpr size_t token = down_buffers(TMAX) * Core::kPitch * sizeof(float), fixed = sizeof(LayerLists<TMAX>) + 128;
+  static_assert((w4_warps(fixed, Core::kBytes + TMAX * token) + 1) * 32 * kSlotsEach > kMaxSlots, "a place for every slot");
+  const size_t per = Core::kBytes + P.T * token;
   const int units = ceil_div(P.d, MT * 16);
-  constexpr size_t fixed = sizeof(LayerLists<TMAX>) + 128;
   const int warps = w4_warps(fixed, per);
   const size_t smem = warps * per;
   // (a constant: host threads with other numbers of tokens may be between this and their launch)

@@ -15,7 +15,6 @@ struct W4MatmulParams {
   W4Shape s;
   const int* off;
   int G, out_fp32;
-  int warps;              // that multiply (the CTA has one more, and 8 at least)
   void* c;
   int* status;
 };
@@ -29,7 +28,7 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) w4_matmul_kernel(W4MatmulPar
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ SegSmem seg;
   __shared__ W4Handover<kSumBuffers> hand;
-  const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5), warps = P.warps;
+  const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5), warps = (blockDim.x >> 5) - 1;
   if (tid == 0) hand.init(warps);
   griddep_wait();
   griddep_launch();
@@ -45,7 +44,6 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) w4_matmul_kernel(W4MatmulPar
     r0 = uniform(seg.off[g] + (tl - seg.tile[g]) * XR);
     R = uniform(min(XR, seg.off[g + 1] - r0));
   };
-  if (warp > warps) return;
   if (warp == warps) {
     for (int u = u0; u < u1; ++u) {
       if (tile != at) rows(tile);
@@ -190,16 +188,16 @@ __global__ void __launch_bounds__(256) quant_w4_kernel(const bf16* __restrict__ 
 }
 
 template <int MT, int XR, int GROUP, bool ZERO>
-cudaError_t launch_matmul(const moe_ops_s* o, W4MatmulParams P, cudaStream_t s) {
+cudaError_t launch_matmul(const moe_ops_s* o, const W4MatmulParams& P, cudaStream_t s) {
   using Core = W4Core<MT, XR, GROUP, ZERO>;
   auto* kern = w4_matmul_kernel<MT, XR, GROUP, ZERO>;
   constexpr size_t per = Core::kBytes + kSumBuffers * XR * Core::kPitch * sizeof(float);
   const long long units = (long long)(ceil_div(P.M, XR) + (P.off ? min(P.G, P.M) : 0)) * ceil_div(P.s.N, MT * 16);
   constexpr size_t fixed = sizeof(SegSmem) + 128;
-  P.warps = w4_warps(fixed, per);
-  const size_t smem = P.warps * per;
+  constexpr int warps = w4_warps(fixed, per);
+  static_assert((warps + 1) * 32 >= 256, "load_segments takes 256 threads");
   MOE_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)w4_smem(fixed)));
-  return launch_pdl(kern, dim3((unsigned)min(units, (long long)o->sms)), dim3(max(P.warps + 1, 8) * 32), smem, s, P);
+  return launch_pdl(kern, dim3((unsigned)min(units, (long long)o->sms)), dim3((warps + 1) * 32), warps * per, s, P);
 }
 template <int MT, int XR> cudaError_t pick_matmul(const moe_ops_s* o, const W4MatmulParams& P, int group, cudaStream_t s) {
   const bool z = P.w.zero != nullptr;
@@ -214,7 +212,7 @@ cudaError_t w4_matmul(const moe_ops_s* o, const void* x, long long ld, int x_row
                       const moe_w4& w, const int* off, int G, int N, int K, void* c, int out_fp32, cudaStream_t s,
                       long long* n) {
   const W4MatmulParams P = {(const bf16*)x, (unsigned)(ld / 8), x_rows, M, row_index,
-                            {w.codes, (const bf16*)w.scale, w.zero}, {N, K, ceil_div(K, w.group)}, off, G, out_fp32, 0, c, o->status};
+                            {w.codes, (const bf16*)w.scale, w.zero}, {N, K, ceil_div(K, w.group)}, off, G, out_fp32, c, o->status};
   *n += 1;
   if (M <= 2) return pick_matmul<2, 2>(o, P, w.group, s);
   return M <= 4 ? pick_matmul<2, 4>(o, P, w.group, s) : pick_matmul<2, 8>(o, P, w.group, s);
