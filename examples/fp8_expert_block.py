@@ -87,7 +87,7 @@ class Fp8ExpertBlock:
     def backward(self, dout, ctx, dh=None):
         """Gradients of x (and residual), and of every weight, for dL/dout (and dL/dh from elsewhere)."""
         ops, c, k, off = self.ops, ctx, self.k, ctx["off"]
-        if self.save8:
+        if "save" in c:                                          # kept by a forward pass with save8
             drows, dWd, dW13, dgate = self._backward8(dout, c)
             y = (c["h"].float() * c["rstd"][:, None] * self.norm_w.float()).bfloat16()
             return self._backward_router(c, y, drows, dWd, dW13, dgate, dh)

@@ -170,3 +170,20 @@ def test_tensors_that_do_not_fit_are_refused():
             call()
             raise AssertionError(i)
     assert ops.launch_count() == before and ops.status() == 0
+
+
+def test_backward_follows_the_forward_pass(example):
+    """What a forward pass kept decides how its backward pass goes, whatever the block was switched to in between."""
+    block = example.Fp8ExpertBlock(256, 128, 8, 2, seed=8, save8=True)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x, res, dout = (torch.randn(70, 256, generator=g, device="cuda").bfloat16() for _ in range(3))
+    ctx8 = block.forward(x, res)[2]
+    want8 = block.backward(dout, ctx8)
+    block.save8 = False
+    ctx = block.forward(x, res)[2]
+    want = block.backward(dout, ctx)
+    got8 = block.backward(dout, ctx8)
+    block.save8 = True
+    got = block.backward(dout, ctx)
+    for n in want:
+        assert torch.equal(got[n], want[n]) and torch.equal(got8[n], want8[n]), n
