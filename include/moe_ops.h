@@ -166,7 +166,7 @@ moe_status moe_swiglu_forward(moe_ops ops, const void* gu, long long ld, int T, 
  * along the tokens, and with them actt [f, Tp], actt_scale [Tp/128, f], those of act', segments and padding as in
  * moe_quant_cols; dgate [T]. off (nullable, G+1 ascending within 0 .. T) tells the segments; rows of no segment are not
  * written. save is 8-byte aligned, dgu, dq, dqt and actt 16-byte. workspace: moe_swiglu_workspace_size bytes, 16-byte
- * aligned, for dgate where that is above 0. */
+ * aligned, for dgate where that is above 0; calls that may run at once need one each. */
 moe_status moe_swiglu_workspace_size(int T, int f, size_t* bytes);
 moe_status moe_swiglu_backward(moe_ops ops, const void* save, const float* save_scale, const void* dact, long long ld,
                                const float* gate, int T, int f, const int32_t* off, int G, void* dgu, void* dq,

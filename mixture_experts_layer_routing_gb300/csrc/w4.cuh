@@ -1,4 +1,4 @@
-// Few rows times 4-bit weights: what the kernels of w4.cu share.
+// Few rows times 4-bit weights: what the kernels of w4_matmul.cu and w4_layer.cu share.
 //
 // A warp takes 256 values of K (a chunk) of MT x 16 weight rows at a time and multiplies them with up to 8 rows of x on
 // the legacy MMA (m16n8k16, weights as its 16 rows, x's rows as its columns): at so few rows tensor throughput is no
@@ -9,9 +9,11 @@
 // What bounds it. The floor is the weights' bytes. Copies alone reach 83% of the copy rate (three stages of 4 KB for each
 // of 14 or 15 warps; with x in the same ring and two stages it was 55%). The products alone take longer: decoding 32 x 256
 // codes is 224 shifts and LOP3s on a pipe that issues one in two cycles and 128 subtractions, of some 640 instructions in
-// all, at 16 warps of 128 registers on an SM. 32,768 x 7168 by one row in 28.9 us (17.8 at the copy rate), by eight in
-// 37.3. Shifts as multiplications on the other pipe (mul.hi) were slower, and so were 24 warps of 80 registers, bulk
-// prefetches of the next units to L2, and two barriers a unit instead of a warp that joins.
+// all, at 16 warps of 128 registers on an SM. 32,768 x 7168 by one row in 29.0 us (17.8 at the copy rate), by eight in
+// 37.7: 17% more instructions (x goes through shared memory for each 32 weight rows), and as x and the sums take room 12
+// warps multiply instead of 15, each of which waits nearly four times as long for shared memory. Shifts as multiplications
+// on the other pipe (mul.hi) were slower, and so were 24 warps of 80 registers, bulk prefetches of the next units to L2,
+// and two barriers a unit instead of a warp that joins.
 //
 // Decoding. A word holds eight values, the even ones in its low half, so (word >> 4i) & 0x000f000f is a pair of
 // neighbours; in the last bits of a bf16 mantissa under the exponent of 128 a code c reads 128 + c, and one packed
@@ -361,8 +363,8 @@ struct W4Cursor {
 constexpr int kSumBuffers = 2;       // of a warp
 
 // One CTA on an SM: the warps that multiply and, one more, the warp that joins; as many as its shared memory holds with
-// `fixed` bytes of the CTA's own. (Two CTAs of 8 warps each took 34.7 us for 32,768 x 7168 and one row, one of 16 takes
-// 30.3: half as many ranges of units, so the longest is nearer to the average.)
+// `fixed` bytes of the CTA's own. (Two CTAs of 8 warps each took 34.7 us for 32,768 x 7168 and one row where one of 16 took
+// 30.3, before the other steps: half as many ranges of units, so the longest is nearer to the average.)
 constexpr size_t w4_smem(size_t fixed) { return 227 * 1024 - 1024 - fixed; }
 constexpr int w4_warps(size_t fixed, size_t per_warp) {
   const size_t n = w4_smem(fixed) / per_warp;

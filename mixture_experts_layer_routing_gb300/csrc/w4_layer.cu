@@ -11,7 +11,7 @@ constexpr int kSlotsEach = 3;                // of a thread that counts, in CTAs
 
 // The experts in use and their tokens, made by every CTA of both kernels from idx alone. Pairs (token, expert) are
 // sorted by expert, then token; an expert that a token names twice is one pair with both gates. A tile is up to `rows`
-// pairs of a slot. TMAX is 16 or 64 (shared memory is what two CTAs on an SM run short of).
+// pairs of a slot. TMAX is 16 or 64: lists for 64 tokens take 6 KB of shared memory more.
 template <int TMAX> struct LayerLists {
   static constexpr int kPairs = TMAX * 16, kWords = (TMAX + 31) / 32;
   unsigned mask[kMaxSlots][kWords];          // tokens of a slot
